@@ -71,7 +71,8 @@ typedef enum {
   QMOE_ST_RANGE = 4    /* a value outside a format's or accumulator's range       -> QMOE_ERR_DEVICE_CHECK */
 } qmoe_status_bit;
 
-typedef enum { QMOE_F16 = 0, QMOE_BF16 = 1 } qmoe_dtype;
+/* QMOE_F32 is taken by the microscaled entry points that say so, no others. */
+typedef enum { QMOE_F16 = 0, QMOE_BF16 = 1, QMOE_F32 = 2 } qmoe_dtype;
 
 /* Path selection for qmoe_forward_ex.
  *   DECODE        per-token GEMV on CUDA cores, fp32 throughout (small T).
@@ -384,6 +385,77 @@ int qmoe_gptq_zero_offset(const int32_t* qzeros, size_t n_words, int32_t* offset
  * already stores one byte per block; this is the packing ONNX MatMulNBits
  * uses for 4-bit zero points.  rows = E * N for a stacked projection. */
 int qmoe_unpack_zero_points(const uint8_t* zp_packed, int rows, int nb, uint8_t* zp_out, void* stream);
+
+/* ---- Microscaled (MX) formats: OCP Microscaling v1.0 blocks of 32 elements.
+ *
+ * An MX tensor [R, K] (K a multiple of 32) is two device buffers:
+ *   codes   MXFP8: uint8 [R, K], one e4m3 code per element;
+ *           MXFP4: uint8 [R, K/2], two e2m1 codes per byte, element k of a
+ *           row in byte k/2, LOW nibble for even k;
+ *   scales  one e8m0 byte s per block of 32 elements along K: the block's
+ *           scale is X = 2^(s - 127), 255 is NaN.  They lie in tiles of 128
+ *           rows x 4 blocks, 512 bytes each, tiles row-major over
+ *           [ceil(R/128), ceil(K/128)]; row r, block b is at byte
+ *             (r/128 * ceil(K/128) + b/4) * 512 + r%32 * 16 + r%128/32 * 4 + b%4.
+ *           Tensor memory holds a product's scales in this order, so the
+ *           tiles are copied there as they are.  Bytes for rows >= R and
+ *           blocks >= K/32 are padding: the calls below write zeros there.
+ *           qmoe_mx_scale_bytes(R, K) gives the size.
+ * An element's value is code * X.  Every codes and scales pointer is 16-byte
+ * aligned; codes, scales, inputs and outputs of one call must not overlap
+ * (qmoe_rmsnorm_mx's residual_out is the exception). */
+typedef enum { QMOE_MXFP8 = 0, QMOE_MXFP4 = 1 } qmoe_mx_format;
+
+/* Bytes of the scale tiles of an MX tensor [R, K]; 0 for R < 1, K < 32 or K
+ * not a multiple of 32.  Host only. */
+size_t qmoe_mx_scale_bytes(int R, int K);
+
+/* Quantise x [M, K] (fp16, bf16 or fp32; finite or not) to an MX tensor:
+ *   s    = clamp(floor(log2(max |v| of the block)) - emax, -127, 127) + 127,
+ *          emax = 8 (e4m3, largest 448) or 2 (e2m1, largest 6); an all-zero
+ *          block has s = 0;
+ *   code = v / X rounded to nearest even, saturating at the largest value.
+ * A block that holds a NaN or an infinity gets s = 255 and zero codes: all
+ * its elements read as NaN.  x is 16-byte aligned.  Bound by HBM. */
+int qmoe_mx_quantize(const void* x, int x_dtype, int format, int M, int K, uint8_t* codes, uint8_t* scales,
+                     void* stream);
+
+/* The values of an MX tensor: out [M, K] (fp16, bf16 or fp32) = code * X,
+ * exact in fp32 and rounded once to out_dtype.  out is 16-byte aligned. */
+int qmoe_mx_dequant(const uint8_t* codes, const uint8_t* scales, int format, int M, int K, void* out, int out_dtype,
+                    void* stream);
+
+/* RMSNorm of the layer stack with the residual's addition and microscaled
+ * output, for a product that takes it (qmoe_mx_matmul):
+ *   h = x + residual (fp32);  residual_out = h rounded to act_dtype;
+ *   y = h / sqrt(mean_h(h^2) + eps) * weight (fp32, from the unrounded h);
+ *   codes, scales = y [T, H] quantised as by qmoe_mx_quantize.
+ * x, residual, residual_out [T, H] and weight [H] are fp16 or bf16
+ * (act_dtype).  residual may be NULL (h = x), weight may be NULL (unit
+ * weight), residual_out may be NULL (not wanted) and may be x or residual
+ * itself.  Requires H a multiple of 32; pointers 16-byte aligned.  A row with
+ * a NaN or an infinity reads as NaN in every block. */
+int qmoe_rmsnorm_mx(const void* x, const void* residual, const void* weight, int act_dtype, int T, int H, float eps,
+                    int format, void* residual_out, uint8_t* codes, uint8_t* scales, void* stream);
+
+/* Product with MXFP4 weights: y[M, N] = x . W^T, x an MX tensor [M, K] of
+ * x_format (MXFP8 or MXFP4), W an MXFP4 tensor [N, K]; products are exact,
+ * sums are fp32, and y is rounded once to y_dtype (fp16, bf16 or fp32;
+ * y aligned to its element size).  Any M and N >= 1.  A NaN scale makes the
+ * outputs of its row NaN.  status_dev (a 4-byte device word that the caller
+ * set to 0, or NULL): a bounded wait of the kernel that ran out sets
+ * QMOE_ST_TIMEOUT there (y is then undefined); read it with
+ * qmoe_get_device_status(status_dev, ...). */
+int qmoe_mx_matmul(const uint8_t* x_codes, const uint8_t* x_scales, int x_format, const uint8_t* w_codes,
+                   const uint8_t* w_scales, int M, int N, int K, void* y, int y_dtype, uint32_t* status_dev,
+                   void* stream);
+
+/* Scale-layout adapters (one-time conversion at model load): row-major
+ * scales [R, K/32], as checkpoints store them, into the tiles above, and
+ * back.  in and out are separate buffers of any alignment on the row-major
+ * side. */
+int qmoe_mx_tile_scales(const uint8_t* scales_rowmajor, int R, int K, uint8_t* scales, void* stream);
+int qmoe_mx_untile_scales(const uint8_t* scales, int R, int K, uint8_t* scales_rowmajor, void* stream);
 
 /* Read (blocking: synchronises `stream`) and clear the device status word
  * of `workspace` (its first 4 bytes; also any 4-byte status word such as

@@ -18,6 +18,8 @@ PATH_AUTO, PATH_DECODE, PATH_PREFILL, PATH_DECODE_SPLIT, PATH_DECODE_FUSED = 0, 
 DECODE_MAX_TOKENS = 16
 AUTO_DECODE_MAX_TOKENS = 5
 DIAG_STALL_GEMM = 1
+F32 = 2                      # the microscaled entry points that say so
+MXFP8, MXFP4 = 0, 1
 _STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported device or shape",
            3: "workspace missing or too small", 4: "CUDA runtime error",
            5: "device wait timed out", 6: "device index check failed"}
@@ -90,6 +92,19 @@ def lib():
         L.qmoe_gptq_zero_offset.argtypes = [vp, sz, vp, vp]
         L.qmoe_unpack_zero_points.restype = i32
         L.qmoe_unpack_zero_points.argtypes = [vp, i32, i32, vp, vp]
+        L.qmoe_mx_scale_bytes.restype = sz
+        L.qmoe_mx_scale_bytes.argtypes = [i32, i32]
+        L.qmoe_mx_quantize.restype = i32
+        L.qmoe_mx_quantize.argtypes = [vp, i32, i32, i32, i32, vp, vp, vp]
+        L.qmoe_mx_dequant.restype = i32
+        L.qmoe_mx_dequant.argtypes = [vp, vp, i32, i32, i32, vp, i32, vp]
+        L.qmoe_rmsnorm_mx.restype = i32
+        L.qmoe_rmsnorm_mx.argtypes = [vp, vp, vp, i32, i32, i32, ctypes.c_float, i32, vp, vp, vp, vp]
+        L.qmoe_mx_matmul.restype = i32
+        L.qmoe_mx_matmul.argtypes = [vp, vp, i32, vp, vp, i32, i32, i32, vp, i32, vp, vp]
+        for f in (L.qmoe_mx_tile_scales, L.qmoe_mx_untile_scales):
+            f.restype = i32
+            f.argtypes = [vp, i32, i32, vp, vp]
         L.qmoe_get_device_status.restype = i32
         L.qmoe_get_device_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32), vp]
         _lib = L
@@ -339,4 +354,159 @@ def qmoe_unpack_zero_points(zp_packed, nb):
     rows = zp_packed.shape[0]
     out = torch.empty((rows, nb), dtype=torch.uint8, device=zp_packed.device)
     _check(lib().qmoe_unpack_zero_points(_p(zp_packed), rows, nb, _p(out), _stream()), "qmoe_unpack_zero_points")
+    return out
+
+
+# ---- microscaled (MX) formats.  An MX tensor [R, K] is (codes, scales): codes
+# uint8 [R, K] (MXFP8) or [R, K/2] (MXFP4), scales a flat uint8 tensor of
+# qmoe_mx_scale_bytes(R, K) bytes in the tile order that qmoe.h defines.
+# These calls check what they are given (CUDA, contiguous, one device, types
+# and sizes) and run on the tensors' device, on torch's current stream there.
+
+_MX_DT = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
+
+
+def _bad(where, what):
+    raise QMoEError(1, "%s: %s" % (where, what))
+
+
+def _mx_rows(t, where, dtypes):
+    """Shape of a contiguous 2-D CUDA tensor of one of the dtypes."""
+    if t.dtype not in dtypes or not t.is_cuda or t.dim() != 2 or not t.is_contiguous():
+        _bad(where, "wants a contiguous 2-D CUDA tensor of %s" % " / ".join(str(d) for d in dtypes))
+    return t.shape
+
+
+def _mx_same(t, like, dtype, numel, where, name):
+    """A contiguous tensor of a given type and size on another one's device."""
+    if t.dtype != dtype or t.numel() != numel or t.device != like.device or not t.is_contiguous():
+        _bad(where, "%s: wants %d contiguous %s on %s" % (name, numel, dtype, like.device))
+    return t
+
+
+def _mx_tensor(codes, scales, fmt, where):
+    """(R, K) of an MX tensor."""
+    if fmt not in (MXFP8, MXFP4):
+        _bad(where, "unknown format %r" % (fmt,))
+    R, c = _mx_rows(codes, where, (torch.uint8,))
+    K = c if fmt == MXFP8 else 2 * c
+    _mx_same(scales, codes, torch.uint8, qmoe_mx_scale_bytes(R, K), where, "scales")
+    return R, K
+
+
+def _mx_out(R, K, fmt, like, codes, scales, where):
+    """(codes, scales) to write an MX tensor [R, K] to: the caller's, or new ones."""
+    if fmt not in (MXFP8, MXFP4):
+        _bad(where, "unknown format %r" % (fmt,))
+    n = qmoe_mx_scale_bytes(R, K)
+    if n == 0:
+        _bad(where, "rows >= 1 and a multiple of 32 columns are wanted, got [%d, %d]" % (R, K))
+    cols = K if fmt == MXFP8 else K // 2
+    if codes is None:
+        codes = torch.empty((R, cols), dtype=torch.uint8, device=like.device)
+    else:
+        _mx_same(codes, like, torch.uint8, R * cols, where, "codes")
+    if scales is None:
+        scales = torch.empty(n, dtype=torch.uint8, device=like.device)
+    else:
+        _mx_same(scales, like, torch.uint8, n, where, "scales")
+    return codes, scales
+
+
+def _mx_call(t, fn, where, *args):
+    """fn(*args, stream) on t's device and its current stream."""
+    if t.device.index == torch.cuda.current_device():
+        _check(fn(*args, _stream()), where)
+    else:
+        with torch.cuda.device(t.device):
+            _check(fn(*args, _stream()), where)
+
+
+def qmoe_mx_scale_bytes(R, K):
+    """Bytes of the scale tiles of an MX tensor [R, K] (0 if it cannot be one)."""
+    return int(lib().qmoe_mx_scale_bytes(R, K))
+
+
+def qmoe_mx_quantize(x, fmt=MXFP8, codes=None, scales=None):
+    """(codes, scales) of x [M, K] (fp16, bf16 or fp32) in MXFP8 or MXFP4."""
+    M, K = _mx_rows(x, "qmoe_mx_quantize", tuple(_MX_DT))
+    codes, scales = _mx_out(M, K, fmt, x, codes, scales, "qmoe_mx_quantize")
+    _mx_call(x, lib().qmoe_mx_quantize, "qmoe_mx_quantize", _p(x), _MX_DT[x.dtype], fmt, M, K, _p(codes), _p(scales))
+    return codes, scales
+
+
+def qmoe_mx_dequant(codes, scales, fmt, dtype=torch.bfloat16, out=None):
+    """[M, K] values (fp16, bf16 or fp32) of an MX tensor."""
+    M, K = _mx_tensor(codes, scales, fmt, "qmoe_mx_dequant")
+    if dtype not in _MX_DT:
+        _bad("qmoe_mx_dequant", "unsupported output type %s" % dtype)
+    if out is None:
+        out = torch.empty((M, K), dtype=dtype, device=codes.device)
+    else:
+        _mx_same(out, codes, dtype, M * K, "qmoe_mx_dequant", "out")
+    _mx_call(codes, lib().qmoe_mx_dequant, "qmoe_mx_dequant", _p(codes), _p(scales), fmt, M, K, _p(out), _MX_DT[dtype])
+    return out
+
+
+def qmoe_rmsnorm_mx(x, residual=None, weight=None, eps=1e-6, fmt=MXFP8, residual_out=None, codes=None, scales=None):
+    """(codes, scales, residual_out) of RMSNorm(x + residual) * weight in MXFP8
+    or MXFP4; residual_out = x + residual (a new tensor unless given; it may be
+    x or residual itself).  Without a residual it is None unless given."""
+    where = "qmoe_rmsnorm_mx"
+    T, H = _mx_rows(x, where, (torch.float16, torch.bfloat16))
+    if residual is not None:
+        _mx_same(residual, x, x.dtype, T * H, where, "residual")
+        if residual_out is None:
+            residual_out = torch.empty_like(x)
+    if residual_out is not None:
+        _mx_same(residual_out, x, x.dtype, T * H, where, "residual_out")
+    if weight is not None:
+        _mx_same(weight, x, x.dtype, H, where, "weight")
+    codes, scales = _mx_out(T, H, fmt, x, codes, scales, where)
+    _mx_call(x, lib().qmoe_rmsnorm_mx, where, _p(x), _p(residual), _p(weight), _MX_DT[x.dtype], T, H, float(eps), fmt,
+             _p(residual_out), _p(codes), _p(scales))
+    return codes, scales, residual_out
+
+
+def qmoe_mx_matmul(x_codes, x_scales, x_fmt, w_codes, w_scales, dtype=torch.bfloat16, out=None, status=None):
+    """y [M, N] (fp16, bf16 or fp32) = x . W^T for an MX tensor x [M, K] and MXFP4
+    weights W [N, K].  status: an int32 [1] device tensor that collects
+    QMOE_ST_TIMEOUT (zero it first)."""
+    where = "qmoe_mx_matmul"
+    M, K = _mx_tensor(x_codes, x_scales, x_fmt, where)
+    N, KW = _mx_tensor(w_codes, w_scales, MXFP4, where)
+    if K != KW or w_codes.device != x_codes.device:
+        _bad(where, "x has %d columns on %s, W has %d on %s" % (K, x_codes.device, KW, w_codes.device))
+    if dtype not in _MX_DT:
+        _bad(where, "unsupported output type %s" % dtype)
+    if out is None:
+        out = torch.empty((M, N), dtype=dtype, device=x_codes.device)
+    else:
+        _mx_same(out, x_codes, dtype, M * N, where, "out")
+    if status is not None:
+        _mx_same(status, x_codes, torch.int32, 1, where, "status")
+    _mx_call(x_codes, lib().qmoe_mx_matmul, where, _p(x_codes), _p(x_scales), x_fmt, _p(w_codes), _p(w_scales), M, N, K,
+             _p(out), _MX_DT[dtype], _p(status))
+    return out
+
+
+def qmoe_mx_tile_scales(scales_rowmajor):
+    """Row-major scale bytes [R, K/32] (as checkpoints store them) -> tiles."""
+    R, nb = _mx_rows(scales_rowmajor, "qmoe_mx_tile_scales", (torch.uint8,))
+    n = qmoe_mx_scale_bytes(R, 32 * nb)
+    if n == 0:
+        _bad("qmoe_mx_tile_scales", "empty scales")
+    out = torch.empty(n, dtype=torch.uint8, device=scales_rowmajor.device)
+    _mx_call(out, lib().qmoe_mx_tile_scales, "qmoe_mx_tile_scales", _p(scales_rowmajor), R, 32 * nb, _p(out))
+    return out
+
+
+def qmoe_mx_untile_scales(scales, R, K):
+    """Scale tiles of an MX tensor [R, K] -> row-major bytes [R, K/32]."""
+    n = qmoe_mx_scale_bytes(R, K)
+    if n == 0 or not scales.is_cuda:
+        _bad("qmoe_mx_untile_scales", "wants CUDA scale tiles of an MX tensor, got [%d, %d]" % (R, K))
+    _mx_same(scales, scales, torch.uint8, n, "qmoe_mx_untile_scales", "scales")
+    out = torch.empty((R, K // 32), dtype=torch.uint8, device=scales.device)
+    _mx_call(out, lib().qmoe_mx_untile_scales, "qmoe_mx_untile_scales", _p(scales), R, K, _p(out))
     return out

@@ -33,6 +33,7 @@ int check_device() {
 }
 
 bool valid_dtype(int d) { return d == QMOE_F16 || d == QMOE_BF16; }
+bool valid_dtype_or_f32(int d) { return valid_dtype(d) || d == QMOE_F32; }
 bool valid_bs(int bs) { return bs == 32 || bs == 64 || bs == 128; }
 
 int check_qweight(const qmoe_qweight& q, int N, int K, int bs) {
@@ -40,6 +41,13 @@ int check_qweight(const qmoe_qweight& q, int N, int K, int bs) {
   if (N < 1 || K < 32 || K % 32 || K % bs) return QMOE_ERR_INVALID_ARG;
   if (!aligned(q.w, 16) || !aligned(q.scales, 2)) return QMOE_ERR_INVALID_ARG;
   return QMOE_OK;
+}
+
+// codes and scales of an MX tensor [R, K]
+int check_mx(const uint8_t* codes, const uint8_t* scales, int format, int R, int K) {
+  if (!codes || !scales || !aligned(codes, 16) || !aligned(scales, 16)) return QMOE_ERR_INVALID_ARG;
+  if (format != QMOE_MXFP8 && format != QMOE_MXFP4) return QMOE_ERR_INVALID_ARG;
+  return R < 1 || K < 32 || K % 32 ? QMOE_ERR_INVALID_ARG : QMOE_OK;
 }
 
 thread_local cudaError_t g_last_cuda_error = cudaSuccess;
@@ -525,6 +533,65 @@ int qmoe_unpack_zero_points(const uint8_t* zp_packed, int rows, int nb, uint8_t*
   int rc = check_device();
   if (rc) return rc;
   return cuda_status(launch_unpack_zp(zp_packed, zp_out, rows, nb, (cudaStream_t)stream));
+}
+
+// ------------------------------------------------------- microscaled formats
+
+size_t qmoe_mx_scale_bytes(int R, int K) {
+  if (R < 1 || K < 32 || K % 32) return 0;
+  return ((size_t)R + 127) / 128 * (((size_t)K + 127) / 128) * 512;
+}
+
+int qmoe_mx_quantize(const void* x, int x_dtype, int format, int M, int K, uint8_t* codes, uint8_t* scales,
+                     void* stream) {
+  if (!valid_dtype_or_f32(x_dtype) || !x || !aligned(x, 16)) return QMOE_ERR_INVALID_ARG;
+  int rc = check_mx(codes, scales, format, M, K);
+  if (rc || (rc = check_device())) return rc;
+  return cuda_status(launch_mx_quantize(x, x_dtype, format, M, K, codes, scales, (cudaStream_t)stream));
+}
+
+int qmoe_mx_dequant(const uint8_t* codes, const uint8_t* scales, int format, int M, int K, void* out, int out_dtype,
+                    void* stream) {
+  if (!valid_dtype_or_f32(out_dtype) || !out || !aligned(out, 16)) return QMOE_ERR_INVALID_ARG;
+  int rc = check_mx(codes, scales, format, M, K);
+  if (rc || (rc = check_device())) return rc;
+  return cuda_status(launch_mx_dequant(codes, scales, format, M, K, out, out_dtype, (cudaStream_t)stream));
+}
+
+int qmoe_rmsnorm_mx(const void* x, const void* residual, const void* weight, int act_dtype, int T, int H, float eps,
+                    int format, void* residual_out, uint8_t* codes, uint8_t* scales, void* stream) {
+  if (!x || !valid_dtype(act_dtype) || !(eps >= 0.f)) return QMOE_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(residual_out, 16))
+    return QMOE_ERR_INVALID_ARG;
+  int rc = check_mx(codes, scales, format, T, H);
+  if (rc || (rc = check_device())) return rc;
+  return cuda_status(launch_mx_rmsnorm(x, residual, weight, act_dtype, T, H, eps, format, residual_out, codes, scales,
+                                       (cudaStream_t)stream));
+}
+
+int qmoe_mx_matmul(const uint8_t* x_codes, const uint8_t* x_scales, int x_format, const uint8_t* w_codes,
+                   const uint8_t* w_scales, int M, int N, int K, void* y, int y_dtype, uint32_t* status_dev,
+                   void* stream) {
+  if (!valid_dtype_or_f32(y_dtype) || !y || !aligned(y, y_dtype == QMOE_F32 ? 4 : 2) || !aligned(status_dev, 4))
+    return QMOE_ERR_INVALID_ARG;
+  int rc = check_mx(x_codes, x_scales, x_format, M, K);
+  if (rc || (rc = check_mx(w_codes, w_scales, QMOE_MXFP4, N, K)) || (rc = check_device())) return rc;
+  return cuda_status(launch_mx_matmul(x_codes, x_scales, x_format, w_codes, w_scales, M, N, K, y, y_dtype, status_dev,
+                                      (cudaStream_t)stream));
+}
+
+int qmoe_mx_tile_scales(const uint8_t* scales_rowmajor, int R, int K, uint8_t* scales, void* stream) {
+  if (!scales_rowmajor || !scales || !aligned(scales, 16) || !qmoe_mx_scale_bytes(R, K)) return QMOE_ERR_INVALID_ARG;
+  int rc = check_device();
+  if (rc) return rc;
+  return cuda_status(launch_mx_retile(scales_rowmajor, scales, R, K, true, (cudaStream_t)stream));
+}
+
+int qmoe_mx_untile_scales(const uint8_t* scales, int R, int K, uint8_t* scales_rowmajor, void* stream) {
+  if (!scales_rowmajor || !scales || !aligned(scales, 16) || !qmoe_mx_scale_bytes(R, K)) return QMOE_ERR_INVALID_ARG;
+  int rc = check_device();
+  if (rc) return rc;
+  return cuda_status(launch_mx_retile(scales, scales_rowmajor, R, K, false, (cudaStream_t)stream));
 }
 
 int qmoe_get_device_status(void* workspace, uint32_t* bits_out, void* stream) {

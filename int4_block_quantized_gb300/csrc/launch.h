@@ -75,6 +75,18 @@ cudaError_t launch_prefill_convert(const PrefillParams& p, void* out, int act_dt
 
 cudaError_t launch_dequant(const uint8_t* w, const void* s, int scale_dtype, const uint8_t* zp,
                            int N, int K, int bs, float* out, cudaStream_t st);
+// microscaled formats (mx.cu) and the product with MXFP4 weights (mx_matmul.cu)
+cudaError_t launch_mx_quantize(const void* x, int x_dtype, int format, int M, int K, uint8_t* codes, uint8_t* scales,
+                               cudaStream_t st);
+cudaError_t launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, int format, int M, int K, void* out,
+                              int out_dtype, cudaStream_t st);
+cudaError_t launch_mx_rmsnorm(const void* x, const void* residual, const void* weight, int act_dtype, int T, int H,
+                              float eps, int format, void* residual_out, uint8_t* codes, uint8_t* scales,
+                              cudaStream_t st);
+cudaError_t launch_mx_retile(const uint8_t* in, uint8_t* out, int R, int K, bool to_tiles, cudaStream_t st);
+cudaError_t launch_mx_matmul(const uint8_t* xc, const uint8_t* xs, int x_format, const uint8_t* wc, const uint8_t* ws,
+                             int M, int N, int K, void* y, int y_dtype, uint32_t* status, cudaStream_t st);
+
 cudaError_t launch_rmsnorm(const void* x, void* out, int act_dtype, int T, int H, float eps,
                            cudaStream_t st);
 

@@ -1,0 +1,202 @@
+// mx.cu -- microscaled formats: quantisation (fp16 / bf16 / fp32 to MXFP8 or
+// MXFP4), the reader, the layer stack's RMSNorm with the residual's addition
+// and microscaled output, and the scale-layout adapters.
+#include <math.h>
+
+#include "launch.h"
+#include "mx.cuh"
+
+namespace qmoe {
+
+// grid of a grid-stride kernel over `work` threads of 256
+static dim3 stride_grid(size_t work) {
+  const size_t cap = (size_t)device_sm_count() * 16;
+  const size_t b = (work + 255) / 256;
+  return dim3((unsigned)(b < 1 ? 1 : b > cap ? cap : b));
+}
+
+// --------------------------------------------------------------- quantise
+// s = floor(log2 max|v|) - emax, code = RN(v / 2^s): a thread takes half a
+// block (16 elements), so a block's maximum needs one shuffle.  Bound by HBM.
+template <typename T, int FMT>
+__global__ void __launch_bounds__(256) mx_quantize_kernel(const void* __restrict__ x, int M, int K,
+                                                          uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+  pdl_wait();
+  const size_t t0 = blockIdx.x * (size_t)256 + threadIdx.x, stride = (size_t)gridDim.x * 256;
+  const uint32_t per_row = (uint32_t)K / 16;
+  const size_t n = (size_t)M * per_row;
+  const int kt = (K + 127) / 128;
+  for (size_t i = t0; i < n; i += stride) {
+    float v[16];
+    load16<T>(x, i * 16, v);
+    const uint32_t s = mx_encode16<FMT>(v, codes, i * 16);
+    if (!(i & 1)) {
+      const int r = (int)(i / per_row);
+      scales[mx_scale_index(r, (int)(i - (size_t)r * per_row) >> 1, kt)] = (uint8_t)s;
+    }
+  }
+  mx_zero_padding(scales, M, K, t0, stride);
+}
+
+template <typename T>
+static cudaError_t launch_quantize_t(const void* x, int format, int M, int K, uint8_t* codes, uint8_t* scales,
+                                     cudaStream_t st) {
+  const dim3 g = stride_grid((size_t)M * (K / 16));
+  if (format == kMxfp8)
+    return launch_kernel(mx_quantize_kernel<T, kMxfp8>, g, dim3(256), 0, st, true, x, M, K, codes, scales);
+  return launch_kernel(mx_quantize_kernel<T, kMxfp4>, g, dim3(256), 0, st, true, x, M, K, codes, scales);
+}
+
+cudaError_t launch_mx_quantize(const void* x, int x_dtype, int format, int M, int K, uint8_t* codes, uint8_t* scales,
+                               cudaStream_t st) {
+  if (x_dtype == QMOE_F32) return launch_quantize_t<float>(x, format, M, K, codes, scales, st);
+  if (x_dtype == QMOE_BF16) return launch_quantize_t<__nv_bfloat16>(x, format, M, K, codes, scales, st);
+  return launch_quantize_t<__half>(x, format, M, K, codes, scales, st);
+}
+
+// ---------------------------------------------------------------- dequant
+// code * X in fp32 (exact), rounded once to T.  Bound by HBM.
+template <typename T, int FMT>
+__global__ void __launch_bounds__(256) mx_dequant_kernel(const uint8_t* __restrict__ codes,
+                                                         const uint8_t* __restrict__ scales, int M, int K,
+                                                         void* __restrict__ out) {
+  pdl_wait();
+  const size_t stride = (size_t)gridDim.x * 256;
+  const uint32_t per_row = (uint32_t)K / 16;
+  const size_t n = (size_t)M * per_row;
+  const int kt = (K + 127) / 128;
+  for (size_t i = blockIdx.x * (size_t)256 + threadIdx.x; i < n; i += stride) {
+    const int r = (int)(i / per_row);
+    const float X = mx_scale(scales[mx_scale_index(r, (int)(i - (size_t)r * per_row) >> 1, kt)]);
+    float v[16];
+    if constexpr (FMT == kMxfp8) {
+      const uint4 c = *reinterpret_cast<const uint4*>(codes + i * 16);
+      mx_from_e4m3x4(c.x, v);
+      mx_from_e4m3x4(c.y, v + 4);
+      mx_from_e4m3x4(c.z, v + 8);
+      mx_from_e4m3x4(c.w, v + 12);
+    } else {
+      const uint2 c = *reinterpret_cast<const uint2*>(codes + i * 8);
+      mx_from_e2m1x8(c.x, v);
+      mx_from_e2m1x8(c.y, v + 8);
+    }
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] *= X;
+    store16<T>(out, i * 16, v);
+  }
+}
+
+template <typename T>
+static cudaError_t launch_dequant_t(const uint8_t* codes, const uint8_t* scales, int format, int M, int K, void* out,
+                                    cudaStream_t st) {
+  const dim3 g = stride_grid((size_t)M * (K / 16));
+  if (format == kMxfp8)
+    return launch_kernel(mx_dequant_kernel<T, kMxfp8>, g, dim3(256), 0, st, true, codes, scales, M, K, out);
+  return launch_kernel(mx_dequant_kernel<T, kMxfp4>, g, dim3(256), 0, st, true, codes, scales, M, K, out);
+}
+
+cudaError_t launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, int format, int M, int K, void* out,
+                              int out_dtype, cudaStream_t st) {
+  if (out_dtype == QMOE_F32) return launch_dequant_t<float>(codes, scales, format, M, K, out, st);
+  if (out_dtype == QMOE_BF16) return launch_dequant_t<__nv_bfloat16>(codes, scales, format, M, K, out, st);
+  return launch_dequant_t<__half>(codes, scales, format, M, K, out, st);
+}
+
+// ---------------------------------------------------------------- RMSNorm
+// h = x + residual in fp32; residual_out = RN(h); y = h / sqrt(mean(h^2) +
+// eps) * weight from the unrounded h, quantised like above.  One CTA per
+// row.  x and residual are read again for the second pass (from L1 / L2), so
+// residual_out may be either of them: each element is read and written by
+// one thread, and nothing is written before the row's sum is complete.
+template <typename T, int FMT>
+__global__ void __launch_bounds__(256) mx_rmsnorm_kernel(const void* x, const void* residual, const void* weight,
+                                                         int M, int H, float eps, void* residual_out, uint8_t* codes,
+                                                         uint8_t* scales) {
+  pdl_wait();
+  const int units = H / 16, kt = (H + 127) / 128, t = blockIdx.x;
+  const size_t row = (size_t)t * H;
+  float ss = 0.f;
+  for (int u = threadIdx.x; u < units; u += 256) {
+    float v[16];
+    load16<T>(x, row + u * 16, v);
+    if (residual) {
+      float r[16];
+      load16<T>(residual, row + u * 16, r);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] += r[j];
+    }
+#pragma unroll
+    for (int j = 0; j < 16; ++j) ss = fmaf(v[j], v[j], ss);
+  }
+  ss = warp_sum(ss);
+  __shared__ float part[8];
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = ss;
+  __syncthreads();
+  float tot = 0.f;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) tot += part[w];
+  const float inv = 1.0f / sqrtf(tot / (float)H + eps);
+  for (int u = threadIdx.x; u < units; u += 256) {
+    float v[16];
+    load16<T>(x, row + u * 16, v);
+    if (residual) {
+      float r[16];
+      load16<T>(residual, row + u * 16, r);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] += r[j];
+    }
+    if (residual_out) store16<T>(residual_out, row + u * 16, v);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] *= inv;
+    if (weight) {
+      float w[16];
+      load16<T>(weight, u * 16, w);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] *= w[j];
+    }
+    const uint32_t s = mx_encode16<FMT>(v, codes, row + u * 16);
+    if (!(u & 1)) scales[mx_scale_index(t, u >> 1, kt)] = (uint8_t)s;
+  }
+  mx_zero_padding(scales, M, H, blockIdx.x * (size_t)256 + threadIdx.x, (size_t)gridDim.x * 256);
+}
+
+cudaError_t launch_mx_rmsnorm(const void* x, const void* residual, const void* weight, int act_dtype, int T, int H,
+                              float eps, int format, void* residual_out, uint8_t* codes, uint8_t* scales,
+                              cudaStream_t st) {
+#define QMOE_N(T_, F_)                                                                                          \
+  return launch_kernel(mx_rmsnorm_kernel<T_, F_>, dim3(T), dim3(256), 0, st, true, x, residual, weight, T, H, eps, \
+                       residual_out, codes, scales)
+  if (act_dtype == QMOE_BF16) {
+    if (format == kMxfp8) QMOE_N(__nv_bfloat16, kMxfp8);
+    QMOE_N(__nv_bfloat16, kMxfp4);
+  }
+  if (format == kMxfp8) QMOE_N(__half, kMxfp8);
+  QMOE_N(__half, kMxfp4);
+#undef QMOE_N
+}
+
+// --------------------------------------------------------- scale adapters
+// Row-major scales [R, K / 32] into tiles (padding zero), or back.
+template <bool TO_TILES>
+__global__ void __launch_bounds__(256) mx_retile_kernel(const uint8_t* __restrict__ in, uint8_t* __restrict__ out,
+                                                        int R, int K) {
+  pdl_wait();
+  const size_t t0 = blockIdx.x * (size_t)256 + threadIdx.x, stride = (size_t)gridDim.x * 256;
+  const int nb = K / 32, kt = (K + 127) / 128;
+  const size_t n = (size_t)R * nb;
+  for (size_t i = t0; i < n; i += stride) {
+    const int r = (int)(i / nb);
+    const size_t j = mx_scale_index(r, (int)(i - (size_t)r * nb), kt);
+    if (TO_TILES) out[j] = in[i];
+    else out[i] = in[j];
+  }
+  if (TO_TILES) mx_zero_padding(out, R, K, t0, stride);
+}
+
+cudaError_t launch_mx_retile(const uint8_t* in, uint8_t* out, int R, int K, bool to_tiles, cudaStream_t st) {
+  const dim3 g = stride_grid((size_t)R * (K / 32));
+  if (to_tiles) return launch_kernel(mx_retile_kernel<true>, g, dim3(256), 0, st, true, in, out, R, K);
+  return launch_kernel(mx_retile_kernel<false>, g, dim3(256), 0, st, true, in, out, R, K);
+}
+
+}  // namespace qmoe

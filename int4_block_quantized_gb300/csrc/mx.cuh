@@ -1,0 +1,162 @@
+// mx.cuh -- microscaled (MX) formats, shared by the quantisers, the reader
+// and the product: the scale-tile index, e8m0 scales, e4m3 / e2m1 codes.
+//
+// A block is 32 consecutive elements of a row with one scale X = 2^(s - 127),
+// s one byte (255: NaN).  A code is an e4m3 byte (MXFP8) or an e2m1 nibble
+// (MXFP4, even k in the low nibble); an element is code * X.
+#pragma once
+
+#include "common.cuh"
+
+namespace qmoe {
+
+constexpr int kMxfp8 = 0, kMxfp4 = 1;  // QMOE_MXFP8, QMOE_MXFP4
+
+// Scales are kept in tiles of 128 rows x 4 blocks, 512 bytes each: the order
+// in which a tensor-core product's scale operand lies in tensor memory (lane
+// r % 32, column r / 32, four blocks to a 32-bit word), so a tile goes there
+// as one contiguous copy.
+__host__ __device__ __forceinline__ size_t mx_scale_index(int r, int b, int kt) {
+  return ((size_t)(r >> 7) * kt + (b >> 2)) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (b & 3);
+}
+
+__device__ __forceinline__ float mx_scale(uint32_t s) {
+  // 2^-127 is subnormal in fp32
+  return __uint_as_float(s == 255u ? 0x7fffffffu : (s ? s << 23 : 0x00400000u));
+}
+
+// Scale byte of a block from the bits of its largest magnitude (the OCP rule
+// floor(log2 max) - emax, emax = 8 for e4m3 and 2 for e2m1).  The biased fp32
+// exponent is floor(log2) + 127; below fp32's normal range the clamp to
+// 2^-127 decides.  NaN and infinity order above every finite magnitude.
+template <int FMT>
+__device__ __forceinline__ uint32_t mx_scale_byte(uint32_t amax_bits) {
+  if (amax_bits >= 0x7f800000u) return 255u;
+  const int s = (int)(amax_bits >> 23) - (FMT == kMxfp8 ? 8 : 2);
+  return s > 0 ? (uint32_t)s : 0u;
+}
+// 1 / X, exact: s <= 254 - emax, so the exponent stays normal
+__device__ __forceinline__ float mx_inv_scale(uint32_t s) { return __uint_as_float((254u - s) << 23); }
+
+// Four e4m3 codes of four scaled values, round to nearest even, saturating.
+__device__ __forceinline__ uint32_t mx_e4m3x4(float a, float b, float c, float d) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(lo) : "f"(a), "f"(b));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(hi) : "f"(c), "f"(d));
+  return (uint32_t)lo | ((uint32_t)hi << 16);
+}
+// Eight e2m1 codes of eight scaled values, likewise; element j in nibble j.
+__device__ __forceinline__ uint32_t mx_e2m1x8(const float* v) {
+  uint32_t r;
+  asm("{\n .reg .b8 b0, b1, b2, b3;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n"
+      " mov.b32 %0, {b0, b1, b2, b3};\n}"
+      : "=r"(r)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return r;
+}
+// Eight e2m1 codes to fp32 (exact; fp16 holds every e2m1 value).
+__device__ __forceinline__ void mx_from_e2m1x8(uint32_t w, float* v) {
+  uint32_t h[4];
+  asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %4;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, b0;\n cvt.rn.f16x2.e2m1x2 %1, b1;\n"
+      " cvt.rn.f16x2.e2m1x2 %2, b2;\n cvt.rn.f16x2.e2m1x2 %3, b3;\n}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<__half2*>(&h[i]));
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+// Four e4m3 codes to fp32 (exact; the NaN code gives NaN).
+__device__ __forceinline__ void mx_from_e4m3x4(uint32_t w, float* v) {
+  uint32_t h[2];
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[0]) : "h"((uint16_t)(w & 0xffffu)));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[1]) : "h"((uint16_t)(w >> 16)));
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<__half2*>(&h[i]));
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+
+// Sixteen elements: fp16 / bf16 from two 16-byte words, fp32 from four.
+template <typename T>
+__device__ __forceinline__ void load16(const void* base, size_t i, float (&v)[16]) {
+  const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + i * sizeof(T));
+#pragma unroll
+  for (int q = 0; q < (int)sizeof(T); ++q) {
+    const uint4 u = p[q];
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (sizeof(T) == 4) {
+        v[q * 4 + j] = __uint_as_float(w[j]);
+      } else {
+        v[q * 8 + 2 * j] = Half<T>::to_float((uint16_t)(w[j] & 0xffffu));
+        v[q * 8 + 2 * j + 1] = Half<T>::to_float((uint16_t)(w[j] >> 16));
+      }
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store16(void* base, size_t i, const float (&v)[16]) {
+  uint4* p = reinterpret_cast<uint4*>(static_cast<uint8_t*>(base) + i * sizeof(T));
+#pragma unroll
+  for (int q = 0; q < (int)sizeof(T); ++q) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (sizeof(T) == 4)
+        w[j] = __float_as_uint(v[q * 4 + j]);
+      else
+        w[j] = (uint32_t)Half<T>::from_float(v[q * 8 + 2 * j]) |
+               ((uint32_t)Half<T>::from_float(v[q * 8 + 2 * j + 1]) << 16);
+    }
+    p[q] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// Half a block per thread, the other half in the neighbouring lane (lane ^
+// 1): the block's scale byte, and this half's codes stored at element i.
+// Both lanes of a pair call it.
+template <int FMT>
+__device__ __forceinline__ uint32_t mx_encode16(float (&v)[16], uint8_t* codes, size_t i) {
+  const uint32_t mask = 3u << (threadIdx.x & 30);
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
+  m = max(m, __shfl_xor_sync(mask, m, 1));
+  const uint32_t s = mx_scale_byte<FMT>(m);
+  const float inv = s == 255u ? 0.f : mx_inv_scale(s);
+#pragma unroll
+  for (int j = 0; j < 16; ++j) v[j] = s == 255u ? 0.f : v[j] * inv;
+  if constexpr (FMT == kMxfp8)
+    *reinterpret_cast<uint4*>(codes + i) =
+        make_uint4(mx_e4m3x4(v[0], v[1], v[2], v[3]), mx_e4m3x4(v[4], v[5], v[6], v[7]),
+                   mx_e4m3x4(v[8], v[9], v[10], v[11]), mx_e4m3x4(v[12], v[13], v[14], v[15]));
+  else
+    *reinterpret_cast<uint2*>(codes + i / 2) = make_uint2(mx_e2m1x8(v), mx_e2m1x8(v + 8));
+  return s;
+}
+
+// Zeroes of the scale tiles' padding, split over n_threads threads: the rows
+// M .. a multiple of 128 (words), and in the rows below M the blocks K / 32 ..
+// a multiple of 4 (bytes).
+__device__ __forceinline__ void mx_zero_padding(uint8_t* scales, int M, int K, size_t thread, size_t n_threads) {
+  const int nb = K / 32, kt = (K + 127) / 128;
+  const size_t words = (size_t)(((M + 127) & ~127) - M) * kt;
+  for (size_t i = thread; i < words; i += n_threads)
+    *reinterpret_cast<uint32_t*>(scales + mx_scale_index(M + (int)(i / kt), 4 * (int)(i % kt), kt)) = 0u;
+  if (nb & 3)
+    for (size_t r = thread; r < (size_t)M; r += n_threads)
+      for (int b = nb; b < 4 * kt; ++b) scales[mx_scale_index((int)r, b, kt)] = 0;
+}
+
+}  // namespace qmoe

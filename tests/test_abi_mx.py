@@ -1,0 +1,77 @@
+"""Host-side checks of the microscaled entry points (no GPU): sizes, and bad
+arguments refused with the documented status before anything is enqueued."""
+import pytest
+import torch
+
+FAKE = 0x10000  # 16-byte aligned, never dereferenced: every call below fails its checks first
+
+
+@pytest.fixture(scope="module")
+def L():
+    from int4_block_quantized_gb300 import build as b
+    b.build()
+    from int4_block_quantized_gb300 import binding
+    return binding.lib()
+
+
+def test_scale_bytes(L):
+    assert L.qmoe_mx_scale_bytes(1, 32) == 512
+    assert L.qmoe_mx_scale_bytes(128, 128) == 512
+    assert L.qmoe_mx_scale_bytes(129, 160) == 4 * 512
+    assert L.qmoe_mx_scale_bytes(2 ** 31 - 1, 2 ** 20) == 2 ** 24 * 2 ** 13 * 512
+    for R, K in ((0, 32), (1, 0), (1, 48), (-1, 32), (1, -32)):
+        assert L.qmoe_mx_scale_bytes(R, K) == 0
+
+
+@pytest.mark.parametrize("kw", [dict(x=None), dict(x=FAKE + 8), dict(xdt=3), dict(xdt=-1), dict(fmt=2), dict(fmt=-1),
+                                dict(M=0), dict(K=0), dict(K=48), dict(c=None), dict(c=FAKE + 4), dict(s=None),
+                                dict(s=FAKE + 8)])
+def test_quantize_and_dequant_refuse(L, kw):
+    a = dict(x=FAKE, xdt=0, fmt=0, M=4, K=64, c=FAKE, s=FAKE)
+    a.update(kw)
+    assert L.qmoe_mx_quantize(a["x"], a["xdt"], a["fmt"], a["M"], a["K"], a["c"], a["s"], None) == 1
+    assert L.qmoe_mx_dequant(a["c"], a["s"], a["fmt"], a["M"], a["K"], a["x"], a["xdt"], None) == 1
+
+
+@pytest.mark.parametrize("kw", [dict(x=None), dict(x=FAKE + 8), dict(r=FAKE + 2), dict(w=FAKE + 4), dict(ro=FAKE + 8),
+                                dict(dt=2), dict(eps=-1.0), dict(eps=float("nan")), dict(fmt=7), dict(T=0), dict(H=40),
+                                dict(c=None), dict(s=None)])
+def test_rmsnorm_refuses(L, kw):
+    a = dict(x=FAKE, r=FAKE, w=FAKE, dt=0, T=4, H=64, eps=1e-6, fmt=0, ro=FAKE, c=FAKE, s=FAKE)
+    a.update(kw)
+    assert L.qmoe_rmsnorm_mx(a["x"], a["r"], a["w"], a["dt"], a["T"], a["H"], a["eps"], a["fmt"], a["ro"], a["c"],
+                             a["s"], None) == 1
+
+
+@pytest.mark.parametrize("kw", [dict(xc=None), dict(xs=None), dict(wc=None), dict(ws=None), dict(xc=FAKE + 8),
+                                dict(xs=FAKE + 8), dict(wc=FAKE + 8), dict(ws=FAKE + 8), dict(fmt=2), dict(M=0),
+                                dict(N=0), dict(K=0), dict(K=100), dict(y=None), dict(ydt=3), dict(y=FAKE + 1),
+                                dict(y=FAKE + 2, ydt=2), dict(st=FAKE + 2)])
+def test_matmul_refuses(L, kw):
+    a = dict(xc=FAKE, xs=FAKE, fmt=0, wc=FAKE, ws=FAKE, M=4, N=8, K=64, y=FAKE, ydt=0, st=None)
+    a.update(kw)
+    assert L.qmoe_mx_matmul(a["xc"], a["xs"], a["fmt"], a["wc"], a["ws"], a["M"], a["N"], a["K"], a["y"], a["ydt"],
+                            a["st"], None) == 1
+
+
+@pytest.mark.parametrize("kw", [dict(i=None), dict(o=None), dict(R=0), dict(K=33)])
+def test_scale_adapters_refuse(L, kw):
+    a = dict(i=FAKE, o=FAKE, R=4, K=64)
+    a.update(kw)
+    for f in (L.qmoe_mx_tile_scales, L.qmoe_mx_untile_scales):
+        assert f(a["i"], a["R"], a["K"], a["o"], None) == 1
+    assert L.qmoe_mx_tile_scales(FAKE, 4, 64, FAKE + 8, None) == 1
+    assert L.qmoe_mx_untile_scales(FAKE + 8, 4, 64, FAKE, None) == 1
+
+
+def test_binding_refuses_what_it_cannot_pass_on(L):
+    """Host tensors, wrong types, shapes and formats never reach the library."""
+    from int4_block_quantized_gb300 import binding as B
+    x, c, s = torch.zeros(4, 64), torch.zeros(4, 64, dtype=torch.uint8), torch.zeros(512, dtype=torch.uint8)
+    for call in (lambda: B.qmoe_mx_quantize(x), lambda: B.qmoe_mx_quantize(x, 5),
+                 lambda: B.qmoe_mx_dequant(c, s, B.MXFP8), lambda: B.qmoe_mx_dequant(c, s, 2),
+                 lambda: B.qmoe_rmsnorm_mx(x.half()), lambda: B.qmoe_mx_matmul(c, s, B.MXFP8, c, s),
+                 lambda: B.qmoe_mx_tile_scales(c), lambda: B.qmoe_mx_untile_scales(s, 4, 64)):
+        with pytest.raises(B.QMoEError) as e:
+            call()
+        assert e.value.code == 1
