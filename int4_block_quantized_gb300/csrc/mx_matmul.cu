@@ -1,86 +1,425 @@
 // mx_matmul.cu -- product of a microscaled tensor with MXFP4 weights:
 //   y[m, n] = sum over blocks b of X_x[m, b] X_w[n, b] sum_{k in b} x[m, k] w[n, k]
 // with fp32 sums, rounded once to the output's type.
+//
+// The tensor cores multiply block-scaled operands directly
+// (tcgen05.mma.block_scale): codes go from HBM to shared memory and scales on
+// to tensor memory as they are, no thread touches either.  Weight rows are
+// the MMA's M = 128 operand and tokens its N, so that one token costs a
+// narrow MMA and not a 128-row one.  A pipeline stage is 128 bytes per row:
+//   MXFP4 x: 256 k (kind::mxf4, four MMAs of 64 k, two scale words);
+//   MXFP8 x: 128 k (kind::mxf8f6f4, four MMAs of 32 k, one scale word), the
+//            e2m1 codes widened on the way in to 16 codes per 16 bytes, the
+//            first 8 of them used.
+#include <cuda.h>
+
 #include "launch.h"
 #include "mx.cuh"
+#include "tmap.h"
 
 namespace qmoe {
 
-// 32 x 32 outputs per CTA, one block (32 k) at a time: the block's codes of 32
-// tokens and 32 weight rows are decoded into shared memory, scales applied.
-template <typename TY, int FMT>
-__global__ void __launch_bounds__(256) mx_matmul_kernel(const uint8_t* __restrict__ xc, const uint8_t* __restrict__ xs,
-                                                        const uint8_t* __restrict__ wc, const uint8_t* __restrict__ ws,
-                                                        int M, int N, int K, TY* __restrict__ y) {
-  __shared__ float sx[32][33], sw[32][33];
-  pdl_wait();
-  const int kt = (K + 127) / 128, tid = threadIdx.x;
-  const int nt = (N + 31) / 32, m0 = (int)(blockIdx.x / nt) * 32, n0 = (int)(blockIdx.x % nt) * 32;
-  float acc[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int b = 0; b < K / 32; ++b) {
-    const int r = tid >> 3, c = (tid & 7) * 4;  // 4 elements of row r
-    {
-      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (m0 + r < M) {
-        const size_t e = (size_t)(m0 + r) * K + b * 32 + c;
-        if (FMT == kMxfp8) mx_from_e4m3x4(*reinterpret_cast<const uint32_t*>(xc + e), v);
-        else mx_from_e2m1x8(*reinterpret_cast<const uint16_t*>(xc + e / 2), v);
-        const float X = mx_scale(xs[mx_scale_index(m0 + r, b, kt)]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] *= X;
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) sx[r][c + j] = v[j];
+constexpr int kMmThreads = 192;       // warp 0 copies, warp 1 issues MMAs, warps 2-5 write y
+constexpr int kMmFillThreads = 320;   // + warps 6-9: weights by loads and stores (see FILL)
+constexpr uint32_t kMmSmem = 232448;  // 227 KB
+constexpr uint32_t kMmBars = 1024;
+
+struct MmParams {
+  const uint8_t *xs, *ws, *wc;
+  void* y;
+  uint32_t* status;
+  int M, N, K, y_dtype;
+  int row_tiles, tok_tiles, kt;  // tiles of 128 weight rows, of BN tokens; scale tiles along K
+  int split;                     // CTAs of a cluster that share a tile's K
+};
+
+template <int XF, int BN>
+struct MmPlan {
+  static constexpr int kStageK = XF == kMxfp4 ? 256 : 128;  // elements
+  static constexpr int kWords = kStageK / 128;              // scale tiles of a stage along K
+  static constexpr int kTokSf = (BN + 127) / 128;           // scale tiles of a stage along the tokens
+  static constexpr uint32_t kA = 128 * 128, kB = BN * 128;
+  // bytes that a weight copy reports: those read, also where the codes are widened
+  static constexpr uint32_t kTxA = XF == kMxfp4 ? kA : kA / 2;
+  static constexpr uint32_t kSf = 512 * kWords * (1 + kTokSf);
+  static constexpr uint32_t kStage = kA + kB + kSf;
+  static constexpr int kStages0 = (int)((kMmSmem - kMmBars - 1024) / (kStage + 1023));
+  static constexpr int kStages = kStages0 > 12 ? 12 : kStages0;
+  static constexpr uint32_t kAb = (kA + kB + 1023) & ~1023u;
+  static constexpr uint32_t kTotal = kMmBars + kStages * (kAb + kSf) + 1024;
+  // tensor memory: two accumulators, then the stage's scales.  At 256 tokens
+  // the two overlap by 32 columns, since the scales need 24 of the 512.
+  static constexpr bool kOverlap = BN == 256;
+  static constexpr uint32_t kAcc1 = kOverlap ? 224 : BN;
+  static constexpr uint32_t kSfa = kAcc1 + BN;
+  static constexpr uint32_t kSfb = kSfa + 4 * kWords;
+  static constexpr uint32_t kCols0 = kSfb + 4 * kWords * kTokSf;
+  static constexpr uint32_t kCols = kCols0 <= 64 ? 64 : kCols0 <= 128 ? 128 : kCols0 <= 256 ? 256 : 512;
+};
+
+// Bounded wait; gives up when another role has (about 2 s, status bit).
+__device__ __forceinline__ bool mm_wait(uint64_t* bar, uint32_t parity, uint32_t* status, volatile int* abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try_wait_sleep(bar, parity, 20000u)) {
+    if (*abort) return false;
+    if (clock64() - t0 > kWaitLimitCycles) {
+      set_status(status, QMOE_ST_TIMEOUT);
+      *abort = 1;
+      return false;
     }
-    {
-      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (n0 + r < N) {
-        mx_from_e2m1x8(*reinterpret_cast<const uint16_t*>(wc + ((size_t)(n0 + r) * K + b * 32 + c) / 2), v);
-        const float X = mx_scale(ws[mx_scale_index(n0 + r, b, kt)]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] *= X;
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) sw[r][c + j] = v[j];
-    }
-    __syncthreads();
-    for (int k = 0; k < 32; ++k) {
-      const float w = sw[tid & 31][k];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] = fmaf(sx[(tid >> 5) * 4 + i][k], w, acc[i]);
-    }
-    __syncthreads();
   }
-  const int n = n0 + (tid & 31);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int m = m0 + (tid >> 5) * 4 + i;
-    if (m < M && n < N) {
-      if constexpr (sizeof(TY) == 4) y[(size_t)m * N + n] = acc[i];
-      else reinterpret_cast<uint16_t*>(y)[(size_t)m * N + n] = Half<TY>::from_float(acc[i]);
+  return true;
+}
+
+__device__ __forceinline__ void mm_store(const MmParams& p, size_t i, float v) {
+  if (p.y_dtype == QMOE_F32) static_cast<float*>(p.y)[i] = v;
+  else static_cast<uint16_t*>(p.y)[i] = p.y_dtype == QMOE_BF16 ? Half<__nv_bfloat16>::from_float(v) : Half<__half>::from_float(v);
+}
+
+// Tile t of the grid: groups of 8 row tiles, so that the tiles in flight share
+// weights and tokens in L2.
+__device__ __forceinline__ void mm_tile(const MmParams& p, int t, int& rt, int& tt) {
+  const int per = 8 * p.tok_tiles, g = t / per, r = t - g * per;
+  const int rows = min(8, p.row_tiles - g * 8);
+  rt = g * 8 + r % rows;
+  tt = r / rows;
+}
+
+// FILL (MXFP8 x only): the TMA copy that widens e2m1 codes wants rows of a
+// multiple of 128 codes on 32-byte boundaries; other weights are read and
+// spread by four warps.
+template <int XF, int BN, bool FILL>
+__global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
+    mx_matmul_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
+                     const MmParams p) {
+  using P = MmPlan<XF, BN>;
+  constexpr int S = P::kStages;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem);
+  uint64_t* empty = full + S;
+  uint64_t* acc_full = empty + S;       // [2]
+  uint64_t* acc_free = acc_full + 2;    // [2]
+  uint64_t* fin = acc_free + 2;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(fin + 1);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+  uint8_t* ring = smem + kMmBars;
+  uint8_t* sfring = ring + S * P::kAb;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], FILL ? 5 : 1);
+      mbar_init(&empty[s], 1);
     }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_free[b], 4);
+    }
+    mbar_init(fin, 1);
+    *s_abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(s_tmem, P::kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  pdl_wait();
+  pdl_trigger();
+
+  // this CTA's tiles and its share [c0, c1) of their stages along K
+  const int rank = p.split > 1 ? (int)cluster_ctarank() : 0;
+  const int tiles = p.row_tiles * p.tok_tiles;
+  const int first = blockIdx.x / p.split, step = p.split > 1 ? tiles : gridDim.x;
+  const int chunks = (p.K + P::kStageK - 1) / P::kStageK;
+  const int c0 = (int)((long long)chunks * rank / p.split), c1 = (int)((long long)chunks * (rank + 1) / p.split);
+
+  if (warp == 0) {
+    // ------------------------------------------------------------- copies
+    if (lane == 0) {
+      int it = 0, s = 0;
+      uint32_t ph = 0;
+      for (int t = first; t < tiles && !*s_abort; t += step) {
+        int rt, tt;
+        mm_tile(p, t, rt, tt);
+        const int m0 = tt * BN;
+        for (int c = c0; c < c1; ++c, ++it) {
+          if (it >= S && !mm_wait(&empty[s], ph ^ 1u, p.status, s_abort)) break;
+          uint8_t* st = ring + s * P::kAb;
+          uint8_t* sf = sfring + s * P::kSf;
+          const int q0 = c * P::kWords, nq = min(P::kWords, p.kt - q0);
+          // scale tiles of the tokens: those that exist (128-row tiles m0 / 128 ..)
+          const int t0 = m0 >> 7, nt = min(P::kTokSf, ((p.M + 127) >> 7) - t0);
+          mbar_arrive_expect_tx(&full[s], (FILL ? 0u : P::kTxA) + P::kB + 512u * nq * (1 + nt));
+          if (!FILL) tma_load_2d(st, &tm_w, c * 128, rt * 128, &full[s]);
+          tma_load_2d(st + P::kA, &tm_x, c * 128, m0, &full[s]);
+          bulk_g2s(sf, p.ws + ((size_t)rt * p.kt + q0) * 512, 512u * nq, &full[s]);
+          for (int i = 0; i < nt; ++i)
+            bulk_g2s(sf + 512 * P::kWords * (1 + i), p.xs + ((size_t)(t0 + i) * p.kt + q0) * 512, 512u * nq, &full[s]);
+          if (++s == S) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      if (*s_abort)  // let the copies in flight land before the CTA exits
+        for (int i = 0; i < S; ++i)
+          if (it > i) mbar_wait(&full[i], ((it - 1 - i) / S) & 1, nullptr);
+    }
+  } else if (warp == 1) {
+    // --------------------------------------------------------------- MMAs
+    int n = 0, s = 0;
+    uint32_t ph = 0;
+    bool ok = true, issued = false;
+    for (int t = first; t < tiles && ok; t += step, ++n) {
+      const int b = n & 1;
+      int rt, tt;
+      mm_tile(p, t, rt, tt);
+      if (P::kOverlap) {
+        if (n >= 1) ok = mm_wait(&acc_free[0], (n - 1) & 1, p.status, s_abort);
+      } else {
+        if (n >= 2) ok = mm_wait(&acc_free[b], ((n >> 1) - 1) & 1, p.status, s_abort);
+      }
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t d = tmem + (b ? P::kAcc1 : 0);
+      // BN = 64: an odd token tile starts in the middle of its scale tile
+      const uint32_t sfb = tmem + P::kSfb + (BN == 64 ? 2 * (tt & 1) : 0);
+      for (int c = c0; c < c1; ++c) {
+        ok = mm_wait(&full[s], ph, p.status, s_abort);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t st = smem_u32(ring + s * P::kAb), sf = smem_u32(sfring + s * P::kSf);
+        const int left = p.K - c * P::kStageK;  // elements from here on
+#pragma unroll
+        for (int q = 0; q < P::kWords; ++q) {
+          if (q * 128 >= left) break;
+          tmem_cp_scales_elect(tmem + P::kSfa + 4 * q, rows16_desc(sf + 512 * q));
+#pragma unroll
+          for (int i = 0; i < P::kTokSf; ++i)
+            tmem_cp_scales_elect(tmem + P::kSfb + 4 * (q * P::kTokSf + i),
+                                 rows16_desc(sf + 512 * (P::kWords * (1 + i) + q)));
+        }
+        const uint64_t da = sw128_desc(st), db = sw128_desc(st + P::kA);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (j * (P::kStageK / 4) >= left) break;
+          const uint32_t acc = (c > c0 || j > 0) ? 1u : 0u;
+          if (XF == kMxfp4)
+            mma_mxf4_elect(d, da + 2 * j, db + 2 * j, idesc_mx(128, BN, 1, 1, 2 * (j & 1), 2 * (j & 1)),
+                           tmem + P::kSfa + 4 * (j >> 1), sfb + 4 * P::kTokSf * (j >> 1), acc);
+          else
+            mma_mxf8f6f4_elect(d, da + 2 * j, db + 2 * j, idesc_mx(128, BN, 5, 0, j, j), tmem + P::kSfa, sfb, acc);
+        }
+        issued = true;
+        mma_commit_elect(&empty[s]);
+        if (++s == S) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+      if (ok) mma_commit_elect(&acc_full[b]);
+    }
+    if (issued) {  // all MMAs have finished before tensor memory is freed
+      mma_commit_elect(fin);
+      mbar_wait(fin, 0, nullptr);
+    }
+  } else if (warp < 6) {
+    // ------------------------------------------------------------- outputs
+    const int qd = warp & 3, row = qd * 32 + lane;
+    int n = 0;
+    for (int t = first; t < tiles; t += step, ++n) {
+      const int b = n & 1;
+      int rt, tt;
+      mm_tile(p, t, rt, tt);
+      if (!mm_wait(&acc_full[b], (n >> 1) & 1, p.status, s_abort)) break;
+      tc_fence_after();
+      const uint32_t d = tmem + ((uint32_t)(qd * 32) << 16) + (b ? P::kAcc1 : 0);
+      const int m0 = tt * BN, nn = rt * 128 + row;
+      constexpr int W = BN < 32 ? BN : 32, C = BN / W;
+      if (p.split > 1) {
+        float* part = reinterpret_cast<float*>(ring);  // [BN][128]: every stage has been read
+        for (int c = 0; c < C; ++c) {
+          uint32_t v[W];
+          if constexpr (W == 32) tmem_ld32(d + c * W, v);
+          else tmem_ld16(d + c * W, v);
+#pragma unroll
+          for (int j = 0; j < W; ++j) part[(c * W + j) * 128 + row] = __uint_as_float(v[j]);
+        }
+      } else {
+        for (int i = 0; i < C; ++i) {
+          // the chunk in the columns that the other accumulator shares comes first
+          const int c = P::kOverlap && b == 0 ? (i + C - 1) % C : i;
+          uint32_t v[W];
+          if constexpr (W == 32) tmem_ld32(d + c * W, v);
+          else tmem_ld16(d + c * W, v);
+          if (P::kOverlap && i == 0) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&acc_free[0]);
+          }
+          if (nn < p.N) {
+#pragma unroll
+            for (int j = 0; j < W; ++j)
+              if (m0 + c * W + j < p.M) mm_store(p, (size_t)(m0 + c * W + j) * p.N + nn, __uint_as_float(v[j]));
+          }
+        }
+        if (!P::kOverlap) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&acc_free[b]);
+        }
+      }
+    }
+  } else if (FILL) {
+    // -------------------------------------- weights of ragged rows (MXFP8 x)
+    const int r = tid - 192;  // row of the tile
+    int it = 0, s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int t = first; t < tiles && ok; t += step) {
+      int rt, tt;
+      mm_tile(p, t, rt, tt);
+      const int nn = rt * 128 + r;
+      const uint8_t* src = p.wc + (size_t)nn * (p.K / 2);
+      for (int c = c0; c < c1; ++c, ++it) {
+        uint4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)  // 32 codes each
+          v[i] = nn < p.N && c * 128 + i * 32 < p.K ? __ldg(reinterpret_cast<const uint4*>(src + c * 64 + i * 16))
+                                                    : make_uint4(0, 0, 0, 0);
+        if (it >= S && !mm_wait(&empty[s], ph ^ 1u, p.status, s_abort)) {
+          ok = false;
+          break;
+        }
+        uint8_t* st = ring + s * P::kAb + r * 128;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          *reinterpret_cast<uint4*>(st + (((2 * i) ^ (r & 7)) << 4)) = make_uint4(v[i].x, v[i].y, 0, 0);
+          *reinterpret_cast<uint4*>(st + (((2 * i + 1) ^ (r & 7)) << 4)) = make_uint4(v[i].z, v[i].w, 0, 0);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[s]);
+        if (++s == S) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+    }
+  }
+  __syncwarp();
+  if (p.split > 1) {
+    // the cluster's partial sums, added in rank order: CTA `rank` writes the
+    // tokens j = rank, rank + split, ...
+    cluster_sync_all();
+    int rt, tt;
+    mm_tile(p, first, rt, tt);
+    const float* part = reinterpret_cast<const float*>(ring);
+    const int rows = min(BN, p.M - tt * BN);
+    for (int i = tid; i < BN * 128; i += blockDim.x) {
+      const int j = (i >> 7) * p.split + rank, nn = rt * 128 + (i & 127);
+      if (j >= rows) break;
+      if (nn < p.N) {
+        float v = 0.f;
+        for (int r = 0; r < p.split; ++r) v += ld_dsmem_f32(part + j * 128 + (i & 127), r);
+        mm_store(p, (size_t)(tt * BN + j) * p.N + nn, v);
+      }
+    }
+    cluster_sync_all();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, P::kCols);
   }
 }
 
-template <typename TY>
-static cudaError_t launch_matmul_t(const uint8_t* xc, const uint8_t* xs, int x_format, const uint8_t* wc,
-                                   const uint8_t* ws, int M, int N, int K, void* y, cudaStream_t st) {
-  const long long tiles = (long long)((N + 31) / 32) * ((M + 31) / 32);
-  if (tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const dim3 g((unsigned)tiles);
-  if (x_format == kMxfp8)
-    return launch_kernel(mx_matmul_kernel<TY, kMxfp8>, g, dim3(256), 0, st, true, xc, xs, wc, ws, M, N, K,
-                         static_cast<TY*>(y));
-  return launch_kernel(mx_matmul_kernel<TY, kMxfp4>, g, dim3(256), 0, st, true, xc, xs, wc, ws, M, N, K,
-                       static_cast<TY*>(y));
+template <int XF, int BN, bool FILL>
+static cudaError_t launch_mm(MmParams p, const uint8_t* xc, cudaStream_t st) {
+  using P = MmPlan<XF, BN>;
+  static_assert(P::kTotal <= kMmSmem && P::kCols0 <= 512, "plan");
+  p.tok_tiles = (p.M + BN - 1) / BN;
+  const long long tiles = (long long)p.row_tiles * p.tok_tiles;
+  if (tiles > (1LL << 27)) return cudaErrorInvalidValue;
+  CUtensorMap tw, tx;
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  const cuuint32_t es[2] = {1, 1};
+  auto map = [&](CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t inner, uint64_t rows,
+                 uint64_t stride, uint32_t box_rows) {
+    const cuuint64_t dims[2] = {inner, rows}, strides[1] = {stride};
+    const cuuint32_t box[2] = {128, box_rows};
+    return fn(m, dt, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  const uint64_t half = p.K / 2;
+  if (!map(&tx, xc, CU_TENSOR_MAP_DATA_TYPE_UINT8, XF == kMxfp4 ? half : p.K, p.M, XF == kMxfp4 ? half : p.K, BN))
+    return cudaErrorNotSupported;
+  if (FILL) {
+    tw = tx;
+  } else if (XF == kMxfp4) {
+    if (!map(&tw, p.wc, CU_TENSOR_MAP_DATA_TYPE_UINT8, half, p.N, half, 128)) return cudaErrorNotSupported;
+  } else {
+    if (!map(&tw, p.wc, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, p.K, p.N, half, 128)) return cudaErrorNotSupported;
+  }
+  // few tiles: a cluster of up to 8 CTAs shares a tile's K
+  const int sms = device_sm_count(), chunks = (p.K + P::kStageK - 1) / P::kStageK;
+  p.split = 1;
+  while (p.split < 8 && 2 * p.split <= chunks && tiles * p.split * 2 <= sms) p.split *= 2;
+  auto kernel = mx_matmul_kernel<XF, BN, FILL>;
+  cudaError_t err = ensure_smem(kernel, P::kTotal);
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.split > 1 ? tiles * p.split : tiles < sms ? tiles : sms));
+  cfg.blockDim = dim3(FILL ? kMmFillThreads : kMmThreads);
+  cfg.dynamicSmemBytes = P::kTotal;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = p.split;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, tw, tx, p);
+}
+
+template <int XF, bool FILL>
+static cudaError_t launch_mm_bn(const MmParams& p, const uint8_t* xc, cudaStream_t st) {
+  if (p.M <= 16) return launch_mm<XF, 16, FILL>(p, xc, st);
+  if (p.M <= 32) return launch_mm<XF, 32, FILL>(p, xc, st);
+  if (p.M <= 64) return launch_mm<XF, 64, FILL>(p, xc, st);
+  // 256-token tiles once they fill the card
+  if ((long long)p.row_tiles * ((p.M + 255) / 256) >= device_sm_count()) return launch_mm<XF, 256, FILL>(p, xc, st);
+  return launch_mm<XF, 128, FILL>(p, xc, st);
 }
 
 cudaError_t launch_mx_matmul(const uint8_t* xc, const uint8_t* xs, int x_format, const uint8_t* wc, const uint8_t* ws,
                              int M, int N, int K, void* y, int y_dtype, uint32_t* status, cudaStream_t st) {
-  (void)status;
-  if (y_dtype == QMOE_F32) return launch_matmul_t<float>(xc, xs, x_format, wc, ws, M, N, K, y, st);
-  if (y_dtype == QMOE_BF16) return launch_matmul_t<__nv_bfloat16>(xc, xs, x_format, wc, ws, M, N, K, y, st);
-  return launch_matmul_t<__half>(xc, xs, x_format, wc, ws, M, N, K, y, st);
+  MmParams p = {};
+  p.xs = xs;
+  p.ws = ws;
+  p.wc = wc;
+  p.y = y;
+  p.status = status;
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.y_dtype = y_dtype;
+  p.row_tiles = (N + 127) / 128;
+  p.kt = (K + 127) / 128;
+  if (x_format == kMxfp4) return launch_mm_bn<kMxfp4, false>(p, xc, st);
+  if (K % 128 || (reinterpret_cast<uintptr_t>(wc) & 31)) return launch_mm_bn<kMxfp8, true>(p, xc, st);
+  return launch_mm_bn<kMxfp8, false>(p, xc, st);
 }
 
 }  // namespace qmoe
