@@ -235,36 +235,42 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// 1 in the lane that elect.sync names (the same one every time), else 0.
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t e;
+  asm volatile("{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n selp.b32 %0, 1, 0, e;\n}" : "=r"(e));
+  return e;
+}
 // Block-scaled D[tmem] (+)= (A x scales) (B x scales)^T, operands by shared-memory
-// descriptors, scales (e8m0) in tensor memory, by the elected lane of a
-// converged warp.  kind::mxf4: e2m1 x e2m1, 64 k, two blocks of 32 per
+// descriptors, scales (e8m0) in tensor memory, by the lane of a converged warp
+// whose `e` (elect_lane) is 1.  kind::mxf4: e2m1 x e2m1, 64 k, two blocks of 32 per
 // instruction; kind::mxf8f6f4: 8-bit containers, 32 k, one block.
-__device__ __forceinline__ void mma_mxf4_elect(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+__device__ __forceinline__ void mma_mxf4(uint32_t e, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                                uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %6, 0;\n"
+      "{\n .reg .pred p, e;\n setp.ne.b32 e, %7, 0;\n setp.ne.b32 p, %6, 0;\n"
       " @e tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(
           d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(e)
       : "memory");
 }
-__device__ __forceinline__ void mma_mxf8f6f4_elect(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+__device__ __forceinline__ void mma_mxf8f6f4(uint32_t e, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                                    uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %6, 0;\n"
+      "{\n .reg .pred p, e;\n setp.ne.b32 e, %7, 0;\n setp.ne.b32 p, %6, 0;\n"
       " @e tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(
           d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(e)
       : "memory");
 }
 // 32 rows x 16 bytes of shared memory into four columns of tensor memory,
 // repeated in all four lane quadrants (a 128 x 4 tile of scales); ordered
 // before the tcgen05.mma that the same lane issues next.
-__device__ __forceinline__ void tmem_cp_scales_elect(uint32_t taddr, uint64_t desc) {
+__device__ __forceinline__ void tmem_cp_scales(uint32_t e, uint32_t taddr, uint64_t desc) {
   asm volatile(
-      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      "{\n .reg .pred e;\n setp.ne.b32 e, %2, 0;\n"
       " @e tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n}" ::"r"(taddr),
-      "l"(desc)
+      "l"(desc), "r"(e)
       : "memory");
 }
 // Unswizzled descriptor of 8-row x 16-byte groups 128 bytes apart.
@@ -322,6 +328,18 @@ __device__ __forceinline__ uint32_t cluster_count_x() {
 }
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// four fp32 to the same shared-memory offset in CTA `rank` of the cluster
+__device__ __forceinline__ void st_dsmem_v4(float* local, uint32_t rank, uint32_t a, uint32_t b, uint32_t c,
+                                            uint32_t d) {
+  uint32_t addr = smem_u32(local), raddr;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(raddr) : "r"(addr), "r"(rank));
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(raddr), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
 }
 // fp32 load from the same shared-memory offset in CTA `rank` of the cluster
 __device__ __forceinline__ float ld_dsmem_f32(const float* local, uint32_t rank) {

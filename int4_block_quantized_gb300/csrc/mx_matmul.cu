@@ -42,11 +42,13 @@ struct MmPlan {
   // bytes that a weight copy reports: those read, also where the codes are widened
   static constexpr uint32_t kTxA = XF == kMxfp4 ? kA : kA / 2;
   static constexpr uint32_t kSf = 512 * kWords * (1 + kTokSf);
-  static constexpr uint32_t kStage = kA + kB + kSf;
-  static constexpr int kStages0 = (int)((kMmSmem - kMmBars - 1024) / (kStage + 1023));
-  static constexpr int kStages = kStages0 > 12 ? 12 : kStages0;
   static constexpr uint32_t kAb = (kA + kB + 1023) & ~1023u;
-  static constexpr uint32_t kTotal = kMmBars + kStages * (kAb + kSf) + 1024;
+  // a split tile's partial sums [split][tokens of a CTA / 4][128][4]: a place of
+  // their own where they are small, else the ring once the cluster is done with it
+  static constexpr uint32_t kPart = BN <= 64 ? (BN < 32 ? 32 : BN) * 512 : 0;
+  static constexpr int kStages0 = (int)((kMmSmem - kMmBars - 1024 - kPart) / (kAb + kSf));
+  static constexpr int kStages = kStages0 > 12 ? 12 : kStages0;
+  static constexpr uint32_t kTotal = kMmBars + kStages * (kAb + kSf) + kPart + 1024;
   // tensor memory: two accumulators, then the stage's scales.  At 256 tokens
   // the two overlap by 32 columns, since the scales need 24 of the 512.
   static constexpr bool kOverlap = BN == 256;
@@ -54,7 +56,6 @@ struct MmPlan {
   static constexpr uint32_t kSfa = kAcc1 + BN;
   static constexpr uint32_t kSfb = kSfa + 4 * kWords;
   static constexpr uint32_t kCols0 = kSfb + 4 * kWords * kTokSf;
-  static constexpr uint32_t kCols = kCols0 <= 64 ? 64 : kCols0 <= 128 ? 128 : kCols0 <= 256 ? 256 : 512;
 };
 
 // Bounded wait; gives up when another role has (about 2 s, status bit).
@@ -122,13 +123,15 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
     fence_barrier_init();
   }
   if (warp == 1) {
-    tmem_alloc(s_tmem, P::kCols);
+    tmem_alloc(s_tmem, 512);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *s_tmem;
+  // all 512 columns are this CTA's, so they start at 0
+  constexpr uint32_t tmem = 0;
+  if (P::kPart && p.split > 1) cluster_arrive();  // this CTA runs: its shared memory may be written
   pdl_wait();
   pdl_trigger();
 
@@ -176,6 +179,7 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
     int n = 0, s = 0;
     uint32_t ph = 0;
     bool ok = true, issued = false;
+    const uint32_t el = elect_lane();
     for (int t = first; t < tiles && ok; t += step, ++n) {
       const int b = n & 1;
       int rt, tt;
@@ -199,10 +203,10 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
 #pragma unroll
         for (int q = 0; q < P::kWords; ++q) {
           if (q * 128 >= left) break;
-          tmem_cp_scales_elect(tmem + P::kSfa + 4 * q, rows16_desc(sf + 512 * q));
+          tmem_cp_scales(el, tmem + P::kSfa + 4 * q, rows16_desc(sf + 512 * q));
 #pragma unroll
           for (int i = 0; i < P::kTokSf; ++i)
-            tmem_cp_scales_elect(tmem + P::kSfb + 4 * (q * P::kTokSf + i),
+            tmem_cp_scales(el, tmem + P::kSfb + 4 * (q * P::kTokSf + i),
                                  rows16_desc(sf + 512 * (P::kWords * (1 + i) + q)));
         }
         const uint64_t da = sw128_desc(st), db = sw128_desc(st + P::kA);
@@ -211,10 +215,10 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
           if (j * (P::kStageK / 4) >= left) break;
           const uint32_t acc = (c > c0 || j > 0) ? 1u : 0u;
           if (XF == kMxfp4)
-            mma_mxf4_elect(d, da + 2 * j, db + 2 * j, idesc_mx(128, BN, 1, 1, 2 * (j & 1), 2 * (j & 1)),
+            mma_mxf4(el, d, da + 2 * j, db + 2 * j, idesc_mx(128, BN, 1, 1, 2 * (j & 1), 2 * (j & 1)),
                            tmem + P::kSfa + 4 * (j >> 1), sfb + 4 * P::kTokSf * (j >> 1), acc);
           else
-            mma_mxf8f6f4_elect(d, da + 2 * j, db + 2 * j, idesc_mx(128, BN, 5, 0, j, j), tmem + P::kSfa, sfb, acc);
+            mma_mxf8f6f4(el, d, da + 2 * j, db + 2 * j, idesc_mx(128, BN, 5, 0, j, j), tmem + P::kSfa, sfb, acc);
         }
         issued = true;
         mma_commit_elect(&empty[s]);
@@ -242,16 +246,7 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
       const uint32_t d = tmem + ((uint32_t)(qd * 32) << 16) + (b ? P::kAcc1 : 0);
       const int m0 = tt * BN, nn = rt * 128 + row;
       constexpr int W = BN < 32 ? BN : 32, C = BN / W;
-      if (p.split > 1) {
-        float* part = reinterpret_cast<float*>(ring);  // [BN][128]: every stage has been read
-        for (int c = 0; c < C; ++c) {
-          uint32_t v[W];
-          if constexpr (W == 32) tmem_ld32(d + c * W, v);
-          else tmem_ld16(d + c * W, v);
-#pragma unroll
-          for (int j = 0; j < W; ++j) part[(c * W + j) * 128 + row] = __uint_as_float(v[j]);
-        }
-      } else {
+      if (p.split == 1) {
         for (int i = 0; i < C; ++i) {
           // the chunk in the columns that the other accumulator shares comes first
           const int c = P::kOverlap && b == 0 ? (i + C - 1) % C : i;
@@ -315,29 +310,54 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
   }
   __syncwarp();
   if (p.split > 1) {
-    // the cluster's partial sums, added in rank order: CTA `rank` writes the
-    // tokens j = rank, rank + split, ...
-    cluster_sync_all();
+    // Each CTA sends its partial sums of tokens j to CTA j / per, which adds
+    // them in rank order and writes y.
+    float* part = reinterpret_cast<float*>(P::kPart ? sfring + S * P::kSf : ring);
     int rt, tt;
     mm_tile(p, first, rt, tt);
-    const float* part = reinterpret_cast<const float*>(ring);
-    const int rows = min(BN, p.M - tt * BN);
-    for (int i = tid; i < BN * 128; i += blockDim.x) {
-      const int j = (i >> 7) * p.split + rank, nn = rt * 128 + (i & 127);
-      if (j >= rows) break;
-      if (nn < p.N) {
-        float v = 0.f;
-        for (int r = 0; r < p.split; ++r) v += ld_dsmem_f32(part + j * 128 + (i & 127), r);
-        mm_store(p, (size_t)(tt * BN + j) * p.N + nn, v);
+    const int rows = min(BN, p.M - tt * BN), per = max(4, BN / p.split), lper = 31 - __clz(per);
+    if (!P::kPart) cluster_arrive();
+    cluster_wait();
+    if (warp >= 2 && warp < 6) {
+      const int qd = warp & 3, row = qd * 32 + lane;
+      constexpr int W = BN < 32 ? BN : 32;
+#pragma unroll 1
+      for (int c = 0; c < rows; c += W) {
+        uint32_t v[W];
+        if constexpr (W == 32) tmem_ld32(tmem + ((uint32_t)(qd * 32) << 16) + c, v);
+        else tmem_ld16(tmem + ((uint32_t)(qd * 32) << 16) + c, v);
+#pragma unroll
+        for (int j = 0; j < W; j += 4)
+          if (c + j < rows)
+            st_dsmem_v4(part + ((rank * per + ((c + j) & (per - 1))) * 128 + 4 * row), (c + j) >> lper, v[j], v[j + 1],
+                        v[j + 2], v[j + 3]);
       }
     }
+    __syncwarp();
     cluster_sync_all();
+    const int mine = min(per, rows - rank * per);
+    const float4* p4 = reinterpret_cast<const float4*>(part);
+    for (int i = tid; i < (mine + 3) / 4 * 128; i += blockDim.x) {
+      const int nn = rt * 128 + (i & 127), j = rank * per + (i >> 7) * 4;
+      if (nn < p.N) {
+        float4 v = p4[i];
+        for (int r = 1; r < p.split; ++r) {
+          const float4 u = p4[r * per * 32 + i];
+          v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+        }
+        const size_t o = (size_t)(tt * BN + j) * p.N + nn;
+        mm_store(p, o, v.x);
+        if (j + 1 < rows) mm_store(p, o + p.N, v.y);
+        if (j + 2 < rows) mm_store(p, o + 2 * (size_t)p.N, v.z);
+        if (j + 3 < rows) mm_store(p, o + 3 * (size_t)p.N, v.w);
+      }
+    }
   }
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, P::kCols);
+    tmem_dealloc(tmem, 512);
   }
 }
 
