@@ -362,6 +362,10 @@ def qmoe_unpack_zero_points(zp_packed, nb):
 # qmoe_mx_scale_bytes(R, K) bytes in the tile order that qmoe.h defines.
 # These calls check what they are given (CUDA, contiguous, one device, types
 # and sizes) and run on the tensors' device, on torch's current stream there.
+# A call's kernel takes a few microseconds at one token, so the host side is
+# kept short: sizes worked out here, plain integers handed to ctypes, and the
+# stream's handle read without building a torch.cuda.Stream (2.9 us of 14 on
+# the GB300's host cores).
 
 _MX_DT = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
 
@@ -370,81 +374,91 @@ def _bad(where, what):
     raise QMoEError(1, "%s: %s" % (where, what))
 
 
-def _mx_rows(t, where, dtypes):
-    """Shape of a contiguous 2-D CUDA tensor of one of the dtypes."""
-    if t.dtype not in dtypes or not t.is_cuda or t.dim() != 2 or not t.is_contiguous():
-        _bad(where, "wants a contiguous 2-D CUDA tensor of %s" % " / ".join(str(d) for d in dtypes))
+def _mx_rows(t, where):
+    """Shape of a contiguous 2-D CUDA tensor."""
+    if not t.is_cuda or t.dim() != 2 or not t.is_contiguous():
+        _bad(where, "wants a contiguous 2-D CUDA tensor")
     return t.shape
 
 
-def _mx_same(t, like, dtype, numel, where, name):
-    """A contiguous tensor of a given type and size on another one's device."""
-    if t.dtype != dtype or t.numel() != numel or t.device != like.device or not t.is_contiguous():
-        _bad(where, "%s: wants %d contiguous %s on %s" % (name, numel, dtype, like.device))
-    return t
+def _mx_same(t, dev, dtype, numel, where, name):
+    """Address of a contiguous tensor of a given type and size on device dev."""
+    if t.dtype != dtype or t.numel() != numel or t.get_device() != dev or not t.is_contiguous():
+        _bad(where, "%s: wants %d contiguous %s on cuda:%d" % (name, numel, dtype, dev))
+    return t.data_ptr()
 
 
 def _mx_tensor(codes, scales, fmt, where):
     """(R, K) of an MX tensor."""
-    if fmt not in (MXFP8, MXFP4):
+    if codes.dtype != torch.uint8:
+        _bad(where, "codes are uint8")
+    R, K = _mx_rows(codes, where)
+    if fmt == MXFP4:
+        K *= 2
+    elif fmt != MXFP8:
         _bad(where, "unknown format %r" % (fmt,))
-    R, c = _mx_rows(codes, where, (torch.uint8,))
-    K = c if fmt == MXFP8 else 2 * c
-    _mx_same(scales, codes, torch.uint8, qmoe_mx_scale_bytes(R, K), where, "scales")
+    _mx_same(scales, codes.get_device(), torch.uint8, qmoe_mx_scale_bytes(R, K), where, "scales")
     return R, K
 
 
-def _mx_out(R, K, fmt, like, codes, scales, where):
+def _mx_out(R, K, fmt, x, codes, scales, where):
     """(codes, scales) to write an MX tensor [R, K] to: the caller's, or new ones."""
-    if fmt not in (MXFP8, MXFP4):
-        _bad(where, "unknown format %r" % (fmt,))
     n = qmoe_mx_scale_bytes(R, K)
-    if n == 0:
-        _bad(where, "rows >= 1 and a multiple of 32 columns are wanted, got [%d, %d]" % (R, K))
+    if n == 0 or (fmt != MXFP8 and fmt != MXFP4):
+        _bad(where, "format %r, [%d, %d]: MXFP8 or MXFP4, rows and a multiple of 32 columns are wanted" % (fmt, R, K))
     cols = K if fmt == MXFP8 else K // 2
     if codes is None:
-        codes = torch.empty((R, cols), dtype=torch.uint8, device=like.device)
+        codes = x.new_empty((R, cols), dtype=torch.uint8)
     else:
-        _mx_same(codes, like, torch.uint8, R * cols, where, "codes")
+        _mx_same(codes, x.get_device(), torch.uint8, R * cols, where, "codes")
     if scales is None:
-        scales = torch.empty(n, dtype=torch.uint8, device=like.device)
+        scales = codes.new_empty(n)
     else:
-        _mx_same(scales, like, torch.uint8, n, where, "scales")
+        _mx_same(scales, x.get_device(), torch.uint8, n, where, "scales")
     return codes, scales
 
 
 def _mx_call(t, fn, where, *args):
     """fn(*args, stream) on t's device and its current stream."""
-    if t.device.index == torch.cuda.current_device():
-        _check(fn(*args, _stream()), where)
+    dev = t.get_device()
+    if dev == torch.cuda.current_device():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
-        with torch.cuda.device(t.device):
-            _check(fn(*args, _stream()), where)
+        with torch.cuda.device(dev):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if rc:
+        _check(rc, where)
 
 
 def qmoe_mx_scale_bytes(R, K):
     """Bytes of the scale tiles of an MX tensor [R, K] (0 if it cannot be one)."""
-    return int(lib().qmoe_mx_scale_bytes(R, K))
+    return (R + 127) // 128 * ((K + 127) // 128) * 512 if R > 0 and K > 0 and K % 32 == 0 else 0
 
 
 def qmoe_mx_quantize(x, fmt=MXFP8, codes=None, scales=None):
     """(codes, scales) of x [M, K] (fp16, bf16 or fp32) in MXFP8 or MXFP4."""
-    M, K = _mx_rows(x, "qmoe_mx_quantize", tuple(_MX_DT))
+    M, K = _mx_rows(x, "qmoe_mx_quantize")
+    dt = _MX_DT.get(x.dtype)
+    if dt is None:
+        _bad("qmoe_mx_quantize", "unsupported input type %s" % x.dtype)
     codes, scales = _mx_out(M, K, fmt, x, codes, scales, "qmoe_mx_quantize")
-    _mx_call(x, lib().qmoe_mx_quantize, "qmoe_mx_quantize", _p(x), _MX_DT[x.dtype], fmt, M, K, _p(codes), _p(scales))
+    _mx_call(x, lib().qmoe_mx_quantize, "qmoe_mx_quantize", x.data_ptr(), dt, fmt, M, K, codes.data_ptr(),
+             scales.data_ptr())
     return codes, scales
 
 
 def qmoe_mx_dequant(codes, scales, fmt, dtype=torch.bfloat16, out=None):
     """[M, K] values (fp16, bf16 or fp32) of an MX tensor."""
     M, K = _mx_tensor(codes, scales, fmt, "qmoe_mx_dequant")
-    if dtype not in _MX_DT:
+    dt = _MX_DT.get(dtype)
+    if dt is None:
         _bad("qmoe_mx_dequant", "unsupported output type %s" % dtype)
     if out is None:
-        out = torch.empty((M, K), dtype=dtype, device=codes.device)
+        out = codes.new_empty((M, K), dtype=dtype)
     else:
-        _mx_same(out, codes, dtype, M * K, "qmoe_mx_dequant", "out")
-    _mx_call(codes, lib().qmoe_mx_dequant, "qmoe_mx_dequant", _p(codes), _p(scales), fmt, M, K, _p(out), _MX_DT[dtype])
+        _mx_same(out, codes.get_device(), dtype, M * K, "qmoe_mx_dequant", "out")
+    _mx_call(codes, lib().qmoe_mx_dequant, "qmoe_mx_dequant", codes.data_ptr(), scales.data_ptr(), fmt, M, K,
+             out.data_ptr(), dt)
     return out
 
 
@@ -453,18 +467,22 @@ def qmoe_rmsnorm_mx(x, residual=None, weight=None, eps=1e-6, fmt=MXFP8, residual
     or MXFP4; residual_out = x + residual (a new tensor unless given; it may be
     x or residual itself).  Without a residual it is None unless given."""
     where = "qmoe_rmsnorm_mx"
-    T, H = _mx_rows(x, where, (torch.float16, torch.bfloat16))
+    T, H = _mx_rows(x, where)
+    dt, dev = x.dtype, x.get_device()
+    if dt != torch.float16 and dt != torch.bfloat16:
+        _bad(where, "unsupported input type %s" % dt)
+    codes, scales = _mx_out(T, H, fmt, x, codes, scales, where)
+    rp = wp = op = None
     if residual is not None:
-        _mx_same(residual, x, x.dtype, T * H, where, "residual")
+        rp = _mx_same(residual, dev, dt, T * H, where, "residual")
         if residual_out is None:
             residual_out = torch.empty_like(x)
     if residual_out is not None:
-        _mx_same(residual_out, x, x.dtype, T * H, where, "residual_out")
+        op = _mx_same(residual_out, dev, dt, T * H, where, "residual_out")
     if weight is not None:
-        _mx_same(weight, x, x.dtype, H, where, "weight")
-    codes, scales = _mx_out(T, H, fmt, x, codes, scales, where)
-    _mx_call(x, lib().qmoe_rmsnorm_mx, where, _p(x), _p(residual), _p(weight), _MX_DT[x.dtype], T, H, float(eps), fmt,
-             _p(residual_out), _p(codes), _p(scales))
+        wp = _mx_same(weight, dev, dt, H, where, "weight")
+    _mx_call(x, lib().qmoe_rmsnorm_mx, where, x.data_ptr(), rp, wp, _MX_DT[dt], T, H, float(eps), fmt, op,
+             codes.data_ptr(), scales.data_ptr())
     return codes, scales, residual_out
 
 
@@ -475,38 +493,41 @@ def qmoe_mx_matmul(x_codes, x_scales, x_fmt, w_codes, w_scales, dtype=torch.bflo
     where = "qmoe_mx_matmul"
     M, K = _mx_tensor(x_codes, x_scales, x_fmt, where)
     N, KW = _mx_tensor(w_codes, w_scales, MXFP4, where)
-    if K != KW or w_codes.device != x_codes.device:
+    dev = x_codes.get_device()
+    if K != KW or w_codes.get_device() != dev:
         _bad(where, "x has %d columns on %s, W has %d on %s" % (K, x_codes.device, KW, w_codes.device))
-    if dtype not in _MX_DT:
+    dt = _MX_DT.get(dtype)
+    if dt is None:
         _bad(where, "unsupported output type %s" % dtype)
     if out is None:
-        out = torch.empty((M, N), dtype=dtype, device=x_codes.device)
+        out = x_codes.new_empty((M, N), dtype=dtype)
     else:
-        _mx_same(out, x_codes, dtype, M * N, where, "out")
-    if status is not None:
-        _mx_same(status, x_codes, torch.int32, 1, where, "status")
-    _mx_call(x_codes, lib().qmoe_mx_matmul, where, _p(x_codes), _p(x_scales), x_fmt, _p(w_codes), _p(w_scales), M, N, K,
-             _p(out), _MX_DT[dtype], _p(status))
+        _mx_same(out, dev, dtype, M * N, where, "out")
+    sp = None if status is None else _mx_same(status, dev, torch.int32, 1, where, "status")
+    _mx_call(x_codes, lib().qmoe_mx_matmul, where, x_codes.data_ptr(), x_scales.data_ptr(), x_fmt, w_codes.data_ptr(),
+             w_scales.data_ptr(), M, N, K, out.data_ptr(), dt, sp)
     return out
 
 
 def qmoe_mx_tile_scales(scales_rowmajor):
     """Row-major scale bytes [R, K/32] (as checkpoints store them) -> tiles."""
-    R, nb = _mx_rows(scales_rowmajor, "qmoe_mx_tile_scales", (torch.uint8,))
+    where = "qmoe_mx_tile_scales"
+    R, nb = _mx_rows(scales_rowmajor, where)
     n = qmoe_mx_scale_bytes(R, 32 * nb)
-    if n == 0:
-        _bad("qmoe_mx_tile_scales", "empty scales")
-    out = torch.empty(n, dtype=torch.uint8, device=scales_rowmajor.device)
-    _mx_call(out, lib().qmoe_mx_tile_scales, "qmoe_mx_tile_scales", _p(scales_rowmajor), R, 32 * nb, _p(out))
+    if n == 0 or scales_rowmajor.dtype != torch.uint8:
+        _bad(where, "wants uint8 scales [R, K/32]")
+    out = scales_rowmajor.new_empty(n)
+    _mx_call(out, lib().qmoe_mx_tile_scales, where, scales_rowmajor.data_ptr(), R, 32 * nb, out.data_ptr())
     return out
 
 
 def qmoe_mx_untile_scales(scales, R, K):
     """Scale tiles of an MX tensor [R, K] -> row-major bytes [R, K/32]."""
+    where = "qmoe_mx_untile_scales"
     n = qmoe_mx_scale_bytes(R, K)
     if n == 0 or not scales.is_cuda:
-        _bad("qmoe_mx_untile_scales", "wants CUDA scale tiles of an MX tensor, got [%d, %d]" % (R, K))
-    _mx_same(scales, scales, torch.uint8, n, "qmoe_mx_untile_scales", "scales")
-    out = torch.empty((R, K // 32), dtype=torch.uint8, device=scales.device)
-    _mx_call(out, lib().qmoe_mx_untile_scales, "qmoe_mx_untile_scales", _p(scales), R, K, _p(out))
+        _bad(where, "wants CUDA scale tiles of an MX tensor, got [%d, %d]" % (R, K))
+    _mx_same(scales, scales.get_device(), torch.uint8, n, where, "scales")
+    out = scales.new_empty((R, K // 32))
+    _mx_call(out, lib().qmoe_mx_untile_scales, where, scales.data_ptr(), R, K, out.data_ptr())
     return out

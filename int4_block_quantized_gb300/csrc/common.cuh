@@ -235,6 +235,45 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// The pair's forms (cta_group::2): two CTAs of a cluster, the even rank leads.
+__device__ __forceinline__ void tmem_alloc2(uint32_t* dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst_smem)), "r"(ncols)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish2() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// the same barrier in both CTAs
+__device__ __forceinline__ void mma_commit2_elect(uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+// shared::cluster address of the same object in CTA `rank`
+__device__ __forceinline__ uint32_t peer_u32(const void* local, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(local)), "r"(rank));
+  return r;
+}
+// load into this CTA's shared memory, completion counted on a barrier of the
+// pair's leader (bar: its shared::cluster address)
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const void* tmap, int c0, int c1, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 // 1 in the lane that elect.sync names (the same one every time), else 0.
 __device__ __forceinline__ uint32_t elect_lane() {
   uint32_t e;
@@ -245,33 +284,60 @@ __device__ __forceinline__ uint32_t elect_lane() {
 // descriptors, scales (e8m0) in tensor memory, by the lane of a converged warp
 // whose `e` (elect_lane) is 1.  kind::mxf4: e2m1 x e2m1, 64 k, two blocks of 32 per
 // instruction; kind::mxf8f6f4: 8-bit containers, 32 k, one block.
+template <int CG>
 __device__ __forceinline__ void mma_mxf4(uint32_t e, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                                uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p, e;\n setp.ne.b32 e, %7, 0;\n setp.ne.b32 p, %6, 0;\n"
-      " @e tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(
-          d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(e)
-      : "memory");
+  if constexpr (CG == 1)
+    asm volatile(
+        "{\n .reg .pred p, e;\n setp.ne.b32 e, %7, 0;\n setp.ne.b32 p, %6, 0;\n"
+        " @e tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(e)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p, e;\n setp.ne.b32 e, %7, 0;\n setp.ne.b32 p, %6, 0;\n"
+        " @e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(e)
+        : "memory");
 }
+template <int CG>
 __device__ __forceinline__ void mma_mxf8f6f4(uint32_t e, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                                    uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p, e;\n setp.ne.b32 e, %7, 0;\n setp.ne.b32 p, %6, 0;\n"
-      " @e tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(
-          d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(e)
-      : "memory");
+  if constexpr (CG == 1)
+    asm volatile(
+        "{\n .reg .pred p, e;\n setp.ne.b32 e, %7, 0;\n setp.ne.b32 p, %6, 0;\n"
+        " @e tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(e)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p, e;\n setp.ne.b32 e, %7, 0;\n setp.ne.b32 p, %6, 0;\n"
+        " @e tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(e)
+        : "memory");
 }
 // 32 rows x 16 bytes of shared memory into four columns of tensor memory,
 // repeated in all four lane quadrants (a 128 x 4 tile of scales); ordered
 // before the tcgen05.mma that the same lane issues next.
+// CG = 2: in both CTAs of the pair, each from its own shared memory.
+template <int CG>
 __device__ __forceinline__ void tmem_cp_scales(uint32_t e, uint32_t taddr, uint64_t desc) {
-  asm volatile(
-      "{\n .reg .pred e;\n setp.ne.b32 e, %2, 0;\n"
-      " @e tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n}" ::"r"(taddr),
-      "l"(desc), "r"(e)
-      : "memory");
+  if constexpr (CG == 1)
+    asm volatile(
+        "{\n .reg .pred e;\n setp.ne.b32 e, %2, 0;\n"
+        " @e tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n}" ::"r"(taddr),
+        "l"(desc), "r"(e)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred e;\n setp.ne.b32 e, %2, 0;\n"
+        " @e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n}" ::"r"(taddr),
+        "l"(desc), "r"(e)
+        : "memory");
 }
 // Unswizzled descriptor of 8-row x 16-byte groups 128 bytes apart.
 __device__ __forceinline__ uint64_t rows16_desc(uint32_t smem_addr) {

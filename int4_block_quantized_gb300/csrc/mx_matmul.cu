@@ -33,12 +33,12 @@ struct MmParams {
   int split;                     // CTAs of a cluster that share a tile's K
 };
 
-template <int XF, int BN>
+template <int XF, int BN, int CG>
 struct MmPlan {
   static constexpr int kStageK = XF == kMxfp4 ? 256 : 128;  // elements
   static constexpr int kWords = kStageK / 128;              // scale tiles of a stage along K
   static constexpr int kTokSf = (BN + 127) / 128;           // scale tiles of a stage along the tokens
-  static constexpr uint32_t kA = 128 * 128, kB = BN * 128;
+  static constexpr uint32_t kA = 128 * 128, kB = BN / CG * 128;  // one CTA's share
   // bytes that a weight copy reports: those read, also where the codes are widened
   static constexpr uint32_t kTxA = XF == kMxfp4 ? kA : kA / 2;
   static constexpr uint32_t kSf = 512 * kWords * (1 + kTokSf);
@@ -78,6 +78,12 @@ __device__ __forceinline__ void mm_store(const MmParams& p, size_t i, float v) {
   else static_cast<uint16_t*>(p.y)[i] = p.y_dtype == QMOE_BF16 ? Half<__nv_bfloat16>::from_float(v) : Half<__half>::from_float(v);
 }
 
+template <int CG>
+__device__ __forceinline__ void mm_commit(uint64_t* bar) {
+  if (CG == 1) mma_commit_elect(bar);
+  else mma_commit2_elect(bar);
+}
+
 // Tile t of the grid: groups of 8 row tiles, so that the tiles in flight share
 // weights and tokens in L2.
 __device__ __forceinline__ void mm_tile(const MmParams& p, int t, int& rt, int& tt) {
@@ -90,11 +96,12 @@ __device__ __forceinline__ void mm_tile(const MmParams& p, int t, int& rt, int& 
 // FILL (MXFP8 x only): the TMA copy that widens e2m1 codes wants rows of a
 // multiple of 128 codes on 32-byte boundaries; other weights are read and
 // spread by four warps.
-template <int XF, int BN, bool FILL>
+template <int XF, int BN, int CG, bool FILL>
 __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
     mx_matmul_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
+                     const __grid_constant__ CUtensorMap tm_ws, const __grid_constant__ CUtensorMap tm_xs,
                      const MmParams p) {
-  using P = MmPlan<XF, BN>;
+  using P = MmPlan<XF, BN, CG>;
   constexpr int S = P::kStages;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -116,18 +123,24 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_free[b], 4);
+      mbar_init(&acc_free[b], 4 * CG);
     }
     mbar_init(fin, 1);
     *s_abort = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
-    tmem_alloc(s_tmem, 512);
-    tmem_relinquish();
+    if (CG == 1) {
+      tmem_alloc(s_tmem, 512);
+      tmem_relinquish();
+    } else {
+      tmem_alloc2(s_tmem, 512);
+      tmem_relinquish2();
+    }
   }
   tc_fence_before();
   __syncthreads();
+  if (CG == 2) cluster_sync_all();  // the pair's barriers are set up
   tc_fence_after();
   // all 512 columns are this CTA's, so they start at 0
   constexpr uint32_t tmem = 0;
@@ -137,8 +150,9 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
 
   // this CTA's tiles and its share [c0, c1) of their stages along K
   const int rank = p.split > 1 ? (int)cluster_ctarank() : 0;
+  const int half = CG == 2 ? (int)cluster_ctarank() : 0;  // of the pair's rows and tokens
   const int tiles = p.row_tiles * p.tok_tiles;
-  const int first = blockIdx.x / p.split, step = p.split > 1 ? tiles : gridDim.x;
+  const int first = blockIdx.x / (CG * p.split), step = p.split > 1 ? tiles : gridDim.x / CG;
   const int chunks = (p.K + P::kStageK - 1) / P::kStageK;
   const int c0 = (int)((long long)chunks * rank / p.split), c1 = (int)((long long)chunks * (rank + 1) / p.split);
 
@@ -158,6 +172,22 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
           const int q0 = c * P::kWords, nq = min(P::kWords, p.kt - q0);
           // scale tiles of the tokens: those that exist (128-row tiles m0 / 128 ..)
           const int t0 = m0 >> 7, nt = min(P::kTokSf, ((p.M + 127) >> 7) - t0);
+          if constexpr (CG == 2) {
+            // both CTAs report to the leader; scale tiles that do not exist read as zeros
+            const uint32_t bar = peer_u32(&full[s], 0);
+            if (half == 0) mbar_arrive_expect_tx(&full[s], 2 * (P::kTxA + P::kB + P::kSf));
+            const int r = rt * 2 + half;
+            tma_load_2d_pair(st, &tm_w, c * 128, r * 128, bar);
+            tma_load_2d_pair(st + P::kA, &tm_x, c * 128, m0 + half * (BN / 2), bar);
+            tma_load_2d_pair(sf, &tm_ws, 0, r * p.kt + q0, bar);
+            for (int i = 0; i < P::kTokSf; ++i)
+              tma_load_2d_pair(sf + 512 * P::kWords * (1 + i), &tm_xs, 0, (t0 + i) * p.kt + q0, bar);
+            if (++s == S) {
+              s = 0;
+              ph ^= 1u;
+            }
+            continue;
+          }
           mbar_arrive_expect_tx(&full[s], (FILL ? 0u : P::kTxA) + P::kB + 512u * nq * (1 + nt));
           if (!FILL) tma_load_2d(st, &tm_w, c * 128, rt * 128, &full[s]);
           tma_load_2d(st + P::kA, &tm_x, c * 128, m0, &full[s]);
@@ -170,11 +200,11 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
           }
         }
       }
-      if (*s_abort)  // let the copies in flight land before the CTA exits
+      if (*s_abort && half == 0)  // let the copies in flight land before the CTA exits
         for (int i = 0; i < S; ++i)
           if (it > i) mbar_wait(&full[i], ((it - 1 - i) / S) & 1, nullptr);
     }
-  } else if (warp == 1) {
+  } else if (warp == 1 && half == 0) {
     // --------------------------------------------------------------- MMAs
     int n = 0, s = 0;
     uint32_t ph = 0;
@@ -203,10 +233,10 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
 #pragma unroll
         for (int q = 0; q < P::kWords; ++q) {
           if (q * 128 >= left) break;
-          tmem_cp_scales(el, tmem + P::kSfa + 4 * q, rows16_desc(sf + 512 * q));
+          tmem_cp_scales<CG>(el, tmem + P::kSfa + 4 * q, rows16_desc(sf + 512 * q));
 #pragma unroll
           for (int i = 0; i < P::kTokSf; ++i)
-            tmem_cp_scales(el, tmem + P::kSfb + 4 * (q * P::kTokSf + i),
+            tmem_cp_scales<CG>(el, tmem + P::kSfb + 4 * (q * P::kTokSf + i),
                                  rows16_desc(sf + 512 * (P::kWords * (1 + i) + q)));
         }
         const uint64_t da = sw128_desc(st), db = sw128_desc(st + P::kA);
@@ -215,25 +245,25 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
           if (j * (P::kStageK / 4) >= left) break;
           const uint32_t acc = (c > c0 || j > 0) ? 1u : 0u;
           if (XF == kMxfp4)
-            mma_mxf4(el, d, da + 2 * j, db + 2 * j, idesc_mx(128, BN, 1, 1, 2 * (j & 1), 2 * (j & 1)),
+            mma_mxf4<CG>(el, d, da + 2 * j, db + 2 * j, idesc_mx(128 * CG, BN, 1, 1, 2 * (j & 1), 2 * (j & 1)),
                            tmem + P::kSfa + 4 * (j >> 1), sfb + 4 * P::kTokSf * (j >> 1), acc);
           else
-            mma_mxf8f6f4(el, d, da + 2 * j, db + 2 * j, idesc_mx(128, BN, 5, 0, j, j), tmem + P::kSfa, sfb, acc);
+            mma_mxf8f6f4<CG>(el, d, da + 2 * j, db + 2 * j, idesc_mx(128 * CG, BN, 5, 0, j, j), tmem + P::kSfa, sfb, acc);
         }
         issued = true;
-        mma_commit_elect(&empty[s]);
+        mm_commit<CG>(&empty[s]);
         if (++s == S) {
           s = 0;
           ph ^= 1u;
         }
       }
-      if (ok) mma_commit_elect(&acc_full[b]);
+      if (ok) mm_commit<CG>(&acc_full[b]);
     }
     if (issued) {  // all MMAs have finished before tensor memory is freed
-      mma_commit_elect(fin);
+      mm_commit<CG>(fin);
       mbar_wait(fin, 0, nullptr);
     }
-  } else if (warp < 6) {
+  } else if (warp >= 2 && warp < 6) {
     // ------------------------------------------------------------- outputs
     const int qd = warp & 3, row = qd * 32 + lane;
     int n = 0;
@@ -244,7 +274,7 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
       if (!mm_wait(&acc_full[b], (n >> 1) & 1, p.status, s_abort)) break;
       tc_fence_after();
       const uint32_t d = tmem + ((uint32_t)(qd * 32) << 16) + (b ? P::kAcc1 : 0);
-      const int m0 = tt * BN, nn = rt * 128 + row;
+      const int m0 = tt * BN, nn = (rt * CG + half) * 128 + row;
       constexpr int W = BN < 32 ? BN : 32, C = BN / W;
       if (p.split == 1) {
         for (int i = 0; i < C; ++i) {
@@ -256,7 +286,10 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
           if (P::kOverlap && i == 0) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&acc_free[0]);
+            if (lane == 0) {
+              if (CG == 1) mbar_arrive(&acc_free[0]);
+              else mbar_arrive_cluster(peer_u32(&acc_free[0], 0));
+            }
           }
           if (nn < p.N) {
 #pragma unroll
@@ -267,7 +300,10 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
         if (!P::kOverlap) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&acc_free[b]);
+          if (lane == 0) {
+            if (CG == 1) mbar_arrive(&acc_free[b]);
+            else mbar_arrive_cluster(peer_u32(&acc_free[b], 0));
+          }
         }
       }
     }
@@ -355,16 +391,19 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (CG == 2) cluster_sync_all();  // neither CTA leaves while the other may use its memory
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    if (CG == 1) tmem_dealloc(tmem, 512);
+    else tmem_dealloc2(tmem, 512);
   }
 }
 
-template <int XF, int BN, bool FILL>
+template <int XF, int BN, int CG, bool FILL>
 static cudaError_t launch_mm(MmParams p, const uint8_t* xc, cudaStream_t st) {
-  using P = MmPlan<XF, BN>;
+  using P = MmPlan<XF, BN, CG>;
   static_assert(P::kTotal <= kMmSmem && P::kCols0 <= 512, "plan");
+  p.row_tiles = (p.N + 128 * CG - 1) / (128 * CG);
   p.tok_tiles = (p.M + BN - 1) / BN;
   const long long tiles = (long long)p.row_tiles * p.tok_tiles;
   if (tiles > (1LL << 27)) return cudaErrorInvalidValue;
@@ -381,7 +420,7 @@ static cudaError_t launch_mm(MmParams p, const uint8_t* xc, cudaStream_t st) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   };
   const uint64_t half = p.K / 2;
-  if (!map(&tx, xc, CU_TENSOR_MAP_DATA_TYPE_UINT8, XF == kMxfp4 ? half : p.K, p.M, XF == kMxfp4 ? half : p.K, BN))
+  if (!map(&tx, xc, CU_TENSOR_MAP_DATA_TYPE_UINT8, XF == kMxfp4 ? half : p.K, p.M, XF == kMxfp4 ? half : p.K, BN / CG))
     return cudaErrorNotSupported;
   if (FILL) {
     tw = tx;
@@ -390,15 +429,27 @@ static cudaError_t launch_mm(MmParams p, const uint8_t* xc, cudaStream_t st) {
   } else {
     if (!map(&tw, p.wc, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, p.K, p.N, half, 128)) return cudaErrorNotSupported;
   }
+  CUtensorMap tws = tw, txs = tx;
+  if (CG == 2) {  // scale tiles as rows of 128 words
+    const cuuint32_t box[2] = {128, (cuuint32_t)P::kWords};
+    const cuuint64_t stride[1] = {512};
+    const cuuint64_t dw[2] = {128, (cuuint64_t)((p.N + 127) / 128) * p.kt}, dx[2] = {128, (cuuint64_t)((p.M + 127) / 128) * p.kt};
+    auto smap = [&](CUtensorMap* m, const void* base, const cuuint64_t* dims) {
+      return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims, stride, box, es,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    if (!smap(&tws, p.ws, dw) || !smap(&txs, p.xs, dx)) return cudaErrorNotSupported;
+  }
   // few tiles: a cluster of up to 8 CTAs shares a tile's K
   const int sms = device_sm_count(), chunks = (p.K + P::kStageK - 1) / P::kStageK;
   p.split = 1;
-  while (p.split < 8 && 2 * p.split <= chunks && tiles * p.split * 2 <= sms) p.split *= 2;
-  auto kernel = mx_matmul_kernel<XF, BN, FILL>;
+  while (CG == 1 && p.split < 8 && 2 * p.split <= chunks && tiles * p.split * 2 <= sms) p.split *= 2;
+  auto kernel = mx_matmul_kernel<XF, BN, CG, FILL>;
   cudaError_t err = ensure_smem(kernel, P::kTotal);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.split > 1 ? tiles * p.split : tiles < sms ? tiles : sms));
+  cfg.gridDim = dim3((unsigned)(p.split > 1 ? tiles * p.split : CG * (tiles < sms / CG ? tiles : sms / CG)));
   cfg.blockDim = dim3(FILL ? kMmFillThreads : kMmThreads);
   cfg.dynamicSmemBytes = P::kTotal;
   cfg.stream = st;
@@ -406,21 +457,24 @@ static cudaError_t launch_mm(MmParams p, const uint8_t* xc, cudaStream_t st) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = p.split;
+  attr[1].val.clusterDim.x = p.split * CG;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, tw, tx, p);
+  return cudaLaunchKernelEx(&cfg, kernel, tw, tx, tws, txs, p);
 }
 
 template <int XF, bool FILL>
 static cudaError_t launch_mm_bn(const MmParams& p, const uint8_t* xc, cudaStream_t st) {
-  if (p.M <= 16) return launch_mm<XF, 16, FILL>(p, xc, st);
-  if (p.M <= 32) return launch_mm<XF, 32, FILL>(p, xc, st);
-  if (p.M <= 64) return launch_mm<XF, 64, FILL>(p, xc, st);
+  if (p.M <= 16) return launch_mm<XF, 16, 1, FILL>(p, xc, st);
+  if (p.M <= 32) return launch_mm<XF, 32, 1, FILL>(p, xc, st);
+  if (p.M <= 64) return launch_mm<XF, 64, 1, FILL>(p, xc, st);
   // 256-token tiles once they fill the card
-  if ((long long)p.row_tiles * ((p.M + 255) / 256) >= device_sm_count()) return launch_mm<XF, 256, FILL>(p, xc, st);
-  return launch_mm<XF, 128, FILL>(p, xc, st);
+  if ((long long)((p.N + 127) / 128) * ((p.M + 255) / 256) >= device_sm_count()) {
+    if constexpr (FILL) return launch_mm<XF, 256, 1, FILL>(p, xc, st);
+    else return launch_mm<XF, 256, 2, false>(p, xc, st);
+  }
+  return launch_mm<XF, 128, 1, FILL>(p, xc, st);
 }
 
 cudaError_t launch_mx_matmul(const uint8_t* xc, const uint8_t* xs, int x_format, const uint8_t* wc, const uint8_t* ws,
@@ -435,7 +489,6 @@ cudaError_t launch_mx_matmul(const uint8_t* xc, const uint8_t* xs, int x_format,
   p.N = N;
   p.K = K;
   p.y_dtype = y_dtype;
-  p.row_tiles = (N + 127) / 128;
   p.kt = (K + 127) / 128;
   if (x_format == kMxfp4) return launch_mm_bn<kMxfp4, false>(p, xc, st);
   if (K % 128 || (reinterpret_cast<uintptr_t>(wc) & 31)) return launch_mm_bn<kMxfp8, true>(p, xc, st);

@@ -230,6 +230,14 @@ def test_matmul_tiles(M, N, K, xf):
 
 
 @pytest.mark.parametrize("xf", FMT)
+@pytest.mark.parametrize("M,N,K", [(2600, 1900, 256), (2817, 1793, 128), (1281, 4001, 640), (5000, 1100, 416),
+                                   (300, 9900, 32), (2561, 2050, 1152)])
+def test_matmul_many_tiles(M, N, K, xf):
+    """More tiles than SMs: several per CTA (or pair of CTAs), ragged last ones."""
+    run_product(M, N, K, xf, (torch.float32, torch.bfloat16)[M % 2], M + N + K)
+
+
+@pytest.mark.parametrize("xf", FMT)
 def test_matmul_scale_extremes(xf):
     """Scales across many binades between blocks, zero codes, the smallest scale."""
     M, N, K = 20, 150, 512
