@@ -19,8 +19,8 @@
 
 namespace qmoe {
 
-constexpr int kMmThreads = 192;       // warp 0 copies, warp 1 issues MMAs, warps 2-5 write y
-constexpr int kMmFillThreads = 320;   // + warps 6-9: weights by loads and stores (see FILL)
+constexpr int kMmThreads = 224;       // warps 0 and 6 copy, warp 1 issues MMAs, warps 2-5 write y
+constexpr int kMmFillThreads = 352;   // + warps 7-10: weights by loads and stores (see FILL)
 constexpr uint32_t kMmSmem = 232448;  // 227 KB
 constexpr uint32_t kMmBars = 1024;
 
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
 
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(&full[s], FILL ? 5 : 1);
+      mbar_init(&full[s], FILL ? 6 : 2);
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -156,54 +156,59 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
   const int chunks = (p.K + P::kStageK - 1) / P::kStageK;
   const int c0 = (int)((long long)chunks * rank / p.split), c1 = (int)((long long)chunks * (rank + 1) / p.split);
 
-  if (warp == 0) {
-    // ------------------------------------------------------------- copies
-    if (lane == 0) {
-      int it = 0, s = 0;
-      uint32_t ph = 0;
-      for (int t = first; t < tiles && !*s_abort; t += step) {
-        int rt, tt;
-        mm_tile(p, t, rt, tt);
-        const int m0 = tt * BN;
-        for (int c = c0; c < c1; ++c, ++it) {
-          if (it >= S && !mm_wait(&empty[s], ph ^ 1u, p.status, s_abort)) break;
+  if (warp == 0 || warp == 6) {
+    // ------------------------------ copies: warp 0 the codes, warp 6 the scales
+    int it = 0, s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    const uint32_t el = elect_lane();
+    for (int t = first; t < tiles && ok; t += step) {
+      int rt, tt;
+      mm_tile(p, t, rt, tt);
+      const int m0 = tt * BN, r = rt * CG + half;
+      // scale tiles of the tokens: those that exist (128-row tiles m0 / 128 ..)
+      const int t0 = m0 >> 7, nt = min(P::kTokSf, ((p.M + 127) >> 7) - t0);
+      for (int c = c0; c < c1; ++c, ++it) {
+        if (it >= S) ok = mm_wait(&empty[s], ph ^ 1u, p.status, s_abort);
+        if (!ok) break;
+        if (el) {
+          const int q0 = c * P::kWords, nq = min(P::kWords, p.kt - q0);
           uint8_t* st = ring + s * P::kAb;
           uint8_t* sf = sfring + s * P::kSf;
-          const int q0 = c * P::kWords, nq = min(P::kWords, p.kt - q0);
-          // scale tiles of the tokens: those that exist (128-row tiles m0 / 128 ..)
-          const int t0 = m0 >> 7, nt = min(P::kTokSf, ((p.M + 127) >> 7) - t0);
           if constexpr (CG == 2) {
             // both CTAs report to the leader; scale tiles that do not exist read as zeros
             const uint32_t bar = peer_u32(&full[s], 0);
-            if (half == 0) mbar_arrive_expect_tx(&full[s], 2 * (P::kTxA + P::kB + P::kSf));
-            const int r = rt * 2 + half;
-            tma_load_2d_pair(st, &tm_w, c * 128, r * 128, bar);
-            tma_load_2d_pair(st + P::kA, &tm_x, c * 128, m0 + half * (BN / 2), bar);
-            tma_load_2d_pair(sf, &tm_ws, 0, r * p.kt + q0, bar);
-            for (int i = 0; i < P::kTokSf; ++i)
-              tma_load_2d_pair(sf + 512 * P::kWords * (1 + i), &tm_xs, 0, (t0 + i) * p.kt + q0, bar);
-            if (++s == S) {
-              s = 0;
-              ph ^= 1u;
+            if (warp == 0) {
+              if (half == 0) mbar_arrive_expect_tx(&full[s], 2 * (P::kTxA + P::kB));
+              tma_load_2d_pair(st, &tm_w, c * 128, r * 128, bar);
+              tma_load_2d_pair(st + P::kA, &tm_x, c * 128, m0 + half * (BN / 2), bar);
+            } else {
+              if (half == 0) mbar_arrive_expect_tx(&full[s], 2 * P::kSf);
+              tma_load_2d_pair(sf, &tm_ws, 0, r * p.kt + q0, bar);
+              for (int i = 0; i < P::kTokSf; ++i)
+                tma_load_2d_pair(sf + 512 * P::kWords * (1 + i), &tm_xs, 0, (t0 + i) * p.kt + q0, bar);
             }
-            continue;
-          }
-          mbar_arrive_expect_tx(&full[s], (FILL ? 0u : P::kTxA) + P::kB + 512u * nq * (1 + nt));
-          if (!FILL) tma_load_2d(st, &tm_w, c * 128, rt * 128, &full[s]);
-          tma_load_2d(st + P::kA, &tm_x, c * 128, m0, &full[s]);
-          bulk_g2s(sf, p.ws + ((size_t)rt * p.kt + q0) * 512, 512u * nq, &full[s]);
-          for (int i = 0; i < nt; ++i)
-            bulk_g2s(sf + 512 * P::kWords * (1 + i), p.xs + ((size_t)(t0 + i) * p.kt + q0) * 512, 512u * nq, &full[s]);
-          if (++s == S) {
-            s = 0;
-            ph ^= 1u;
+          } else if (warp == 0) {
+            mbar_arrive_expect_tx(&full[s], (FILL ? 0u : P::kTxA) + P::kB);
+            if (!FILL) tma_load_2d(st, &tm_w, c * 128, rt * 128, &full[s]);
+            tma_load_2d(st + P::kA, &tm_x, c * 128, m0, &full[s]);
+          } else {
+            mbar_arrive_expect_tx(&full[s], 512u * nq * (1 + nt));
+            bulk_g2s(sf, p.ws + ((size_t)rt * p.kt + q0) * 512, 512u * nq, &full[s]);
+            for (int i = 0; i < nt; ++i)
+              bulk_g2s(sf + 512 * P::kWords * (1 + i), p.xs + ((size_t)(t0 + i) * p.kt + q0) * 512, 512u * nq, &full[s]);
           }
         }
+        __syncwarp();
+        if (++s == S) {
+          s = 0;
+          ph ^= 1u;
+        }
       }
-      if (*s_abort && half == 0)  // let the copies in flight land before the CTA exits
-        for (int i = 0; i < S; ++i)
-          if (it > i) mbar_wait(&full[i], ((it - 1 - i) / S) & 1, nullptr);
     }
+    if (*s_abort && half == 0 && lane == 0)  // let the copies in flight land before the CTA exits
+      for (int i = 0; i < S; ++i)
+        if (it > i) mbar_wait(&full[i], ((it - 1 - i) / S) & 1, nullptr);
   } else if (warp == 1 && half == 0) {
     // --------------------------------------------------------------- MMAs
     int n = 0, s = 0;
@@ -250,8 +255,8 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
           else
             mma_mxf8f6f4<CG>(el, d, da + 2 * j, db + 2 * j, idesc_mx(128 * CG, BN, 5, 0, j, j), tmem + P::kSfa, sfb, acc);
         }
-        issued = true;
         mm_commit<CG>(&empty[s]);
+        issued = true;
         if (++s == S) {
           s = 0;
           ph ^= 1u;
@@ -309,7 +314,7 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
     }
   } else if (FILL) {
     // -------------------------------------- weights of ragged rows (MXFP8 x)
-    const int r = tid - 192;  // row of the tile
+    const int r = tid - kMmThreads;  // row of the tile
     int it = 0, s = 0;
     uint32_t ph = 0;
     bool ok = true;
