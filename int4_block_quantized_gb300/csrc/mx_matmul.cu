@@ -19,8 +19,8 @@
 
 namespace qmoe {
 
-constexpr int kMmThreads = 224;       // warps 0 and 6 copy, warp 1 issues MMAs, warps 2-5 write y
-constexpr int kMmFillThreads = 352;   // + warps 7-10: weights by loads and stores (see FILL)
+constexpr int kMmThreads = 352;       // warps 0 and 6 copy, warp 1 issues MMAs, warps 2-5 and 7-10 write y
+constexpr int kMmFillThreads = 480;   // + warps 11-14: weights by loads and stores (see FILL)
 constexpr uint32_t kMmSmem = 232448;  // 227 KB
 constexpr uint32_t kMmBars = 1024;
 
@@ -78,6 +78,37 @@ __device__ __forceinline__ void mm_store(const MmParams& p, size_t i, float v) {
   else static_cast<uint16_t*>(p.y)[i] = p.y_dtype == QMOE_BF16 ? Half<__nv_bfloat16>::from_float(v) : Half<__half>::from_float(v);
 }
 
+// W tokens' results of one output column: y[i], y[i + N], ... , the first `rows` of them.
+template <int W>
+__device__ __forceinline__ void mm_store_cols(const MmParams& p, size_t i, int rows, const uint32_t (&v)[W]) {
+  const size_t N = p.N;
+  if (p.y_dtype == QMOE_F32) {
+    uint32_t* y = static_cast<uint32_t*>(p.y) + i;
+#pragma unroll
+    for (int j = 0; j < W; ++j, y += N)
+      if (j < rows) *y = v[j];
+    return;
+  }
+  uint16_t* y = static_cast<uint16_t*>(p.y) + i;
+  const bool bf = p.y_dtype == QMOE_BF16;
+#pragma unroll
+  for (int j = 0; j < W; j += 2) {
+    const float a = __uint_as_float(v[j]), b = __uint_as_float(v[j + 1]);
+    uint32_t u;
+    if (bf) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+      u = *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+      const __half2 h = __floats2half2_rn(a, b);
+      u = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    if (j < rows) *y = (uint16_t)(u & 0xffffu);
+    y += N;
+    if (j + 1 < rows) *y = (uint16_t)(u >> 16);
+    y += N;
+  }
+}
+
 template <int CG>
 __device__ __forceinline__ void mm_commit(uint64_t* bar) {
   if (CG == 1) mma_commit_elect(bar);
@@ -123,7 +154,7 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_free[b], 4 * CG);
+      mbar_init(&acc_free[b], 8 * CG);
     }
     mbar_init(fin, 1);
     *s_abort = 0;
@@ -268,9 +299,11 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
       mm_commit<CG>(fin);
       mbar_wait(fin, 0, nullptr);
     }
-  } else if (warp >= 2 && warp < 6) {
+  } else if (warp >= 2 && warp < 11) {
     // ------------------------------------------------------------- outputs
-    const int qd = warp & 3, row = qd * 32 + lane;
+    // Two warps per lane quadrant take the accumulator's chunks in turn (one
+    // warp needed longer for 256 tokens than the MMAs of 2048 k).
+    const int qd = warp & 3, row = qd * 32 + lane, set = warp > 6;
     int n = 0;
     for (int t = first; t < tiles; t += step, ++n) {
       const int b = n & 1;
@@ -281,35 +314,27 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
       const uint32_t d = tmem + ((uint32_t)(qd * 32) << 16) + (b ? P::kAcc1 : 0);
       const int m0 = tt * BN, nn = (rt * CG + half) * 128 + row;
       constexpr int W = BN < 32 ? BN : 32, C = BN / W;
+      auto freed = [&](uint64_t* bar) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (CG == 1) mbar_arrive(bar);
+          else mbar_arrive_cluster(peer_u32(bar, 0));
+        }
+      };
+      if (P::kOverlap && set) freed(&acc_free[0]);  // done with the tile before, and not the first chunk's
       if (p.split == 1) {
-        for (int i = 0; i < C; ++i) {
-          // the chunk in the columns that the other accumulator shares comes first
+        for (int i = set; i < C; i += 2) {
+          // the columns that the other accumulator shares come first
           const int c = P::kOverlap && b == 0 ? (i + C - 1) % C : i;
           uint32_t v[W];
           if constexpr (W == 32) tmem_ld32(d + c * W, v);
           else tmem_ld16(d + c * W, v);
-          if (P::kOverlap && i == 0) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              if (CG == 1) mbar_arrive(&acc_free[0]);
-              else mbar_arrive_cluster(peer_u32(&acc_free[0], 0));
-            }
-          }
-          if (nn < p.N) {
-#pragma unroll
-            for (int j = 0; j < W; ++j)
-              if (m0 + c * W + j < p.M) mm_store(p, (size_t)(m0 + c * W + j) * p.N + nn, __uint_as_float(v[j]));
-          }
+          if (P::kOverlap && i == 0) freed(&acc_free[0]);
+          const int m = m0 + c * W;
+          if (nn < p.N && m < p.M) mm_store_cols<W>(p, (size_t)m * p.N + nn, p.M - m, v);
         }
-        if (!P::kOverlap) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if (CG == 1) mbar_arrive(&acc_free[b]);
-            else mbar_arrive_cluster(peer_u32(&acc_free[b], 0));
-          }
-        }
+        if (!P::kOverlap) freed(&acc_free[b]);
       }
     }
   } else if (FILL) {
@@ -359,11 +384,11 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
     const int rows = min(BN, p.M - tt * BN), per = max(4, BN / p.split), lper = 31 - __clz(per);
     if (!P::kPart) cluster_arrive();
     cluster_wait();
-    if (warp >= 2 && warp < 6) {
+    if (warp >= 2 && warp < 11 && warp != 6) {
       const int qd = warp & 3, row = qd * 32 + lane;
       constexpr int W = BN < 32 ? BN : 32;
 #pragma unroll 1
-      for (int c = 0; c < rows; c += W) {
+      for (int c = warp > 6 ? W : 0; c < rows; c += 2 * W) {
         uint32_t v[W];
         if constexpr (W == 32) tmem_ld32(tmem + ((uint32_t)(qd * 32) << 16) + c, v);
         else tmem_ld16(tmem + ((uint32_t)(qd * 32) << 16) + c, v);
