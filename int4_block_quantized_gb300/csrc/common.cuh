@@ -246,15 +246,6 @@ __device__ __forceinline__ void tmem_relinquish2() {
 __device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t ncols) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
-// the same barrier in both CTAs
-__device__ __forceinline__ void mma_commit2_elect(uint64_t* bar) {
-  asm volatile(
-      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
-      " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}" ::"r"(
-          smem_u32(bar)),
-      "h"((uint16_t)3)
-      : "memory");
-}
 // shared::cluster address of the same object in CTA `rank`
 __device__ __forceinline__ uint32_t peer_u32(const void* local, uint32_t rank) {
   uint32_t r;
@@ -281,67 +272,64 @@ __device__ __forceinline__ uint32_t elect_lane() {
   return e;
 }
 // Block-scaled D[tmem] (+)= (A x scales) (B x scales)^T, operands by shared-memory
-// descriptors, scales (e8m0) in tensor memory, by the lane of a converged warp
-// whose `e` (elect_lane) is 1.  kind::mxf4: e2m1 x e2m1, 64 k, two blocks of 32 per
-// instruction; kind::mxf8f6f4: 8-bit containers, 32 k, one block.
+// descriptors (128-byte swizzle as sw128_desc; `a`, `b` are the low words, the
+// high word is constant), scales (e8m0) in tensor memory, by the lane of a
+// converged warp whose `e` (elect_lane) is 1.  kind::mxf4: e2m1 x e2m1, 64 k,
+// two blocks of 32 per instruction; kind::mxf8f6f4: 8-bit containers, 32 k,
+// one block.  CG: CTAs that share the product (cta_group).
+#define QMOE_MMA_MX(CGS, KIND, VEC)                                                                              \
+  asm volatile(                                                                                                  \
+      "{\n .reg .pred p, e;\n .reg .b64 a, b;\n mov.b64 a, {%1, %8};\n mov.b64 b, {%2, %8};\n"                    \
+      " setp.ne.b32 e, %7, 0;\n setp.ne.b32 p, %6, 0;\n"                                                         \
+      " @e tcgen05.mma.cta_group::" CGS ".kind::" KIND ".block_scale.scale_vec::" VEC                            \
+      " [%0], a, b, %3, [%4], [%5], p;\n}" ::"r"(d_tmem), "r"(a), "r"(b), "r"(idesc), "r"(sfa), "r"(sfb),        \
+      "r"(accumulate), "r"(e), "n"((1024u >> 4) | 1u << 14 | 2u << 29)                                           \
+      : "memory")
 template <int CG>
-__device__ __forceinline__ void mma_mxf4(uint32_t e, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                               uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+__device__ __forceinline__ void mma_mxf4(uint32_t e, uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc,
+                                         uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  if constexpr (CG == 1) QMOE_MMA_MX("1", "mxf4", "2X");
+  else QMOE_MMA_MX("2", "mxf4", "2X");
+}
+template <int CG>
+__device__ __forceinline__ void mma_mxf8f6f4(uint32_t e, uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc,
+                                             uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  if constexpr (CG == 1) QMOE_MMA_MX("1", "mxf8f6f4", "1X");
+  else QMOE_MMA_MX("2", "mxf8f6f4", "1X");
+}
+#undef QMOE_MMA_MX
+// 32 rows x 16 bytes of shared memory (`a`: address / 16; 8-row groups 128
+// bytes apart, unswizzled) into four columns of tensor memory, repeated in all
+// four lane quadrants (a 128 x 4 tile of scales); ordered before the
+// tcgen05.mma that the same lane issues next.  CG = 2: in both CTAs of the
+// pair, each from its own shared memory.
+#define QMOE_CP_SCALES(CGS)                                                                                         \
+  asm volatile("{\n .reg .pred e;\n .reg .b64 a;\n mov.b64 a, {%1, %3};\n setp.ne.b32 e, %2, 0;\n"                 \
+               " @e tcgen05.cp.cta_group::" CGS ".32x128b.warpx4 [%0], a;\n}" ::"r"(taddr),                         \
+               "r"(a), "r"(e), "n"((128u >> 4) | 1u << 14)                                                          \
+               : "memory")
+template <int CG>
+__device__ __forceinline__ void tmem_cp_scales(uint32_t e, uint32_t taddr, uint32_t a) {
+  if constexpr (CG == 1) QMOE_CP_SCALES("1");
+  else QMOE_CP_SCALES("2");
+}
+#undef QMOE_CP_SCALES
+// commit by the lane that issued; CG = 2: the same barrier in both CTAs
+template <int CG>
+__device__ __forceinline__ void mma_commit_mx(uint32_t e, uint64_t* bar) {
   if constexpr (CG == 1)
     asm volatile(
-        "{\n .reg .pred p, e;\n setp.ne.b32 e, %7, 0;\n setp.ne.b32 p, %6, 0;\n"
-        " @e tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(
-            d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(e)
+        "{\n .reg .pred e;\n setp.ne.b32 e, %1, 0;\n"
+        " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(smem_u32(bar)),
+        "r"(e)
         : "memory");
   else
     asm volatile(
-        "{\n .reg .pred p, e;\n setp.ne.b32 e, %7, 0;\n setp.ne.b32 p, %6, 0;\n"
-        " @e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(
-            d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(e)
+        "{\n .reg .pred e;\n setp.ne.b32 e, %1, 0;\n"
+        " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n}" ::"r"(
+            smem_u32(bar)),
+        "r"(e), "h"((uint16_t)3)
         : "memory");
-}
-template <int CG>
-__device__ __forceinline__ void mma_mxf8f6f4(uint32_t e, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                                   uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
-  if constexpr (CG == 1)
-    asm volatile(
-        "{\n .reg .pred p, e;\n setp.ne.b32 e, %7, 0;\n setp.ne.b32 p, %6, 0;\n"
-        " @e tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(
-            d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(e)
-        : "memory");
-  else
-    asm volatile(
-        "{\n .reg .pred p, e;\n setp.ne.b32 e, %7, 0;\n setp.ne.b32 p, %6, 0;\n"
-        " @e tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(
-            d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(e)
-        : "memory");
-}
-// 32 rows x 16 bytes of shared memory into four columns of tensor memory,
-// repeated in all four lane quadrants (a 128 x 4 tile of scales); ordered
-// before the tcgen05.mma that the same lane issues next.
-// CG = 2: in both CTAs of the pair, each from its own shared memory.
-template <int CG>
-__device__ __forceinline__ void tmem_cp_scales(uint32_t e, uint32_t taddr, uint64_t desc) {
-  if constexpr (CG == 1)
-    asm volatile(
-        "{\n .reg .pred e;\n setp.ne.b32 e, %2, 0;\n"
-        " @e tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n}" ::"r"(taddr),
-        "l"(desc), "r"(e)
-        : "memory");
-  else
-    asm volatile(
-        "{\n .reg .pred e;\n setp.ne.b32 e, %2, 0;\n"
-        " @e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n}" ::"r"(taddr),
-        "l"(desc), "r"(e)
-        : "memory");
-}
-// Unswizzled descriptor of 8-row x 16-byte groups 128 bytes apart.
-__device__ __forceinline__ uint64_t rows16_desc(uint32_t smem_addr) {
-  return (uint64_t)((smem_addr >> 4) & 0x3FFFu) | (uint64_t)(128u >> 4) << 32 | (uint64_t)1u << 46;
 }
 // Instruction descriptor of the block-scaled kinds, e8m0 scales, both operands
 // K-major; the formats' codes depend on the kind, sf_a / sf_b name the byte of

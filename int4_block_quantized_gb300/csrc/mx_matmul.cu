@@ -109,11 +109,6 @@ __device__ __forceinline__ void mm_store_cols(const MmParams& p, size_t i, int r
   }
 }
 
-template <int CG>
-__device__ __forceinline__ void mm_commit(uint64_t* bar) {
-  if (CG == 1) mma_commit_elect(bar);
-  else mma_commit2_elect(bar);
-}
 
 // Tile t of the grid: groups of 8 row tiles, so that the tiles in flight share
 // weights and tokens in L2.
@@ -145,7 +140,8 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   uint8_t* ring = smem + kMmBars;
   uint8_t* sfring = ring + S * P::kAb;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be the same in all lanes
 
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
@@ -269,13 +265,13 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
 #pragma unroll
         for (int q = 0; q < P::kWords; ++q) {
           if (q * 128 >= left) break;
-          tmem_cp_scales<CG>(el, tmem + P::kSfa + 4 * q, rows16_desc(sf + 512 * q));
+          tmem_cp_scales<CG>(el, tmem + P::kSfa + 4 * q, (sf >> 4) + 32 * q);
 #pragma unroll
           for (int i = 0; i < P::kTokSf; ++i)
             tmem_cp_scales<CG>(el, tmem + P::kSfb + 4 * (q * P::kTokSf + i),
-                                 rows16_desc(sf + 512 * (P::kWords * (1 + i) + q)));
+                                 (sf >> 4) + 32 * (P::kWords * (1 + i) + q));
         }
-        const uint64_t da = sw128_desc(st), db = sw128_desc(st + P::kA);
+        const uint32_t da = (st >> 4) | 1u << 16, db = ((st + P::kA) >> 4) | 1u << 16;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           if (j * (P::kStageK / 4) >= left) break;
@@ -286,17 +282,17 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
           else
             mma_mxf8f6f4<CG>(el, d, da + 2 * j, db + 2 * j, idesc_mx(128 * CG, BN, 5, 0, j, j), tmem + P::kSfa, sfb, acc);
         }
-        mm_commit<CG>(&empty[s]);
+        mma_commit_mx<CG>(el, &empty[s]);
         issued = true;
         if (++s == S) {
           s = 0;
           ph ^= 1u;
         }
       }
-      if (ok) mm_commit<CG>(&acc_full[b]);
+      if (ok) mma_commit_mx<CG>(el, &acc_full[b]);
     }
     if (issued) {  // all MMAs have finished before tensor memory is freed
-      mm_commit<CG>(fin);
+      mma_commit_mx<CG>(el, fin);
       mbar_wait(fin, 0, nullptr);
     }
   } else if (warp >= 2 && warp < 11) {
