@@ -30,6 +30,7 @@ struct MmParams {
   uint32_t* status;
   int M, N, K, y_dtype;
   int row_tiles, tok_tiles, kt;  // tiles of 128 weight rows, of BN tokens; scale tiles along K
+  int wide_out;                  // y: 16 bits, rows on 16-byte boundaries
   int split;                     // CTAs of a cluster that share a tile's K
 };
 
@@ -46,9 +47,11 @@ struct MmPlan {
   // a split tile's partial sums [split][tokens of a CTA / 4][128][4]: a place of
   // their own where they are small, else the ring once the cluster is done with it
   static constexpr uint32_t kPart = BN <= 64 ? (BN < 32 ? 32 : BN) * 512 : 0;
-  static constexpr int kStages0 = (int)((kMmSmem - kMmBars - 1024 - kPart) / (kAb + kSf));
+  // 2 KB per output warp: 32 tokens x 32 outputs of 16 bits, turned round there
+  static constexpr uint32_t kOut = BN >= 32 ? 8 * 2048 : 0;
+  static constexpr int kStages0 = (int)((kMmSmem - kMmBars - 1024 - kPart - kOut) / (kAb + kSf));
   static constexpr int kStages = kStages0 > 12 ? 12 : kStages0;
-  static constexpr uint32_t kTotal = kMmBars + kStages * (kAb + kSf) + kPart + 1024;
+  static constexpr uint32_t kTotal = kMmBars + kOut + kStages * (kAb + kSf) + kPart + 1024;
   // tensor memory: two accumulators, then the stage's scales.  At 256 tokens
   // the two overlap by 32 columns, since the scales need 24 of the 512.
   static constexpr bool kOverlap = BN == 256;
@@ -78,6 +81,16 @@ __device__ __forceinline__ void mm_store(const MmParams& p, size_t i, float v) {
   else static_cast<uint16_t*>(p.y)[i] = p.y_dtype == QMOE_BF16 ? Half<__nv_bfloat16>::from_float(v) : Half<__half>::from_float(v);
 }
 
+// two results to the output's 16-bit type
+__device__ __forceinline__ uint32_t mm_pack(const MmParams& p, uint32_t a, uint32_t b) {
+  if (p.y_dtype == QMOE_BF16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(a), __uint_as_float(b));
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __half2 h = __floats2half2_rn(__uint_as_float(a), __uint_as_float(b));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
 // W tokens' results of one output column: y[i], y[i + N], ... , the first `rows` of them.
 template <int W>
 __device__ __forceinline__ void mm_store_cols(const MmParams& p, size_t i, int rows, const uint32_t (&v)[W]) {
@@ -90,18 +103,9 @@ __device__ __forceinline__ void mm_store_cols(const MmParams& p, size_t i, int r
     return;
   }
   uint16_t* y = static_cast<uint16_t*>(p.y) + i;
-  const bool bf = p.y_dtype == QMOE_BF16;
 #pragma unroll
   for (int j = 0; j < W; j += 2) {
-    const float a = __uint_as_float(v[j]), b = __uint_as_float(v[j + 1]);
-    uint32_t u;
-    if (bf) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-      u = *reinterpret_cast<const uint32_t*>(&h);
-    } else {
-      const __half2 h = __floats2half2_rn(a, b);
-      u = *reinterpret_cast<const uint32_t*>(&h);
-    }
+    const uint32_t u = mm_pack(p, v[j], v[j + 1]);
     if (j < rows) *y = (uint16_t)(u & 0xffffu);
     y += N;
     if (j + 1 < rows) *y = (uint16_t)(u >> 16);
@@ -138,7 +142,8 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
   uint64_t* fin = acc_free + 2;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(fin + 1);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
-  uint8_t* ring = smem + kMmBars;
+  uint8_t* outbuf = smem + kMmBars;  // 1024-byte aligned, as the ring behind it
+  uint8_t* ring = outbuf + P::kOut;
   uint8_t* sfring = ring + S * P::kAb;
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be the same in all lanes
@@ -300,6 +305,7 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
     // Two warps per lane quadrant take the accumulator's chunks in turn (one
     // warp needed longer for 256 tokens than the MMAs of 2048 k).
     const int qd = warp & 3, row = qd * 32 + lane, set = warp > 6;
+    uint8_t* buf = outbuf + (warp - 2 - set) * 2048;
     int n = 0;
     for (int t = first; t < tiles; t += step, ++n) {
       const int b = n & 1;
@@ -323,11 +329,37 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
         for (int i = set; i < C; i += 2) {
           // the columns that the other accumulator shares come first
           const int c = P::kOverlap && b == 0 ? (i + C - 1) % C : i;
+          const int m = m0 + c * W;
+          if constexpr (W == 32) {
+            if (p.wide_out) {
+              uint32_t lo[16], hi[16];
+              tmem_ld_frag(d + c * W, lo, hi);
+              if (P::kOverlap && i == 0) freed(&acc_free[0]);
+              const int n0 = nn - lane;
+              if (m >= p.M || n0 >= p.N) continue;
+              // token 8 g + lane % 8 is a row of 64 bytes; its four 16-byte
+              // pieces (8 outputs each) are permuted against bank conflicts
+              const uint32_t a = smem_u32(buf) + (lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
+#pragma unroll
+              for (int g = 0; g < 4; ++g)
+                stmatrix_t4(a + g * 512, mm_pack(p, lo[4 * g], lo[4 * g + 1]), mm_pack(p, lo[4 * g + 2], lo[4 * g + 3]),
+                            mm_pack(p, hi[4 * g], hi[4 * g + 1]), mm_pack(p, hi[4 * g + 2], hi[4 * g + 3]));
+              __syncwarp();
+              const int tok = lane >> 2, piece = lane & 3;
+              uint16_t* y = static_cast<uint16_t*>(p.y) + (size_t)(m + tok) * p.N + n0 + piece * 8;
+#pragma unroll
+              for (int g = 0; g < 4; ++g, y += (size_t)8 * p.N)
+                if (m + 8 * g + tok < p.M && n0 + piece * 8 < p.N)
+                  *reinterpret_cast<uint4*>(y) =
+                      *reinterpret_cast<const uint4*>(buf + g * 512 + tok * 64 + ((piece ^ ((tok >> 1) & 3)) << 4));
+              __syncwarp();
+              continue;
+            }
+          }
           uint32_t v[W];
           if constexpr (W == 32) tmem_ld32(d + c * W, v);
           else tmem_ld16(d + c * W, v);
           if (P::kOverlap && i == 0) freed(&acc_free[0]);
-          const int m = m0 + c * W;
           if (nn < p.N && m < p.M) mm_store_cols<W>(p, (size_t)m * p.N + nn, p.M - m, v);
         }
         if (!P::kOverlap) freed(&acc_free[b]);
@@ -467,6 +499,7 @@ static cudaError_t launch_mm(MmParams p, const uint8_t* xc, cudaStream_t st) {
     };
     if (!smap(&tws, p.ws, dw) || !smap(&txs, p.xs, dx)) return cudaErrorNotSupported;
   }
+  p.wide_out = p.y_dtype != QMOE_F32 && p.N % 8 == 0 && !(reinterpret_cast<uintptr_t>(p.y) & 15);
   // few tiles: a cluster of up to 8 CTAs shares a tile's K
   const int sms = device_sm_count(), chunks = (p.K + P::kStageK - 1) / P::kStageK;
   p.split = 1;

@@ -238,6 +238,25 @@ def test_matmul_many_tiles(M, N, K, xf):
 
 
 @pytest.mark.parametrize("xf", FMT)
+@pytest.mark.parametrize("M,N,K", [(33, 40, 96), (70, 136, 160), (200, 1000, 256), (2600, 1912, 256), (2817, 1800, 128),
+                                   (1281, 4008, 640), (129, 8, 128)])
+@pytest.mark.parametrize("dtype", DT[:2])
+def test_matmul_rows_of_y_on_16_bytes(M, N, K, xf, dtype):
+    """N a multiple of 8 (y is then written in tiles), ragged tiles either way;
+    and the same into a y that does not start on 16 bytes, which has to agree."""
+    xc, xs = random_mx(M, K, xf, M + 1)
+    wc, ws = random_mx(N, K, B.MXFP4, N + 2)
+    x, w = to_dev(xc, xs, xf), to_dev(wc, ws, B.MXFP4)
+    buf = torch.full((M * N + 64,), 7.0, dtype=dtype, device=DEV)
+    y = B.qmoe_mx_matmul(*x, xf, *w, dtype, out=buf[16:16 + M * N].view(M, N))
+    assert (buf[:16] == 7).all() and (buf[16 + M * N:] == 7).all()
+    check_product(xc, xs, xf, wc, ws, y, dtype)
+    other = torch.full((M * N + 64,), 7.0, dtype=dtype, device=DEV)
+    assert torch.equal(B.qmoe_mx_matmul(*x, xf, *w, dtype, out=other[3:3 + M * N].view(M, N)), y)
+    assert (other[:3] == 7).all() and (other[3 + M * N:] == 7).all()
+
+
+@pytest.mark.parametrize("xf", FMT)
 def test_matmul_scale_extremes(xf):
     """Scales across many binades between blocks, zero codes, the smallest scale."""
     M, N, K = 20, 150, 512
