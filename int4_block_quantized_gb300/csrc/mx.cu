@@ -22,18 +22,14 @@ template <typename T, int FMT>
 __global__ void __launch_bounds__(256) mx_quantize_kernel(const void* __restrict__ x, int M, int K,
                                                           uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
   pdl_wait();
-  const size_t t0 = blockIdx.x * (size_t)256 + threadIdx.x, stride = (size_t)gridDim.x * 256;
-  const uint32_t per_row = (uint32_t)K / 16;
-  const size_t n = (size_t)M * per_row;
+  const uint32_t t0 = blockIdx.x * 256 + threadIdx.x, stride = gridDim.x * 256;
   const int kt = (K + 127) / 128;
-  for (size_t i = t0; i < n; i += stride) {
+  for (RowWalk w(t0, stride, (uint32_t)K / 16); w.r < (uint32_t)M; w.next()) {
+    const size_t i = (size_t)w.r * K + 16 * w.u;
     float v[16];
-    load16<T>(x, i * 16, v);
-    const uint32_t s = mx_encode16<FMT>(v, codes, i * 16);
-    if (!(i & 1)) {
-      const int r = (int)(i / per_row);
-      scales[mx_scale_index(r, (int)(i - (size_t)r * per_row) >> 1, kt)] = (uint8_t)s;
-    }
+    load16<T>(x, i, v);
+    const uint32_t s = mx_encode16<FMT>(v, codes, i);
+    if (!(w.u & 1)) scales[mx_scale_index((int)w.r, (int)w.u >> 1, kt)] = (uint8_t)s;
   }
   mx_zero_padding(scales, M, K, t0, stride);
 }
@@ -41,7 +37,7 @@ __global__ void __launch_bounds__(256) mx_quantize_kernel(const void* __restrict
 template <typename T>
 static cudaError_t launch_quantize_t(const void* x, int format, int M, int K, uint8_t* codes, uint8_t* scales,
                                      cudaStream_t st) {
-  const dim3 g = stride_grid((size_t)M * (K / 16));
+  const dim3 g = stride_grid((size_t)M * (K / 16) + mx_padding_words(M, K));
   if (format == kMxfp8)
     return launch_kernel(mx_quantize_kernel<T, kMxfp8>, g, dim3(256), 0, st, true, x, M, K, codes, scales);
   return launch_kernel(mx_quantize_kernel<T, kMxfp4>, g, dim3(256), 0, st, true, x, M, K, codes, scales);
@@ -61,28 +57,25 @@ __global__ void __launch_bounds__(256) mx_dequant_kernel(const uint8_t* __restri
                                                          const uint8_t* __restrict__ scales, int M, int K,
                                                          void* __restrict__ out) {
   pdl_wait();
-  const size_t stride = (size_t)gridDim.x * 256;
-  const uint32_t per_row = (uint32_t)K / 16;
-  const size_t n = (size_t)M * per_row;
   const int kt = (K + 127) / 128;
-  for (size_t i = blockIdx.x * (size_t)256 + threadIdx.x; i < n; i += stride) {
-    const int r = (int)(i / per_row);
-    const float X = mx_scale(scales[mx_scale_index(r, (int)(i - (size_t)r * per_row) >> 1, kt)]);
+  for (RowWalk w(blockIdx.x * 256 + threadIdx.x, gridDim.x * 256, (uint32_t)K / 16); w.r < (uint32_t)M; w.next()) {
+    const size_t i = (size_t)w.r * K + 16 * w.u;
+    const float X = mx_scale(scales[mx_scale_index((int)w.r, (int)w.u >> 1, kt)]);
     float v[16];
     if constexpr (FMT == kMxfp8) {
-      const uint4 c = *reinterpret_cast<const uint4*>(codes + i * 16);
+      const uint4 c = *reinterpret_cast<const uint4*>(codes + i);
       mx_from_e4m3x4(c.x, v);
       mx_from_e4m3x4(c.y, v + 4);
       mx_from_e4m3x4(c.z, v + 8);
       mx_from_e4m3x4(c.w, v + 12);
     } else {
-      const uint2 c = *reinterpret_cast<const uint2*>(codes + i * 8);
+      const uint2 c = *reinterpret_cast<const uint2*>(codes + i / 2);
       mx_from_e2m1x8(c.x, v);
       mx_from_e2m1x8(c.y, v + 8);
     }
 #pragma unroll
     for (int j = 0; j < 16; ++j) v[j] *= X;
-    store16<T>(out, i * 16, v);
+    store16<T>(out, i, v);
   }
 }
 
@@ -104,29 +97,41 @@ cudaError_t launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, int f
 
 // ---------------------------------------------------------------- RMSNorm
 // h = x + residual in fp32; residual_out = RN(h); y = h / sqrt(mean(h^2) +
-// eps) * weight from the unrounded h, quantised like above.  One CTA per
-// row.  x and residual are read again for the second pass (from L1 / L2), so
-// residual_out may be either of them: each element is read and written by
-// one thread, and nothing is written before the row's sum is complete.
-template <typename T, int FMT>
+// eps) * weight from the unrounded h, quantised like above.  One CTA per row;
+// a thread keeps its U units of 16 elements in registers between the sum and
+// the output (U = 0: rows too long for that, read twice).  residual_out may be
+// x or residual: each element is read and written by one thread, and nothing
+// is written before the row's sum is complete.
+template <typename T>
+__device__ __forceinline__ void norm_load(const void* x, const void* residual, size_t i, float (&v)[16]) {
+  load16<T>(x, i, v);
+  if (residual) {
+    float r[16];
+    load16<T>(residual, i, r);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] += r[j];
+  }
+}
+
+template <typename T, int FMT, int U>
 __global__ void __launch_bounds__(256) mx_rmsnorm_kernel(const void* x, const void* residual, const void* weight,
                                                          int M, int H, float eps, void* residual_out, uint8_t* codes,
                                                          uint8_t* scales) {
   pdl_wait();
   const int units = H / 16, kt = (H + 127) / 128, t = blockIdx.x;
   const size_t row = (size_t)t * H;
+  constexpr int R = U ? U : 1;
+  float h[R][16], w[16];
   float ss = 0.f;
-  for (int u = threadIdx.x; u < units; u += 256) {
-    float v[16];
-    load16<T>(x, row + u * 16, v);
-    if (residual) {
-      float r[16];
-      load16<T>(residual, row + u * 16, r);
+  const bool keep_weight = U == 1 && weight && threadIdx.x < units;  // read beside x
+  if (keep_weight) load16<T>(weight, threadIdx.x * 16, w);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) v[j] += r[j];
-    }
+  for (int k = 0; k < (U ? U : 1 << 30); ++k) {
+    const int u = threadIdx.x + 256 * k;
+    if (u >= units) break;
+    norm_load<T>(x, residual, row + u * 16, h[U ? k : 0]);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) ss = fmaf(v[j], v[j], ss);
+    for (int j = 0; j < 16; ++j) ss = fmaf(h[U ? k : 0][j], h[U ? k : 0][j], ss);
   }
   ss = warp_sum(ss);
   __shared__ float part[8];
@@ -134,45 +139,47 @@ __global__ void __launch_bounds__(256) mx_rmsnorm_kernel(const void* x, const vo
   __syncthreads();
   float tot = 0.f;
 #pragma unroll
-  for (int w = 0; w < 8; ++w) tot += part[w];
+  for (int i = 0; i < 8; ++i) tot += part[i];
   const float inv = 1.0f / sqrtf(tot / (float)H + eps);
-  for (int u = threadIdx.x; u < units; u += 256) {
-    float v[16];
-    load16<T>(x, row + u * 16, v);
-    if (residual) {
-      float r[16];
-      load16<T>(residual, row + u * 16, r);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) v[j] += r[j];
-    }
+  for (int k = 0; k < (U ? U : 1 << 30); ++k) {
+    const int u = threadIdx.x + 256 * k;
+    if (u >= units) break;
+    float(&v)[16] = h[U ? k : 0];
+    if (!U) norm_load<T>(x, residual, row + u * 16, v);
     if (residual_out) store16<T>(residual_out, row + u * 16, v);
 #pragma unroll
     for (int j = 0; j < 16; ++j) v[j] *= inv;
     if (weight) {
-      float w[16];
-      load16<T>(weight, u * 16, w);
+      if (!keep_weight) load16<T>(weight, u * 16, w);
 #pragma unroll
       for (int j = 0; j < 16; ++j) v[j] *= w[j];
     }
     const uint32_t s = mx_encode16<FMT>(v, codes, row + u * 16);
     if (!(u & 1)) scales[mx_scale_index(t, u >> 1, kt)] = (uint8_t)s;
   }
-  mx_zero_padding(scales, M, H, blockIdx.x * (size_t)256 + threadIdx.x, (size_t)gridDim.x * 256);
+  mx_zero_padding(scales, M, H, blockIdx.x * 256 + threadIdx.x, gridDim.x * 256);
+}
+
+template <typename T, int FMT>
+static cudaError_t launch_rmsnorm_t(const void* x, const void* residual, const void* weight, int M, int H, float eps,
+                                    void* residual_out, uint8_t* codes, uint8_t* scales, cudaStream_t st) {
+  auto go = [&](auto kernel) {
+    return launch_kernel(kernel, dim3(M), dim3(256), 0, st, true, x, residual, weight, M, H, eps, residual_out, codes,
+                         scales);
+  };
+  if (H <= 4096) return go(mx_rmsnorm_kernel<T, FMT, 1>);
+  if (H <= 8192) return go(mx_rmsnorm_kernel<T, FMT, 2>);
+  return go(mx_rmsnorm_kernel<T, FMT, 0>);
 }
 
 cudaError_t launch_mx_rmsnorm(const void* x, const void* residual, const void* weight, int act_dtype, int T, int H,
                               float eps, int format, void* residual_out, uint8_t* codes, uint8_t* scales,
                               cudaStream_t st) {
-#define QMOE_N(T_, F_)                                                                                          \
-  return launch_kernel(mx_rmsnorm_kernel<T_, F_>, dim3(T), dim3(256), 0, st, true, x, residual, weight, T, H, eps, \
-                       residual_out, codes, scales)
-  if (act_dtype == QMOE_BF16) {
-    if (format == kMxfp8) QMOE_N(__nv_bfloat16, kMxfp8);
-    QMOE_N(__nv_bfloat16, kMxfp4);
-  }
-  if (format == kMxfp8) QMOE_N(__half, kMxfp8);
-  QMOE_N(__half, kMxfp4);
-#undef QMOE_N
+  auto go = [&](auto fn) { return fn(x, residual, weight, T, H, eps, residual_out, codes, scales, st); };
+  if (act_dtype == QMOE_BF16)
+    return format == kMxfp8 ? go(launch_rmsnorm_t<__nv_bfloat16, kMxfp8>) : go(launch_rmsnorm_t<__nv_bfloat16, kMxfp4>);
+  return format == kMxfp8 ? go(launch_rmsnorm_t<__half, kMxfp8>) : go(launch_rmsnorm_t<__half, kMxfp4>);
 }
 
 // --------------------------------------------------------- scale adapters
@@ -181,12 +188,10 @@ template <bool TO_TILES>
 __global__ void __launch_bounds__(256) mx_retile_kernel(const uint8_t* __restrict__ in, uint8_t* __restrict__ out,
                                                         int R, int K) {
   pdl_wait();
-  const size_t t0 = blockIdx.x * (size_t)256 + threadIdx.x, stride = (size_t)gridDim.x * 256;
+  const uint32_t t0 = blockIdx.x * 256 + threadIdx.x, stride = gridDim.x * 256;
   const int nb = K / 32, kt = (K + 127) / 128;
-  const size_t n = (size_t)R * nb;
-  for (size_t i = t0; i < n; i += stride) {
-    const int r = (int)(i / nb);
-    const size_t j = mx_scale_index(r, (int)(i - (size_t)r * nb), kt);
+  for (RowWalk w(t0, stride, (uint32_t)nb); w.r < (uint32_t)R; w.next()) {
+    const size_t i = (size_t)w.r * nb + w.u, j = mx_scale_index((int)w.r, (int)w.u, kt);
     if (TO_TILES) out[j] = in[i];
     else out[i] = in[j];
   }

@@ -86,42 +86,89 @@ __device__ __forceinline__ void mx_from_e4m3x4(uint32_t w, float* v) {
   }
 }
 
-// Sixteen elements: fp16 / bf16 from two 16-byte words, fp32 from four.
+// 32 bytes: one access on a 32-byte boundary (a whole sector; two 16-byte
+// stores would reach L2 as two half sectors), else two of 16.
+__device__ __forceinline__ void load32(const void* p, uint32_t (&w)[8]) {
+  if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p)
+                 : "memory");
+  } else {
+    const uint4 a = static_cast<const uint4*>(p)[0], b = static_cast<const uint4*>(p)[1];
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+  }
+}
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
+  if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+    asm volatile("st.global.v8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "l"(p)
+                 : "memory");
+  } else {
+    static_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    static_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+// Sixteen elements of fp16, bf16 or fp32 at element i (a multiple of 16).
 template <typename T>
 __device__ __forceinline__ void load16(const void* base, size_t i, float (&v)[16]) {
-  const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + i * sizeof(T));
+  const uint8_t* p = static_cast<const uint8_t*>(base) + i * sizeof(T);
+  uint32_t w[8];
+  if constexpr (sizeof(T) == 4) {
 #pragma unroll
-  for (int q = 0; q < (int)sizeof(T); ++q) {
-    const uint4 u = p[q];
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    for (int q = 0; q < 2; ++q) {
+      load32(p + 32 * q, w);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (sizeof(T) == 4) {
-        v[q * 4 + j] = __uint_as_float(w[j]);
-      } else {
-        v[q * 8 + 2 * j] = Half<T>::to_float((uint16_t)(w[j] & 0xffffu));
-        v[q * 8 + 2 * j + 1] = Half<T>::to_float((uint16_t)(w[j] >> 16));
-      }
+      for (int j = 0; j < 8; ++j) v[q * 8 + j] = __uint_as_float(w[j]);
+    }
+  } else {
+    load32(p, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[2 * j] = Half<T>::to_float((uint16_t)(w[j] & 0xffffu));
+      v[2 * j + 1] = Half<T>::to_float((uint16_t)(w[j] >> 16));
     }
   }
 }
 template <typename T>
 __device__ __forceinline__ void store16(void* base, size_t i, const float (&v)[16]) {
-  uint4* p = reinterpret_cast<uint4*>(static_cast<uint8_t*>(base) + i * sizeof(T));
+  uint8_t* p = static_cast<uint8_t*>(base) + i * sizeof(T);
+  uint32_t w[8];
+  if constexpr (sizeof(T) == 4) {
 #pragma unroll
-  for (int q = 0; q < (int)sizeof(T); ++q) {
-    uint32_t w[4];
+    for (int q = 0; q < 2; ++q) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (sizeof(T) == 4)
-        w[j] = __float_as_uint(v[q * 4 + j]);
-      else
-        w[j] = (uint32_t)Half<T>::from_float(v[q * 8 + 2 * j]) |
-               ((uint32_t)Half<T>::from_float(v[q * 8 + 2 * j + 1]) << 16);
+      for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(v[q * 8 + j]);
+      store32(p + 32 * q, w);
     }
-    p[q] = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      w[j] = (uint32_t)Half<T>::from_float(v[2 * j]) | ((uint32_t)Half<T>::from_float(v[2 * j + 1]) << 16);
+    store32(p, w);
   }
 }
+
+// Rows of `per_row` units walked with a fixed stride: one 32-bit division at
+// the start and at the stride, none per step (a 64-bit one cost the reader a
+// quarter of its time).
+struct RowWalk {
+  uint32_t per_row, dr, du, r, u;
+  __device__ __forceinline__ RowWalk(uint32_t start, uint32_t stride, uint32_t per_row_)
+      : per_row(per_row_), dr(stride / per_row_), r(start / per_row_) {
+    du = stride - dr * per_row;
+    u = start - r * per_row;
+  }
+  __device__ __forceinline__ void next() {
+    r += dr;
+    u += du;
+    if (u >= per_row) {
+      u -= per_row;
+      ++r;
+    }
+  }
+};
 
 // Half a block per thread, the other half in the neighbouring lane (lane ^
 // 1): the block's scale byte, and this half's codes stored at element i.
@@ -149,13 +196,16 @@ __device__ __forceinline__ uint32_t mx_encode16(float (&v)[16], uint8_t* codes, 
 // Zeroes of the scale tiles' padding, split over n_threads threads: the rows
 // M .. a multiple of 128 (words), and in the rows below M the blocks K / 32 ..
 // a multiple of 4 (bytes).
-__device__ __forceinline__ void mx_zero_padding(uint8_t* scales, int M, int K, size_t thread, size_t n_threads) {
+__host__ __device__ __forceinline__ uint32_t mx_padding_words(int M, int K) {
+  return (uint32_t)(-M & 127) * (uint32_t)((K + 127) / 128);
+}
+__device__ __forceinline__ void mx_zero_padding(uint8_t* scales, int M, int K, uint32_t thread, uint32_t n_threads) {
   const int nb = K / 32, kt = (K + 127) / 128;
-  const size_t words = (size_t)(((M + 127) & ~127) - M) * kt;
-  for (size_t i = thread; i < words; i += n_threads)
-    *reinterpret_cast<uint32_t*>(scales + mx_scale_index(M + (int)(i / kt), 4 * (int)(i % kt), kt)) = 0u;
+  const uint32_t words = mx_padding_words(M, K), rows = (uint32_t)(-M & 127);
+  for (uint32_t i = thread; i < words; i += n_threads)  // along the rows: neighbours in a tile
+    *reinterpret_cast<uint32_t*>(scales + mx_scale_index(M + (int)(i % rows), 4 * (int)(i / rows), kt)) = 0u;
   if (nb & 3)
-    for (size_t r = thread; r < (size_t)M; r += n_threads)
+    for (uint32_t r = thread; r < (uint32_t)M; r += n_threads)
       for (int b = nb; b < 4 * kt; ++b) scales[mx_scale_index((int)r, b, kt)] = 0;
 }
 

@@ -261,38 +261,46 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
       const uint32_t d = tmem + (b ? P::kAcc1 : 0);
       // BN = 64: an odd token tile starts in the middle of its scale tile
       const uint32_t sfb = tmem + P::kSfb + (BN == 64 ? 2 * (tt & 1) : 0);
-      for (int c = c0; c < c1; ++c) {
-        ok = mm_wait(&full[s], ph, p.status, s_abort);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t st = smem_u32(ring + s * P::kAb), sf = smem_u32(sfring + s * P::kSf);
-        const int left = p.K - c * P::kStageK;  // elements from here on
+      // one stage: its scales, then its MMAs (the first `words` scale words and
+      // `mmas` instructions: fewer only where K ends)
+      auto issue = [&](int slot, bool first_stage, int words, int mmas) {
+        const uint32_t st = smem_u32(ring + slot * P::kAb) >> 4, sf = smem_u32(sfring + slot * P::kSf) >> 4;
 #pragma unroll
         for (int q = 0; q < P::kWords; ++q) {
-          if (q * 128 >= left) break;
-          tmem_cp_scales<CG>(el, tmem + P::kSfa + 4 * q, (sf >> 4) + 32 * q);
+          if (q >= words) break;
+          tmem_cp_scales<CG>(el, tmem + P::kSfa + 4 * q, sf + 32 * q);
 #pragma unroll
           for (int i = 0; i < P::kTokSf; ++i)
-            tmem_cp_scales<CG>(el, tmem + P::kSfb + 4 * (q * P::kTokSf + i),
-                                 (sf >> 4) + 32 * (P::kWords * (1 + i) + q));
+            tmem_cp_scales<CG>(el, tmem + P::kSfb + 4 * (q * P::kTokSf + i), sf + 32 * (P::kWords * (1 + i) + q));
         }
-        const uint32_t da = (st >> 4) | 1u << 16, db = ((st + P::kA) >> 4) | 1u << 16;
+        const uint32_t da = st | 1u << 16, db = (st + (P::kA >> 4)) | 1u << 16;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          if (j * (P::kStageK / 4) >= left) break;
-          const uint32_t acc = (c > c0 || j > 0) ? 1u : 0u;
+          if (j >= mmas) break;
+          const uint32_t acc = (j > 0 || !first_stage) ? 1u : 0u;
           if (XF == kMxfp4)
             mma_mxf4<CG>(el, d, da + 2 * j, db + 2 * j, idesc_mx(128 * CG, BN, 1, 1, 2 * (j & 1), 2 * (j & 1)),
-                           tmem + P::kSfa + 4 * (j >> 1), sfb + 4 * P::kTokSf * (j >> 1), acc);
+                         tmem + P::kSfa + 4 * (j >> 1), sfb + 4 * P::kTokSf * (j >> 1), acc);
           else
             mma_mxf8f6f4<CG>(el, d, da + 2 * j, db + 2 * j, idesc_mx(128 * CG, BN, 5, 0, j, j), tmem + P::kSfa, sfb, acc);
         }
-        mma_commit_mx<CG>(el, &empty[s]);
-        issued = true;
+        mma_commit_mx<CG>(el, &empty[slot]);
+      };
+      bool ready = mbar_try_wait(&full[s], ph);
+      for (int c = c0; c < c1; ++c) {
+        if (!ready) ok = mm_wait(&full[s], ph, p.status, s_abort);
+        if (!ok) break;
+        const int slot = s;
         if (++s == S) {
           s = 0;
           ph ^= 1u;
         }
+        ready = c + 1 < c1 && mbar_try_wait(&full[s], ph);  // the next stage's answer arrives meanwhile
+        tc_fence_after();
+        const int left = p.K - c * P::kStageK;  // elements from here on
+        if (left >= P::kStageK) issue(slot, c == c0, P::kWords, 4);
+        else issue(slot, c == c0, (left + 127) / 128, (left + P::kStageK / 4 - 1) / (P::kStageK / 4));
+        issued = true;
       }
       if (ok) mma_commit_mx<CG>(el, &acc_full[b]);
     }
@@ -458,9 +466,10 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
 }
 
 template <int XF, int BN, int CG, bool FILL>
-static cudaError_t launch_mm(MmParams p, const uint8_t* xc, cudaStream_t st) {
+static cudaError_t launch_mm(MmParams p, int split, const uint8_t* xc, cudaStream_t st) {
   using P = MmPlan<XF, BN, CG>;
   static_assert(P::kTotal <= kMmSmem && P::kCols0 <= 512, "plan");
+  p.split = split;
   p.row_tiles = (p.N + 128 * CG - 1) / (128 * CG);
   p.tok_tiles = (p.M + BN - 1) / BN;
   const long long tiles = (long long)p.row_tiles * p.tok_tiles;
@@ -500,10 +509,7 @@ static cudaError_t launch_mm(MmParams p, const uint8_t* xc, cudaStream_t st) {
     if (!smap(&tws, p.ws, dw) || !smap(&txs, p.xs, dx)) return cudaErrorNotSupported;
   }
   p.wide_out = p.y_dtype != QMOE_F32 && p.N % 8 == 0 && !(reinterpret_cast<uintptr_t>(p.y) & 15);
-  // few tiles: a cluster of up to 8 CTAs shares a tile's K
-  const int sms = device_sm_count(), chunks = (p.K + P::kStageK - 1) / P::kStageK;
-  p.split = 1;
-  while (CG == 1 && p.split < 8 && 2 * p.split <= chunks && tiles * p.split * 2 <= sms) p.split *= 2;
+  const int sms = device_sm_count();
   auto kernel = mx_matmul_kernel<XF, BN, CG, FILL>;
   cudaError_t err = ensure_smem(kernel, P::kTotal);
   if (err != cudaSuccess) return err;
@@ -523,17 +529,88 @@ static cudaError_t launch_mm(MmParams p, const uint8_t* xc, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, kernel, tw, tx, tws, txs, p);
 }
 
+// CTAs of clusters of `split` that the device holds at once, one CTA to an SM.
+static int mm_capacity(int split) {
+  static int cached[64][4] = {};
+  const int l = split == 8 ? 3 : split == 4 ? 2 : split == 2 ? 1 : 0;
+  int dev = 0;
+  if (l == 0 || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return device_sm_count();
+  if (!cached[dev][l]) {
+    using P = MmPlan<kMxfp4, 16, 1>;
+    auto kernel = mx_matmul_kernel<kMxfp4, 16, 1, false>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(split);
+    cfg.blockDim = dim3(kMmThreads);
+    cfg.dynamicSmemBytes = P::kTotal;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = split;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (ensure_smem(kernel, P::kTotal) != cudaSuccess || cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1)
+      return split;  // not known: no more than one cluster at a time
+    cached[dev][l] = n * split;
+  }
+  return cached[dev][l];
+}
+
+// Tokens per tile (and a pair of CTAs or one) and CTAs per tile along K, by an
+// estimate of the time in ns: a start, the stages of the CTA with the most
+// tiles, what each further tile adds beyond its MMAs, and the exchange of a
+// split tile's sums.  The constants are fits to measured kernel times on GB300
+// (us; x in MXFP8; tokens a tile / CTAs along K, 2 x 256 a pair):
+//     16 x 1408 x 2048    16/8 3.9   16/4 4.0   16/2 4.4   16/1 4.7
+//     64 x 2048 x 5632    64/4 6.0   64/2 7.6   64/1 9.6   128/4 7.1  128/1 9.9
+//    512 x 1408 x 2048    64/1 5.4   128/1 5.9  128/2 8.0  256/1 8.6  2x256/1 9.1
+//   2048 x 1408 x 2048    256/1 9.5  128/1 9.7  2x256/1 10.1  64/1 11.5
+//    512 x 8192 x 8192    2x256/1 24  256/1 27  128/1 28   64/1 46
+//   2048 x 11264 x 2048   2x256/1 33  256/1 35  128/1 39   64/1 59
+struct MmChoice {
+  int bn, cg, split;
+};
+static MmChoice mm_choose(int M, int N, int chunks, bool fill) {
+  static const struct {
+    int bn, cg, start, stage, tile, exchange;
+  } kinds[] = {{16, 1, 1900, 170, 300, 1200},  {32, 1, 2000, 170, 350, 1300}, {64, 1, 2900, 165, 500, 1400},
+               {128, 1, 3600, 185, 1200, 2200}, {256, 1, 4000, 340, 1800, 0},  {256, 2, 4600, 300, 1500, 0}};
+  MmChoice best = {128, 1, 1};
+  long long least = -1;
+  for (const auto& k : kinds) {
+    if (k.bn < 64 && M > k.bn) continue;  // 16 and 32 tokens: a single tile, at the head of its scale tile
+    if (k.cg == 2 && fill) continue;
+    const int stage = fill ? 2 * k.stage : k.stage;  // weights by loads and stores: 340 ns at 16 to 128 tokens
+    const long long tiles = (long long)((N + 128 * k.cg - 1) / (128 * k.cg)) * ((M + k.bn - 1) / k.bn);
+    for (int split = 1; split <= 8; split *= 2) {
+      if (split > 1 && (!k.exchange || split > chunks || tiles * split > mm_capacity(split))) break;
+      const long long slots = split > 1 ? tiles : device_sm_count() / k.cg;
+      const long long rounds = (tiles + slots - 1) / slots;
+      const long long t = k.start + rounds * ((chunks + split - 1) / split) * stage + (rounds - 1) * k.tile +
+                          (split > 1 ? k.exchange : 0);
+      if (least < 0 || t < least) {
+        least = t;
+        best = {k.bn, k.cg, split};
+      }
+    }
+  }
+  return best;
+}
+
 template <int XF, bool FILL>
 static cudaError_t launch_mm_bn(const MmParams& p, const uint8_t* xc, cudaStream_t st) {
-  if (p.M <= 16) return launch_mm<XF, 16, 1, FILL>(p, xc, st);
-  if (p.M <= 32) return launch_mm<XF, 32, 1, FILL>(p, xc, st);
-  if (p.M <= 64) return launch_mm<XF, 64, 1, FILL>(p, xc, st);
-  // 256-token tiles once they fill the card
-  if ((long long)((p.N + 127) / 128) * ((p.M + 255) / 256) >= device_sm_count()) {
-    if constexpr (FILL) return launch_mm<XF, 256, 1, FILL>(p, xc, st);
-    else return launch_mm<XF, 256, 2, false>(p, xc, st);
+  const int stage = MmPlan<XF, 128, 1>::kStageK;
+  const MmChoice c = mm_choose(p.M, p.N, (p.K + stage - 1) / stage, FILL);
+  switch (c.bn) {
+    case 16: return launch_mm<XF, 16, 1, FILL>(p, c.split, xc, st);
+    case 32: return launch_mm<XF, 32, 1, FILL>(p, c.split, xc, st);
+    case 64: return launch_mm<XF, 64, 1, FILL>(p, c.split, xc, st);
+    case 128: return launch_mm<XF, 128, 1, FILL>(p, c.split, xc, st);
+    default:
+      if constexpr (!FILL)
+        if (c.cg == 2) return launch_mm<XF, 256, 2, false>(p, 1, xc, st);
+      return launch_mm<XF, 256, 1, FILL>(p, 1, xc, st);
   }
-  return launch_mm<XF, 128, 1, FILL>(p, xc, st);
 }
 
 cudaError_t launch_mx_matmul(const uint8_t* xc, const uint8_t* xs, int x_format, const uint8_t* wc, const uint8_t* ws,
