@@ -97,11 +97,16 @@ cudaError_t launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, int f
 
 // ---------------------------------------------------------------- RMSNorm
 // h = x + residual in fp32; residual_out = RN(h); y = h / sqrt(mean(h^2) +
-// eps) * weight from the unrounded h, quantised like above.  One CTA per row;
-// a thread keeps its U units of 16 elements in registers between the sum and
-// the output (U = 0: rows too long for that, read twice).  residual_out may be
-// x or residual: each element is read and written by one thread, and nothing
-// is written before the row's sum is complete.
+// eps) * weight from the unrounded h, quantised like above.  One CTA per row,
+// a thread to 16 elements, which it keeps in registers between the sum and the
+// output (KEEP; rows beyond 16384 are read twice).  residual_out may be x or
+// residual: each element is read and written by one thread, and nothing is
+// written before the row's sum is complete.
+// Bound by HBM.  32 registers a thread (the launch bound), so that 2048 threads
+// fit an SM and one row's loads run during another's sum: 16384 x 4096 bf16
+// with residual takes 70 us at 32 registers (6.76 TB/s) and 95 us at 55;
+// reading the row twice instead of keeping it takes 76 us.  One thread per 16
+// elements, and not 256 throughout: 16384 x 2048 takes 36 us instead of 45.
 template <typename T>
 __device__ __forceinline__ void norm_load(const void* x, const void* residual, size_t i, float (&v)[16]) {
   load16<T>(x, i, v);
@@ -113,64 +118,60 @@ __device__ __forceinline__ void norm_load(const void* x, const void* residual, s
   }
 }
 
-template <typename T, int FMT, int U>
-__global__ void __launch_bounds__(256) mx_rmsnorm_kernel(const void* x, const void* residual, const void* weight,
-                                                         int M, int H, float eps, void* residual_out, uint8_t* codes,
-                                                         uint8_t* scales) {
+template <typename T, int FMT, bool KEEP>
+__global__ void __launch_bounds__(1024, 2)
+    mx_rmsnorm_kernel(const void* x, const void* residual, const void* weight, int M, int H, float eps,
+                      void* residual_out, uint8_t* codes, uint8_t* scales) {
   pdl_wait();
-  const int units = H / 16, kt = (H + 127) / 128, t = blockIdx.x;
+  const int units = H / 16, kt = (H + 127) / 128, t = blockIdx.x, threads = blockDim.x;
+  if (t >= M) {  // the last CTAs: the scale tiles' rows behind row M
+    mx_zero_rows(scales, M, H, (t - M) * threads + threadIdx.x, (gridDim.x - M) * threads);
+    return;
+  }
   const size_t row = (size_t)t * H;
-  constexpr int R = U ? U : 1;
-  float h[R][16], w[16];
+  float v[16];
   float ss = 0.f;
-  const bool keep_weight = U == 1 && weight && threadIdx.x < units;  // read beside x
-  if (keep_weight) load16<T>(weight, threadIdx.x * 16, w);
+  for (int u = threadIdx.x; u < units; u += threads) {
+    norm_load<T>(x, residual, row + u * 16, v);
 #pragma unroll
-  for (int k = 0; k < (U ? U : 1 << 30); ++k) {
-    const int u = threadIdx.x + 256 * k;
-    if (u >= units) break;
-    norm_load<T>(x, residual, row + u * 16, h[U ? k : 0]);
-#pragma unroll
-    for (int j = 0; j < 16; ++j) ss = fmaf(h[U ? k : 0][j], h[U ? k : 0][j], ss);
+    for (int j = 0; j < 16; ++j) ss = fmaf(v[j], v[j], ss);
+    if (KEEP) break;
   }
   ss = warp_sum(ss);
-  __shared__ float part[8];
+  __shared__ float part[32];
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = ss;
   __syncthreads();
   float tot = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) tot += part[i];
+  for (int i = 0; i < threads / 32; ++i) tot += part[i];
   const float inv = 1.0f / sqrtf(tot / (float)H + eps);
-#pragma unroll
-  for (int k = 0; k < (U ? U : 1 << 30); ++k) {
-    const int u = threadIdx.x + 256 * k;
-    if (u >= units) break;
-    float(&v)[16] = h[U ? k : 0];
-    if (!U) norm_load<T>(x, residual, row + u * 16, v);
+  for (int u = threadIdx.x; u < units; u += threads) {
+    if (!KEEP) norm_load<T>(x, residual, row + u * 16, v);
     if (residual_out) store16<T>(residual_out, row + u * 16, v);
 #pragma unroll
     for (int j = 0; j < 16; ++j) v[j] *= inv;
     if (weight) {
-      if (!keep_weight) load16<T>(weight, u * 16, w);
+      float w[16];
+      load16<T>(weight, u * 16, w);
 #pragma unroll
       for (int j = 0; j < 16; ++j) v[j] *= w[j];
     }
     const uint32_t s = mx_encode16<FMT>(v, codes, row + u * 16);
     if (!(u & 1)) scales[mx_scale_index(t, u >> 1, kt)] = (uint8_t)s;
+    if (KEEP) break;
   }
-  mx_zero_padding(scales, M, H, blockIdx.x * 256 + threadIdx.x, gridDim.x * 256);
+  if (H / 32 + (int)threadIdx.x < 4 * kt) scales[mx_scale_index(t, H / 32 + threadIdx.x, kt)] = 0;
 }
 
 template <typename T, int FMT>
 static cudaError_t launch_rmsnorm_t(const void* x, const void* residual, const void* weight, int M, int H, float eps,
                                     void* residual_out, uint8_t* codes, uint8_t* scales, cudaStream_t st) {
-  auto go = [&](auto kernel) {
-    return launch_kernel(kernel, dim3(M), dim3(256), 0, st, true, x, residual, weight, M, H, eps, residual_out, codes,
-                         scales);
-  };
-  if (H <= 4096) return go(mx_rmsnorm_kernel<T, FMT, 1>);
-  if (H <= 8192) return go(mx_rmsnorm_kernel<T, FMT, 2>);
-  return go(mx_rmsnorm_kernel<T, FMT, 0>);
+  const int threads = H > 16384 ? 1024 : (H / 16 + 31) / 32 * 32;
+  const uint32_t pad = (mx_padding_words(M, H) + 4 * threads - 1) / (4 * threads);
+  const long long grid = (long long)M + (pad < 64 ? pad : 64);
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+  return launch_kernel(H > 16384 ? mx_rmsnorm_kernel<T, FMT, false> : mx_rmsnorm_kernel<T, FMT, true>,
+                       dim3((unsigned)grid), dim3(threads), 0, st, true, x, residual, weight, M, H, eps, residual_out,
+                       codes, scales);
 }
 
 cudaError_t launch_mx_rmsnorm(const void* x, const void* residual, const void* weight, int act_dtype, int T, int H,

@@ -199,11 +199,15 @@ __device__ __forceinline__ uint32_t mx_encode16(float (&v)[16], uint8_t* codes, 
 __host__ __device__ __forceinline__ uint32_t mx_padding_words(int M, int K) {
   return (uint32_t)(-M & 127) * (uint32_t)((K + 127) / 128);
 }
-__device__ __forceinline__ void mx_zero_padding(uint8_t* scales, int M, int K, uint32_t thread, uint32_t n_threads) {
-  const int nb = K / 32, kt = (K + 127) / 128;
+__device__ __forceinline__ void mx_zero_rows(uint8_t* scales, int M, int K, uint32_t thread, uint32_t n_threads) {
+  const int kt = (K + 127) / 128;
   const uint32_t words = mx_padding_words(M, K), rows = (uint32_t)(-M & 127);
   for (uint32_t i = thread; i < words; i += n_threads)  // along the rows: neighbours in a tile
     *reinterpret_cast<uint32_t*>(scales + mx_scale_index(M + (int)(i % rows), 4 * (int)(i / rows), kt)) = 0u;
+}
+__device__ __forceinline__ void mx_zero_padding(uint8_t* scales, int M, int K, uint32_t thread, uint32_t n_threads) {
+  const int nb = K / 32, kt = (K + 127) / 128;
+  mx_zero_rows(scales, M, K, thread, n_threads);
   if (nb & 3)
     for (uint32_t r = thread; r < (uint32_t)M; r += n_threads)
       for (int b = nb; b < 4 * kt; ++b) scales[mx_scale_index((int)r, b, kt)] = 0;
