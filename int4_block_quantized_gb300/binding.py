@@ -367,6 +367,7 @@ def qmoe_unpack_zero_points(zp_packed, nb):
 # stream's handle read without building a torch.cuda.Stream (2.9 us on the
 # GB300's host cores), outputs from torch.empty (1.6 us; new_empty takes 3.4).
 
+_U8 = torch.uint8
 _MX_DT = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
 
 
@@ -375,10 +376,11 @@ def _bad(where, what):
 
 
 def _mx_rows(t, where):
-    """Shape of a contiguous 2-D CUDA tensor."""
-    if not t.is_cuda or t.dim() != 2 or not t.is_contiguous():
+    """(rows, columns, device index) of a contiguous 2-D CUDA tensor."""
+    shape, dev = t.shape, t.get_device()
+    if dev < 0 or len(shape) != 2 or not t.is_contiguous():
         _bad(where, "wants a contiguous 2-D CUDA tensor")
-    return t.shape
+    return shape[0], shape[1], dev
 
 
 def _mx_same(t, dev, dtype, numel, where, name):
@@ -389,39 +391,37 @@ def _mx_same(t, dev, dtype, numel, where, name):
 
 
 def _mx_tensor(codes, scales, fmt, where):
-    """(R, K) of an MX tensor."""
-    if codes.dtype != torch.uint8:
+    """(R, K, device index, address of the scales) of an MX tensor."""
+    R, K, dev = _mx_rows(codes, where)
+    if codes.dtype != _U8:
         _bad(where, "codes are uint8")
-    R, K = _mx_rows(codes, where)
     if fmt == MXFP4:
         K *= 2
     elif fmt != MXFP8:
         _bad(where, "unknown format %r" % (fmt,))
-    _mx_same(scales, codes.get_device(), torch.uint8, qmoe_mx_scale_bytes(R, K), where, "scales")
-    return R, K
+    return R, K, dev, _mx_same(scales, dev, _U8, qmoe_mx_scale_bytes(R, K), where, "scales")
 
 
-def _mx_out(R, K, fmt, x, codes, scales, where):
+def _mx_out(R, K, fmt, x, dev, codes, scales, where):
     """(codes, scales) to write an MX tensor [R, K] to: the caller's, or new ones."""
     n = qmoe_mx_scale_bytes(R, K)
     if n == 0 or (fmt != MXFP8 and fmt != MXFP4):
         _bad(where, "format %r, [%d, %d]: MXFP8 or MXFP4, rows and a multiple of 32 columns are wanted" % (fmt, R, K))
     cols = K if fmt == MXFP8 else K // 2
     if codes is None:
-        codes = torch.empty((R, cols), dtype=torch.uint8, device=x.device)
+        codes = torch.empty((R, cols), dtype=_U8, device=x.device)
     else:
-        _mx_same(codes, x.get_device(), torch.uint8, R * cols, where, "codes")
+        _mx_same(codes, dev, _U8, R * cols, where, "codes")
     if scales is None:
-        scales = torch.empty(n, dtype=torch.uint8, device=x.device)
+        scales = torch.empty(n, dtype=_U8, device=x.device)
     else:
-        _mx_same(scales, x.get_device(), torch.uint8, n, where, "scales")
+        _mx_same(scales, dev, _U8, n, where, "scales")
     return codes, scales
 
 
-def _mx_call(t, fn, where, *args):
-    """fn(*args, stream) on t's device and its current stream."""
-    dev = t.get_device()
-    if dev == torch.cuda.current_device():
+def _mx_call(dev, fn, where, *args):
+    """fn(*args, stream) on device dev and its current stream."""
+    if dev == torch._C._cuda_getDevice():
         rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
@@ -437,28 +437,27 @@ def qmoe_mx_scale_bytes(R, K):
 
 def qmoe_mx_quantize(x, fmt=MXFP8, codes=None, scales=None):
     """(codes, scales) of x [M, K] (fp16, bf16 or fp32) in MXFP8 or MXFP4."""
-    M, K = _mx_rows(x, "qmoe_mx_quantize")
+    M, K, dev = _mx_rows(x, "qmoe_mx_quantize")
     dt = _MX_DT.get(x.dtype)
     if dt is None:
         _bad("qmoe_mx_quantize", "unsupported input type %s" % x.dtype)
-    codes, scales = _mx_out(M, K, fmt, x, codes, scales, "qmoe_mx_quantize")
-    _mx_call(x, lib().qmoe_mx_quantize, "qmoe_mx_quantize", x.data_ptr(), dt, fmt, M, K, codes.data_ptr(),
+    codes, scales = _mx_out(M, K, fmt, x, dev, codes, scales, "qmoe_mx_quantize")
+    _mx_call(dev, lib().qmoe_mx_quantize, "qmoe_mx_quantize", x.data_ptr(), dt, fmt, M, K, codes.data_ptr(),
              scales.data_ptr())
     return codes, scales
 
 
 def qmoe_mx_dequant(codes, scales, fmt, dtype=torch.bfloat16, out=None):
     """[M, K] values (fp16, bf16 or fp32) of an MX tensor."""
-    M, K = _mx_tensor(codes, scales, fmt, "qmoe_mx_dequant")
+    M, K, dev, sp = _mx_tensor(codes, scales, fmt, "qmoe_mx_dequant")
     dt = _MX_DT.get(dtype)
     if dt is None:
         _bad("qmoe_mx_dequant", "unsupported output type %s" % dtype)
     if out is None:
         out = torch.empty((M, K), dtype=dtype, device=codes.device)
     else:
-        _mx_same(out, codes.get_device(), dtype, M * K, "qmoe_mx_dequant", "out")
-    _mx_call(codes, lib().qmoe_mx_dequant, "qmoe_mx_dequant", codes.data_ptr(), scales.data_ptr(), fmt, M, K,
-             out.data_ptr(), dt)
+        _mx_same(out, dev, dtype, M * K, "qmoe_mx_dequant", "out")
+    _mx_call(dev, lib().qmoe_mx_dequant, "qmoe_mx_dequant", codes.data_ptr(), sp, fmt, M, K, out.data_ptr(), dt)
     return out
 
 
@@ -467,11 +466,11 @@ def qmoe_rmsnorm_mx(x, residual=None, weight=None, eps=1e-6, fmt=MXFP8, residual
     or MXFP4; residual_out = x + residual (a new tensor unless given; it may be
     x or residual itself).  Without a residual it is None unless given."""
     where = "qmoe_rmsnorm_mx"
-    T, H = _mx_rows(x, where)
-    dt, dev = x.dtype, x.get_device()
+    T, H, dev = _mx_rows(x, where)
+    dt = x.dtype
     if dt != torch.float16 and dt != torch.bfloat16:
         _bad(where, "unsupported input type %s" % dt)
-    codes, scales = _mx_out(T, H, fmt, x, codes, scales, where)
+    codes, scales = _mx_out(T, H, fmt, x, dev, codes, scales, where)
     rp = wp = op = None
     if residual is not None:
         rp = _mx_same(residual, dev, dt, T * H, where, "residual")
@@ -481,7 +480,7 @@ def qmoe_rmsnorm_mx(x, residual=None, weight=None, eps=1e-6, fmt=MXFP8, residual
         op = _mx_same(residual_out, dev, dt, T * H, where, "residual_out")
     if weight is not None:
         wp = _mx_same(weight, dev, dt, H, where, "weight")
-    _mx_call(x, lib().qmoe_rmsnorm_mx, where, x.data_ptr(), rp, wp, _MX_DT[dt], T, H, float(eps), fmt, op,
+    _mx_call(dev, lib().qmoe_rmsnorm_mx, where, x.data_ptr(), rp, wp, _MX_DT[dt], T, H, float(eps), fmt, op,
              codes.data_ptr(), scales.data_ptr())
     return codes, scales, residual_out
 
@@ -491,10 +490,9 @@ def qmoe_mx_matmul(x_codes, x_scales, x_fmt, w_codes, w_scales, dtype=torch.bflo
     weights W [N, K].  status: an int32 [1] device tensor that collects
     QMOE_ST_TIMEOUT (zero it first)."""
     where = "qmoe_mx_matmul"
-    M, K = _mx_tensor(x_codes, x_scales, x_fmt, where)
-    N, KW = _mx_tensor(w_codes, w_scales, MXFP4, where)
-    dev = x_codes.get_device()
-    if K != KW or w_codes.get_device() != dev:
+    M, K, dev, xs = _mx_tensor(x_codes, x_scales, x_fmt, where)
+    N, KW, dev_w, ws = _mx_tensor(w_codes, w_scales, MXFP4, where)
+    if K != KW or dev_w != dev:
         _bad(where, "x has %d columns on %s, W has %d on %s" % (K, x_codes.device, KW, w_codes.device))
     dt = _MX_DT.get(dtype)
     if dt is None:
@@ -503,21 +501,21 @@ def qmoe_mx_matmul(x_codes, x_scales, x_fmt, w_codes, w_scales, dtype=torch.bflo
         out = torch.empty((M, N), dtype=dtype, device=x_codes.device)
     else:
         _mx_same(out, dev, dtype, M * N, where, "out")
-    sp = None if status is None else _mx_same(status, dev, torch.int32, 1, where, "status")
-    _mx_call(x_codes, lib().qmoe_mx_matmul, where, x_codes.data_ptr(), x_scales.data_ptr(), x_fmt, w_codes.data_ptr(),
-             w_scales.data_ptr(), M, N, K, out.data_ptr(), dt, sp)
+    st = None if status is None else _mx_same(status, dev, torch.int32, 1, where, "status")
+    _mx_call(dev, lib().qmoe_mx_matmul, where, x_codes.data_ptr(), xs, x_fmt, w_codes.data_ptr(), ws, M, N, K,
+             out.data_ptr(), dt, st)
     return out
 
 
 def qmoe_mx_tile_scales(scales_rowmajor):
     """Row-major scale bytes [R, K/32] (as checkpoints store them) -> tiles."""
     where = "qmoe_mx_tile_scales"
-    R, nb = _mx_rows(scales_rowmajor, where)
+    R, nb, dev = _mx_rows(scales_rowmajor, where)
     n = qmoe_mx_scale_bytes(R, 32 * nb)
     if n == 0 or scales_rowmajor.dtype != torch.uint8:
         _bad(where, "wants uint8 scales [R, K/32]")
     out = torch.empty(n, dtype=torch.uint8, device=scales_rowmajor.device)
-    _mx_call(out, lib().qmoe_mx_tile_scales, where, scales_rowmajor.data_ptr(), R, 32 * nb, out.data_ptr())
+    _mx_call(dev, lib().qmoe_mx_tile_scales, where, scales_rowmajor.data_ptr(), R, 32 * nb, out.data_ptr())
     return out
 
 
@@ -529,5 +527,5 @@ def qmoe_mx_untile_scales(scales, R, K):
         _bad(where, "wants CUDA scale tiles of an MX tensor, got [%d, %d]" % (R, K))
     _mx_same(scales, scales.get_device(), torch.uint8, n, where, "scales")
     out = torch.empty((R, K // 32), dtype=torch.uint8, device=scales.device)
-    _mx_call(out, lib().qmoe_mx_untile_scales, where, scales.data_ptr(), R, K, out.data_ptr())
+    _mx_call(scales.get_device(), lib().qmoe_mx_untile_scales, where, scales.data_ptr(), R, K, out.data_ptr())
     return out
