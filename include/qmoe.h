@@ -401,8 +401,8 @@ int qmoe_unpack_zero_points(const uint8_t* zp_packed, int rows, int nb, uint8_t*
  *           tiles are copied there as they are.  Bytes for rows >= R and
  *           blocks >= K/32 are padding: the calls below write zeros there.
  *           qmoe_mx_scale_bytes(R, K) gives the size.
- * An element's value is code * X.  Every codes and scales pointer is 16-byte
- * aligned; codes, scales, inputs and outputs of one call must not overlap
+ * An element's value is code * X.  R and K are at most 2^30
+ * (QMOE_ERR_UNSUPPORTED).  Every codes and scales pointer is 16-byte aligned; codes, scales, inputs and outputs of one call must not overlap
  * (qmoe_rmsnorm_mx's residual_out is the exception). */
 typedef enum { QMOE_MXFP8 = 0, QMOE_MXFP4 = 1 } qmoe_mx_format;
 
@@ -442,7 +442,10 @@ int qmoe_rmsnorm_mx(const void* x, const void* residual, const void* weight, int
  * x_format (MXFP8 or MXFP4), W an MXFP4 tensor [N, K]; products are exact,
  * sums are fp32, and y is rounded once to y_dtype (fp16, bf16 or fp32;
  * y aligned to its element size).  Any M and N >= 1.  A NaN scale makes the
- * outputs of its row NaN.  status_dev (a 4-byte device word that the caller
+ * outputs of its row NaN; the scales' padding behind K has to be zeros (the
+ * calls here write it so), that behind the last row may be anything.
+ * One kernel; the choice of its tile and the split of K go by M, N and K
+ * alone, and results are the same in every call.  status_dev (a 4-byte device word that the caller
  * set to 0, or NULL): a bounded wait of the kernel that ran out sets
  * QMOE_ST_TIMEOUT there (y is then undefined); read it with
  * qmoe_get_device_status(status_dev, ...). */

@@ -47,7 +47,8 @@ int check_qweight(const qmoe_qweight& q, int N, int K, int bs) {
 int check_mx(const uint8_t* codes, const uint8_t* scales, int format, int R, int K) {
   if (!codes || !scales || !aligned(codes, 16) || !aligned(scales, 16)) return QMOE_ERR_INVALID_ARG;
   if (format != QMOE_MXFP8 && format != QMOE_MXFP4) return QMOE_ERR_INVALID_ARG;
-  return R < 1 || K < 32 || K % 32 ? QMOE_ERR_INVALID_ARG : QMOE_OK;
+  if (R < 1 || K < 32 || K % 32) return QMOE_ERR_INVALID_ARG;
+  return R > (1 << 30) || K > (1 << 30) ? QMOE_ERR_UNSUPPORTED : QMOE_OK;  // tile counts stay in 32 bits
 }
 
 thread_local cudaError_t g_last_cuda_error = cudaSuccess;

@@ -259,8 +259,8 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
       if (!ok) break;
       tc_fence_after();
       const uint32_t d = tmem + (b ? P::kAcc1 : 0);
-      // BN = 64: an odd token tile starts in the middle of its scale tile
-      const uint32_t sfb = tmem + P::kSfb + (BN == 64 ? 2 * (tt & 1) : 0);
+      // 64 or 192 tokens: an odd token tile starts in the middle of a scale tile
+      const uint32_t sfb = tmem + P::kSfb + (BN % 128 == 64 ? 2 * (tt & 1) : 0);
       // one stage: its scales, then its MMAs (the first `words` scale words and
       // `mmas` instructions: fewer only where K ends)
       auto issue = [&](int slot, bool first_stage, int words, int mmas) {
@@ -558,35 +558,43 @@ static int mm_capacity(int split) {
 
 // Tokens per tile (and a pair of CTAs or one) and CTAs per tile along K, by an
 // estimate of the time in ns: a start, the stages of the CTA with the most
-// tiles, what each further tile adds beyond its MMAs, and the exchange of a
-// split tile's sums.  The constants are fits to measured kernel times on GB300
-// (us; x in MXFP8; tokens a tile / CTAs along K, 2 x 256 a pair):
+// tiles, what each further tile adds beyond its MMAs (at least its epilogue's
+// time in all, which short K leave bare), and the exchange of a split tile's
+// sums.  The constants are fits to measured kernel times on GB300
+// (us; x in MXFP8; tokens a tile / CTAs along K, 2 x for a pair):
 //     16 x 1408 x 2048    16/8 3.9   16/4 4.0   16/2 4.4   16/1 4.7
 //     64 x 2048 x 5632    64/4 6.0   64/2 7.6   64/1 9.6   128/4 7.1  128/1 9.9
-//    512 x 1408 x 2048    64/1 5.4   128/1 5.9  128/2 8.0  256/1 8.6  2x256/1 9.1
-//   2048 x 1408 x 2048    256/1 9.5  128/1 9.7  2x256/1 10.1  64/1 11.5
-//    512 x 8192 x 8192    2x256/1 24  256/1 27  128/1 28   64/1 46
-//   2048 x 11264 x 2048   2x256/1 33  256/1 35  128/1 39   64/1 59
+//    512 x 1408 x 2048    64/1 5.3   128/1 6.0  192/1 7.3  2x192/1 7.8  2x256/1 9.1
+//   2048 x 1408 x 2048    192/1 8.0  2x192/1 8.6  128/1 9.7  2x256/1 9.9  64/1 11.4
+//    512 x 8192 x 8192    2x256/1 24  128/1 28  2x192/1 33  192/1 35  64/1 46
+//   2048 x 8192 x 8192    2x192/1 82  192/1 85  2x256/1 87  128/1 89  64/1 154
+//   2048 x 11264 x 2048   2x192/1 33  2x256/1 34  192/1 37  128/1 39  64/1 59
+//   4085 x 3895 x 512 (x in MXFP4)  128/1 13.1  192/1 13.4  64/1 13.9  2x256/1 15.4  2x192/1 16.9
+// (192 tokens: two whole accumulators fit tensor memory; at 256 the next tile's
+// first MMA waits until the epilogue has taken the shared columns.)
 struct MmChoice {
   int bn, cg, split;
 };
 static MmChoice mm_choose(int M, int N, int chunks, bool fill) {
   static const struct {
-    int bn, cg, start, stage, tile, exchange;
-  } kinds[] = {{16, 1, 1900, 170, 300, 1200},  {32, 1, 2000, 170, 350, 1300}, {64, 1, 2900, 165, 500, 1400},
-               {128, 1, 3600, 185, 1200, 2200}, {256, 1, 4000, 340, 1800, 0},  {256, 2, 4600, 300, 1500, 0}};
+    int bn, cg, start, stage, tile, epilogue, exchange;
+  } kinds[] = {{16, 1, 1900, 170, 300, 200, 1200},   {32, 1, 2000, 170, 350, 300, 1300},
+               {64, 1, 2900, 165, 500, 850, 1400},   {128, 1, 3600, 185, 1200, 1350, 2900},
+               {192, 1, 3900, 250, 500, 1900, 0},    {192, 2, 4200, 240, 300, 2500, 0},
+               {256, 2, 4600, 300, 1500, 2700, 0}};
   MmChoice best = {128, 1, 1};
   long long least = -1;
   for (const auto& k : kinds) {
     if (k.bn < 64 && M > k.bn) continue;  // 16 and 32 tokens: a single tile, at the head of its scale tile
     if (k.cg == 2 && fill) continue;
-    const int stage = fill ? 2 * k.stage : k.stage;  // weights by loads and stores: 340 ns at 16 to 128 tokens
+    const int stage = fill ? 450 : k.stage;  // weights by loads and stores: 340 to 560 ns whatever the tokens
     const long long tiles = (long long)((N + 128 * k.cg - 1) / (128 * k.cg)) * ((M + k.bn - 1) / k.bn);
     for (int split = 1; split <= 8; split *= 2) {
       if (split > 1 && (!k.exchange || split > chunks || tiles * split > mm_capacity(split))) break;
       const long long slots = split > 1 ? tiles : device_sm_count() / k.cg;
       const long long rounds = (tiles + slots - 1) / slots;
-      const long long t = k.start + rounds * ((chunks + split - 1) / split) * stage + (rounds - 1) * k.tile +
+      const long long one = (long long)((chunks + split - 1) / split) * stage, more = one + k.tile;
+      const long long t = k.start + one + (rounds - 1) * (more > k.epilogue ? more : k.epilogue) +
                           (split > 1 ? k.exchange : 0);
       if (least < 0 || t < least) {
         least = t;
@@ -606,11 +614,12 @@ static cudaError_t launch_mm_bn(const MmParams& p, const uint8_t* xc, cudaStream
     case 32: return launch_mm<XF, 32, 1, FILL>(p, c.split, xc, st);
     case 64: return launch_mm<XF, 64, 1, FILL>(p, c.split, xc, st);
     case 128: return launch_mm<XF, 128, 1, FILL>(p, c.split, xc, st);
-    default:
-      if constexpr (!FILL)
-        if (c.cg == 2) return launch_mm<XF, 256, 2, false>(p, 1, xc, st);
-      return launch_mm<XF, 256, 1, FILL>(p, 1, xc, st);
   }
+  if constexpr (!FILL) {
+    if (c.bn == 256) return launch_mm<XF, 256, 2, false>(p, 1, xc, st);
+    if (c.cg == 2) return launch_mm<XF, 192, 2, false>(p, 1, xc, st);
+  }
+  return launch_mm<XF, 192, 1, FILL>(p, 1, xc, st);
 }
 
 cudaError_t launch_mx_matmul(const uint8_t* xc, const uint8_t* xs, int x_format, const uint8_t* wc, const uint8_t* ws,

@@ -54,6 +54,16 @@ def test_matmul_refuses(L, kw):
                             a["st"], None) == 1
 
 
+def test_sizes_beyond_2_30_are_unsupported(L):
+    big = (1 << 30) + 32
+    for R, K in ((big, 64), (4, big)):
+        assert L.qmoe_mx_quantize(FAKE, 0, 0, R, K, FAKE, FAKE, None) == 2
+        assert L.qmoe_mx_dequant(FAKE, FAKE, 0, R, K, FAKE, 0, None) == 2
+        assert L.qmoe_rmsnorm_mx(FAKE, None, None, 0, R, K, 0.0, 0, None, FAKE, FAKE, None) == 2
+        assert L.qmoe_mx_matmul(FAKE, FAKE, 0, FAKE, FAKE, R, 8, K, FAKE, 0, None, None) == 2
+    assert L.qmoe_mx_matmul(FAKE, FAKE, 0, FAKE, FAKE, 8, big, 64, FAKE, 0, None, None) == 2
+
+
 @pytest.mark.parametrize("kw", [dict(i=None), dict(o=None), dict(R=0), dict(K=33)])
 def test_scale_adapters_refuse(L, kw):
     a = dict(i=FAKE, o=FAKE, R=4, K=64)

@@ -8,6 +8,10 @@ y (1 -+ that).  A product of two elements is exact in fp32; a sum of K of them
 in any order, each addition off by at most a whole step, is off by at most
 K 2^-23 times the sum of magnitudes, and the result is rounded once (half a
 step of the output's type)."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -16,6 +20,7 @@ from int4_block_quantized_gb300 import binding as B
 from oracle import mx
 
 pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 DEV = "cuda"
 DT = [torch.float16, torch.bfloat16, torch.float32]
 FMT = [B.MXFP8, B.MXFP4]
@@ -224,7 +229,8 @@ def test_matmul_few_tokens(M, N, K, xf, dtype):
 @pytest.mark.parametrize("xf", FMT)
 @pytest.mark.parametrize("M,N,K", [(16, 512, 1024), (17, 130, 416), (31, 384, 2048), (32, 256, 256), (33, 256, 5632),
                                    (64, 127, 512), (65, 129, 1408), (127, 255, 320), (128, 128, 640), (129, 257, 768),
-                                   (200, 640, 2048), (333, 411, 1440), (512, 1408, 2048), (700, 300, 128)])
+                                   (200, 640, 2048), (333, 411, 1440), (512, 1408, 2048), (700, 300, 128), (1, 1, 128),
+                                   (344, 62, 2912), (1019, 68, 4160), (400, 30, 4096), (2100, 130, 96)])
 def test_matmul_tiles(M, N, K, xf):
     run_product(M, N, K, xf, (torch.float32, torch.bfloat16, torch.float16)[(M + N) % 3], M + N + K)
 
@@ -330,6 +336,51 @@ def test_matmul_is_reproducible_on_streams_and_in_graphs(M, N, K, xf):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, ref)
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    """Nothing of the operators needs a call before the capture."""
+    code = """
+import sys; sys.path.insert(0, %r)
+import torch
+from int4_block_quantized_gb300 import binding as B
+g = torch.Generator(device="cuda").manual_seed(1)
+x, r, w = (torch.randn(s, generator=g, device="cuda").half() for s in ((5, 512), (5, 512), (300, 512)))
+graph = torch.cuda.CUDAGraph()
+def run():
+    c, s, total = B.qmoe_rmsnorm_mx(x, r)
+    wc, ws = B.qmoe_mx_quantize(w, B.MXFP4)
+    return total, B.qmoe_mx_matmul(c, s, B.MXFP8, wc, ws), B.qmoe_mx_dequant(wc, ws, B.MXFP4), B.qmoe_mx_untile_scales(ws, 300, 512)
+with torch.cuda.graph(graph):
+    out = run()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(out, run()))
+""" % ROOT
+    subprocess.run([sys.executable, "-c", code], check=True, timeout=300)
+
+
+def test_graphs_on_two_streams_at_once():
+    """Two captured graphs share weights and run side by side."""
+    M, N, K = 40, 1408, 2048
+    w = to_dev(*random_mx(N, K, B.MXFP4, 2), B.MXFP4)
+    xs = [to_dev(*random_mx(M, K, B.MXFP8, 3 + i), B.MXFP8) for i in range(2)]
+    ref = [B.qmoe_mx_matmul(*x, B.MXFP8, *w) for x in xs]
+    graphs, outs = [], []
+    for x in xs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(B.qmoe_mx_matmul(*x, B.MXFP8, *w))
+        graphs.append(g)
+    side = [torch.cuda.Stream() for _ in range(2)]
+    for s in side:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        for g, s in zip(graphs, side):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, ref))
 
 
 # ------------------------------------------------------------------ together
