@@ -375,31 +375,53 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
     }
   } else if (FILL) {
     // -------------------------------------- weights of ragged rows (MXFP8 x)
-    const int r = tid - kMmThreads;  // row of the tile
-    int it = 0, s = 0;
+    // A warp takes 32 rows, four lanes the 64 bytes of a row's stage (8 rows of
+    // two whole sectors per load: with a row per lane a load touches 32 lines,
+    // and 64 rows by 128 tokens took 340 ns a stage).  Loads run three stages
+    // ahead of their stores.
+    const int r0 = (warp - kMmThreads / 32) * 32 + (lane >> 2), piece = lane & 3;
+    int s = 0;
     uint32_t ph = 0;
-    bool ok = true;
-    for (int t = first; t < tiles && ok; t += step) {
-      int rt, tt;
-      mm_tile(p, t, rt, tt);
-      const int nn = rt * 128 + r;
-      const uint8_t* src = p.wc + (size_t)nn * (p.K / 2);
-      for (int c = c0; c < c1; ++c, ++it) {
-        uint4 v[4];
+    const int nc = c1 - c0, mine = first < tiles ? (tiles - 1 - first) / step + 1 : 0;
+    const long long total = (long long)mine * nc;
+    long long loaded = 0;
+    int lt = first, lc = c0, lrt = 0, ltt = 0;  // the next stage to load
+    if (mine) mm_tile(p, lt, lrt, ltt);
+    auto load = [&](uint4(&v)[4]) {
+      if (loaded >= total) return;
+      const int k = lc * 128 + piece * 32;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)  // 32 codes each
-          v[i] = nn < p.N && c * 128 + i * 32 < p.K ? __ldg(reinterpret_cast<const uint4*>(src + c * 64 + i * 16))
-                                                    : make_uint4(0, 0, 0, 0);
-        if (it >= S && !mm_wait(&empty[s], ph ^ 1u, p.status, s_abort)) {
-          ok = false;
-          break;
-        }
-        uint8_t* st = ring + s * P::kAb + r * 128;
+      for (int i = 0; i < 4; ++i) {
+        const int nn = lrt * 128 + r0 + 8 * i;
+        v[i] = nn < p.N && k < p.K ? __ldg(reinterpret_cast<const uint4*>(p.wc + (size_t)nn * (p.K / 2) + k / 2))
+                                   : make_uint4(0, 0, 0, 0);
+      }
+      ++loaded;
+      if (++lc == c1) {
+        lc = c0;
+        lt += step;
+        if (lt < tiles) mm_tile(p, lt, lrt, ltt);
+      }
+    };
+    uint4 v[3][4];
+#pragma unroll
+    for (int q = 0; q < 3; ++q) load(v[q]);
+    bool ok = true;
+    for (long long it = 0; it < total && ok; it += 3) {
+#pragma unroll
+      for (int q = 0; q < 3; ++q) {
+        if (it + q >= total) break;
+        if (it + q >= S) ok = mm_wait(&empty[s], ph ^ 1u, p.status, s_abort);
+        if (!ok) break;
+        uint8_t* st = ring + s * P::kAb;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          *reinterpret_cast<uint4*>(st + (((2 * i) ^ (r & 7)) << 4)) = make_uint4(v[i].x, v[i].y, 0, 0);
-          *reinterpret_cast<uint4*>(st + (((2 * i + 1) ^ (r & 7)) << 4)) = make_uint4(v[i].z, v[i].w, 0, 0);
+          const int r = r0 + 8 * i;
+          *reinterpret_cast<uint4*>(st + r * 128 + (((2 * piece) ^ (r & 7)) << 4)) = make_uint4(v[q][i].x, v[q][i].y, 0, 0);
+          *reinterpret_cast<uint4*>(st + r * 128 + (((2 * piece + 1) ^ (r & 7)) << 4)) =
+              make_uint4(v[q][i].z, v[q][i].w, 0, 0);
         }
+        load(v[q]);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[s]);
