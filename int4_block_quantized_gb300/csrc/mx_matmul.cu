@@ -20,7 +20,7 @@
 namespace qmoe {
 
 constexpr int kMmThreads = 352;       // warps 0 and 6 copy, warp 1 issues MMAs, warps 2-5 and 7-10 write y
-constexpr int kMmFillThreads = 480;   // + warps 11-14: weights by loads and stores (see FILL)
+constexpr int kMmFillThreads = 608;   // + warps 11-18: weights by loads and stores (see FILL)
 constexpr uint32_t kMmSmem = 232448;  // 227 KB
 constexpr uint32_t kMmBars = 1024;
 
@@ -125,7 +125,7 @@ __device__ __forceinline__ void mm_tile(const MmParams& p, int t, int& rt, int& 
 
 // FILL (MXFP8 x only): the TMA copy that widens e2m1 codes wants rows of a
 // multiple of 128 codes on 32-byte boundaries; other weights are read and
-// spread by four warps.
+// spread by eight warps.
 template <int XF, int BN, int CG, bool FILL>
 __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
     mx_matmul_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
@@ -375,18 +375,25 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
     }
   } else if (FILL) {
     // -------------------------------------- weights of ragged rows (MXFP8 x)
-    // A warp takes 32 rows, four lanes the 64 bytes of a row's stage (8 rows of
-    // two whole sectors per load: with a row per lane a load touches 32 lines,
-    // and 64 rows by 128 tokens took 340 ns a stage).  Loads run three stages
-    // ahead of their stores.
-    const int r0 = (warp - kMmThreads / 32) * 32 + (lane >> 2), piece = lane & 3;
-    int s = 0;
-    uint32_t ph = 0;
+    // Two groups of four warps take turns at the stages; a warp takes 32 rows,
+    // four lanes the 64 bytes of a row's stage (8 rows of two whole sectors per
+    // load; with a row per lane a load touches 32 lines).  Loads run three of
+    // the group's stages ahead of their stores.  3272 x 3655 x 3232 takes 44 us
+    // so, 47 with one group, 62 with a row per lane and one stage ahead.
+    const int group = warp >= kMmThreads / 32 + 4;
+    const int r0 = ((warp - kMmThreads / 32) & 3) * 32 + (lane >> 2), piece = lane & 3;
     const int nc = c1 - c0, mine = first < tiles ? (tiles - 1 - first) / step + 1 : 0;
     const long long total = (long long)mine * nc;
-    long long loaded = 0;
-    int lt = first, lc = c0, lrt = 0, ltt = 0;  // the next stage to load
-    if (mine) mm_tile(p, lt, lrt, ltt);
+    long long loaded = group;
+    int lt = first, lc = c0 + group, lrt = 0, ltt = 0;  // the next stage to load
+    auto settle = [&]() {
+      while (lc >= c1) {
+        lc -= nc;
+        lt += step;
+      }
+      if (lt < tiles) mm_tile(p, lt, lrt, ltt);
+    };
+    settle();
     auto load = [&](uint4(&v)[4]) {
       if (loaded >= total) return;
       const int k = lc * 128 + piece * 32;
@@ -396,22 +403,22 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
         v[i] = nn < p.N && k < p.K ? __ldg(reinterpret_cast<const uint4*>(p.wc + (size_t)nn * (p.K / 2) + k / 2))
                                    : make_uint4(0, 0, 0, 0);
       }
-      ++loaded;
-      if (++lc == c1) {
-        lc = c0;
-        lt += step;
-        if (lt < tiles) mm_tile(p, lt, lrt, ltt);
-      }
+      loaded += 2;
+      lc += 2;
+      if (lc >= c1) settle();
     };
     uint4 v[3][4];
 #pragma unroll
     for (int q = 0; q < 3; ++q) load(v[q]);
+    int s = group;
+    uint32_t ph = 0;
     bool ok = true;
-    for (long long it = 0; it < total && ok; it += 3) {
+    for (long long it = group; it < total && ok; it += 6) {
 #pragma unroll
       for (int q = 0; q < 3; ++q) {
-        if (it + q >= total) break;
-        if (it + q >= S) ok = mm_wait(&empty[s], ph ^ 1u, p.status, s_abort);
+        const long long n = it + 2 * q;
+        if (n >= total) break;
+        if (n >= S) ok = mm_wait(&empty[s], ph ^ 1u, p.status, s_abort);
         if (!ok) break;
         uint8_t* st = ring + s * P::kAb;
 #pragma unroll
@@ -425,8 +432,9 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[s]);
-        if (++s == S) {
-          s = 0;
+        s += 2;
+        if (s >= S) {
+          s -= S;
           ph ^= 1u;
         }
       }
@@ -609,7 +617,7 @@ static MmChoice mm_choose(int M, int N, int chunks, bool fill) {
   for (const auto& k : kinds) {
     if (k.bn < 64 && M > k.bn) continue;  // 16 and 32 tokens: a single tile, at the head of its scale tile
     if (k.cg == 2 && fill) continue;
-    const int stage = fill ? 450 : k.stage;  // weights by loads and stores: 340 to 560 ns whatever the tokens
+    const int stage = fill ? 230 + k.bn : k.stage;  // weights by loads and stores: 240 ns at 16 tokens, 420 at 192
     const long long tiles = (long long)((N + 128 * k.cg - 1) / (128 * k.cg)) * ((M + k.bn - 1) / k.bn);
     for (int split = 1; split <= 8; split *= 2) {
       if (split > 1 && (!k.exchange || split > chunks || tiles * split > mm_capacity(split))) break;
