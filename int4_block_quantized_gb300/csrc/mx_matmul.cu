@@ -113,7 +113,6 @@ __device__ __forceinline__ void mm_store_cols(const MmParams& p, size_t i, int r
   }
 }
 
-
 // Tile t of the grid: groups of 8 row tiles, so that the tiles in flight share
 // weights and tokens in L2.
 __device__ __forceinline__ void mm_tile(const MmParams& p, int t, int& rt, int& tt) {

@@ -338,6 +338,55 @@ def test_matmul_is_reproducible_on_streams_and_in_graphs(M, N, K, xf):
         assert torch.equal(out, ref)
 
 
+def at_16(t):
+    """A copy of t that starts on a 16-byte boundary and on no 32-byte one."""
+    n = 16 // t.element_size()
+    buf = torch.empty(t.numel() + 2 * n, dtype=t.dtype, device=DEV)
+    return buf[n:n + t.numel()].view(t.shape).copy_(t)
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("dtype", DT)
+def test_streams_on_16_byte_boundaries(dtype, fmt):
+    """Every pointer off a 32-byte boundary gives what aligned ones give."""
+    M, K = 37, 416
+    x, r = make(M, K, 1, dtype).to(DEV), make(M, K, 2, dtype).to(DEV)
+    ref = B.qmoe_mx_quantize(x, fmt)
+    out = tuple(at_16(t) for t in ref)
+    got = B.qmoe_mx_quantize(at_16(x), fmt, codes=out[0].zero_(), scales=out[1].zero_())
+    assert got[0].data_ptr() % 32 == 16 and all(torch.equal(a, b) for a, b in zip(got, ref))
+    v = B.qmoe_mx_dequant(*ref, fmt, dtype)
+    assert torch.equal(B.qmoe_mx_dequant(*got, fmt, dtype, out=at_16(torch.zeros_like(v))), v)
+    if dtype != torch.float32:
+        w = make(1, K, 3, dtype).to(DEV)[0]
+        ref = B.qmoe_rmsnorm_mx(x, r, w, fmt=fmt)
+        got = B.qmoe_rmsnorm_mx(at_16(x), at_16(r), at_16(w), fmt=fmt, residual_out=at_16(x), codes=at_16(ref[0]).zero_(),
+                                scales=at_16(ref[1]).zero_())
+        assert all(torch.equal(a, b) for a, b in zip(got, ref))
+
+
+@pytest.mark.parametrize("xf", FMT)
+@pytest.mark.parametrize("M,N,K", [(5, 300, 512), (150, 700, 1024), (2700, 1900, 256)])
+def test_matmul_on_16_byte_boundaries(M, N, K, xf):
+    """Weights off a 32-byte boundary take the other way in; sums are in another
+    order only where the split of K differs, so fp32 results agree to rounding."""
+    x, w = to_dev(*random_mx(M, K, xf, 4), xf), to_dev(*random_mx(N, K, B.MXFP4, 5), B.MXFP4)
+    xc, xs = random_mx(M, K, xf, 4)
+    wc, ws = random_mx(N, K, B.MXFP4, 5)
+    y = B.qmoe_mx_matmul(at_16(x[0]), at_16(x[1]), xf, at_16(w[0]), at_16(w[1]), torch.float32)
+    check_product(xc, xs, xf, wc, ws, y, torch.float32)
+
+
+@pytest.mark.parametrize("M", [2, 70])
+def test_matmul_nan_code_spoils_its_row(M):
+    """e4m3 has a NaN code; the product's row is NaN, the others are not."""
+    N, K = 140, 256
+    xc, xs = random_mx(M, K, B.MXFP8, 6)
+    xc[M - 1, 77] = 0xff
+    y = f64(B.qmoe_mx_matmul(*to_dev(xc, xs, B.MXFP8), B.MXFP8, *to_dev(*random_mx(N, K, B.MXFP4, 7), B.MXFP4), torch.float32))
+    assert np.isnan(y[M - 1]).all() and np.isfinite(y[:M - 1]).all()
+
+
 def test_first_calls_of_a_process_inside_a_capture():
     """Nothing of the operators needs a call before the capture."""
     code = """
