@@ -6,6 +6,8 @@
 // (MXFP4, even k in the low nibble); an element is code * X.
 #pragma once
 
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace qmoe {
@@ -131,6 +133,20 @@ __device__ __forceinline__ void load16(const void* base, size_t i, float (&v)[16
     }
   }
 }
+// sixteen values rounded to a 16-bit type
+template <typename T>
+__device__ __forceinline__ void pack16(const float (&v)[16], uint32_t (&w)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+      w[j] = *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+      const __half2 h = __floats2half2_rn(v[2 * j], v[2 * j + 1]);
+      w[j] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+}
 template <typename T>
 __device__ __forceinline__ void store16(void* base, size_t i, const float (&v)[16]) {
   uint8_t* p = static_cast<uint8_t*>(base) + i * sizeof(T);
@@ -143,9 +159,7 @@ __device__ __forceinline__ void store16(void* base, size_t i, const float (&v)[1
       store32(p + 32 * q, w);
     }
   } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      w[j] = (uint32_t)Half<T>::from_float(v[2 * j]) | ((uint32_t)Half<T>::from_float(v[2 * j + 1]) << 16);
+    pack16<T>(v, w);
     store32(p, w);
   }
 }
@@ -171,25 +185,56 @@ struct RowWalk {
 };
 
 // Half a block per thread, the other half in the neighbouring lane (lane ^
-// 1): the block's scale byte, and this half's codes stored at element i.
-// Both lanes of a pair call it.
+// 1).  Both lanes of a pair call these.
+__device__ __forceinline__ uint32_t mx_pair_mask() { return 3u << (threadIdx.x & 30); }
+// The largest magnitude of the block, as bits; NaN where the block has one.
+__device__ __forceinline__ uint32_t mx_block_max(const float (&v)[16]) {
+  float m = 0.f;
+#pragma unroll
+  for (int j = 0; j < 16; j += 2)
+    asm("max.NaN.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(fabsf(v[j])), "f"(fabsf(v[j + 1])));
+  const uint32_t b = __float_as_uint(m);
+  return max(b, __shfl_xor_sync(mx_pair_mask(), b, 1));
+}
+// Codes of sixteen values times `scale`.
 template <int FMT>
-__device__ __forceinline__ uint32_t mx_encode16(float (&v)[16], uint8_t* codes, size_t i) {
-  const uint32_t mask = 3u << (threadIdx.x & 30);
-  uint32_t m = 0;
+struct MxCodes {
+  uint32_t w[FMT == kMxfp8 ? 4 : 2];
+  __device__ __forceinline__ void set(const float (&v)[16], float scale) {
+    float u[8];
 #pragma unroll
-  for (int j = 0; j < 16; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
-  m = max(m, __shfl_xor_sync(mask, m, 1));
-  const uint32_t s = mx_scale_byte<FMT>(m);
-  const float inv = s == 255u ? 0.f : mx_inv_scale(s);
+    for (int h = 0; h < 2; ++h) {
 #pragma unroll
-  for (int j = 0; j < 16; ++j) v[j] = s == 255u ? 0.f : v[j] * inv;
-  if constexpr (FMT == kMxfp8)
-    *reinterpret_cast<uint4*>(codes + i) =
-        make_uint4(mx_e4m3x4(v[0], v[1], v[2], v[3]), mx_e4m3x4(v[4], v[5], v[6], v[7]),
-                   mx_e4m3x4(v[8], v[9], v[10], v[11]), mx_e4m3x4(v[12], v[13], v[14], v[15]));
-  else
-    *reinterpret_cast<uint2*>(codes + i / 2) = make_uint2(mx_e2m1x8(v), mx_e2m1x8(v + 8));
+      for (int j = 0; j < 8; ++j) u[j] = v[8 * h + j] * scale;
+      if constexpr (FMT == kMxfp8) {
+        w[2 * h] = mx_e4m3x4(u[0], u[1], u[2], u[3]);
+        w[2 * h + 1] = mx_e4m3x4(u[4], u[5], u[6], u[7]);
+      } else {
+        w[h] = mx_e2m1x8(u);
+      }
+    }
+  }
+  __device__ __forceinline__ bool same(const MxCodes& o) const {
+    uint32_t d = 0;
+#pragma unroll
+    for (uint32_t i = 0; i < sizeof(w) / 4; ++i) d |= w[i] ^ o.w[i];
+    return d == 0;
+  }
+  // at element i; `keep` = false: zeros (a block with a NaN or infinity)
+  __device__ __forceinline__ void store(uint8_t* codes, size_t i, bool keep) const {
+    if constexpr (FMT == kMxfp8)
+      *reinterpret_cast<uint4*>(codes + i) = keep ? make_uint4(w[0], w[1], w[2], w[3]) : make_uint4(0, 0, 0, 0);
+    else
+      *reinterpret_cast<uint2*>(codes + i / 2) = keep ? make_uint2(w[0], w[1]) : make_uint2(0, 0);
+  }
+};
+// scale byte of the block (returned) and codes
+template <int FMT>
+__device__ __forceinline__ uint32_t mx_encode16(const float (&v)[16], uint8_t* codes, size_t i) {
+  const uint32_t s = mx_scale_byte<FMT>(mx_block_max(v));
+  MxCodes<FMT> c;
+  c.set(v, mx_inv_scale(s == 255u ? 127u : s));
+  c.store(codes, i, s != 255u);
   return s;
 }
 
