@@ -433,8 +433,9 @@ int qmoe_mx_dequant(const uint8_t* codes, const uint8_t* scales, int format, int
  * x, residual, residual_out [T, H] and weight [H] are fp16 or bf16
  * (act_dtype).  residual may be NULL (h = x), weight may be NULL (unit
  * weight), residual_out may be NULL (not wanted) and may be x or residual
- * itself.  Requires H a multiple of 32; pointers 16-byte aligned.  A row with
- * a NaN or an infinity reads as NaN in every block. */
+ * itself.  Requires H a multiple of 32; pointers 16-byte aligned.  A NaN makes
+ * its whole row read as NaN; an infinity makes its own block NaN and the rest
+ * of its row 0 (also where the sum of squares leaves fp32's range). */
 int qmoe_rmsnorm_mx(const void* x, const void* residual, const void* weight, int act_dtype, int T, int H, float eps,
                     int format, void* residual_out, uint8_t* codes, uint8_t* scales, void* stream);
 
