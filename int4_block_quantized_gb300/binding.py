@@ -375,31 +375,19 @@ def _bad(where, what):
     raise QMoEError(1, "%s: %s" % (where, what))
 
 
-def _mx_rows(t, where):
-    """(rows, columns, device index) of a contiguous 2-D CUDA tensor."""
-    shape, dev = t.shape, t.get_device()
-    if dev < 0 or len(shape) != 2 or not t.is_contiguous():
-        _bad(where, "wants a contiguous 2-D CUDA tensor")
-    return shape[0], shape[1], dev
+def _mx_size(t, where):
+    """(rows, columns) of a 2-D tensor."""
+    shape = t.shape
+    if len(shape) != 2:
+        _bad(where, "wants 2-D tensors, got %s" % (tuple(shape),))
+    return shape
 
 
-def _mx_same(t, dev, dtype, numel, where, name):
-    """Address of a contiguous tensor of a given type and size on device dev."""
-    if t.dtype != dtype or t.numel() != numel or t.get_device() != dev or not t.is_contiguous():
-        _bad(where, "%s: wants %d contiguous %s on cuda:%d" % (name, numel, dtype, dev))
-    return t.data_ptr()
-
-
-def _mx_tensor(codes, scales, fmt, where):
-    """(R, K, device index, address of the scales) of an MX tensor."""
-    R, K, dev = _mx_rows(codes, where)
-    if codes.dtype != _U8:
-        _bad(where, "codes are uint8")
-    if fmt == MXFP4:
-        K *= 2
-    elif fmt != MXFP8:
-        _bad(where, "unknown format %r" % (fmt,))
-    return R, K, dev, _mx_same(scales, dev, _U8, qmoe_mx_scale_bytes(R, K), where, "scales")
+def _mx_check(t, dev, dtype, numel, where, name):
+    """A contiguous tensor of a type and size on device dev, or an error."""
+    if dev < 0 or t.get_device() != dev or t.dtype is not dtype or t.numel() != numel or not t.is_contiguous():
+        _bad(where, "%s: wants %d contiguous %s on one CUDA device, got %s %s on %s%s" % (
+            name, numel, dtype, tuple(t.shape), t.dtype, t.device, "" if t.is_contiguous() else ", not contiguous"))
 
 
 def _mx_out(R, K, fmt, x, dev, codes, scales, where):
@@ -407,15 +395,15 @@ def _mx_out(R, K, fmt, x, dev, codes, scales, where):
     n = qmoe_mx_scale_bytes(R, K)
     if n == 0 or (fmt != MXFP8 and fmt != MXFP4):
         _bad(where, "format %r, [%d, %d]: MXFP8 or MXFP4, rows and a multiple of 32 columns are wanted" % (fmt, R, K))
-    cols = K if fmt == MXFP8 else K // 2
+    cols = K >> fmt
     if codes is None:
         codes = torch.empty((R, cols), dtype=_U8, device=x.device)
     else:
-        _mx_same(codes, dev, _U8, R * cols, where, "codes")
+        _mx_check(codes, dev, _U8, R * cols, where, "codes")
     if scales is None:
         scales = torch.empty(n, dtype=_U8, device=x.device)
     else:
-        _mx_same(scales, dev, _U8, n, where, "scales")
+        _mx_check(scales, dev, _U8, n, where, "scales")
     return codes, scales
 
 
@@ -437,27 +425,31 @@ def qmoe_mx_scale_bytes(R, K):
 
 def qmoe_mx_quantize(x, fmt=MXFP8, codes=None, scales=None):
     """(codes, scales) of x [M, K] (fp16, bf16 or fp32) in MXFP8 or MXFP4."""
-    M, K, dev = _mx_rows(x, "qmoe_mx_quantize")
-    dt = _MX_DT.get(x.dtype)
-    if dt is None:
-        _bad("qmoe_mx_quantize", "unsupported input type %s" % x.dtype)
-    codes, scales = _mx_out(M, K, fmt, x, dev, codes, scales, "qmoe_mx_quantize")
-    _mx_call(dev, lib().qmoe_mx_quantize, "qmoe_mx_quantize", x.data_ptr(), dt, fmt, M, K, codes.data_ptr(),
-             scales.data_ptr())
+    where = "qmoe_mx_quantize"
+    M, K = _mx_size(x, where)
+    dt, dev = _MX_DT.get(x.dtype), x.get_device()
+    if dt is None or dev < 0 or not x.is_contiguous():
+        _bad(where, "x: wants a contiguous CUDA tensor of fp16, bf16 or fp32, got %s on %s" % (x.dtype, x.device))
+    codes, scales = _mx_out(M, K, fmt, x, dev, codes, scales, where)
+    _mx_call(dev, lib().qmoe_mx_quantize, where, x.data_ptr(), dt, fmt, M, K, codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
 def qmoe_mx_dequant(codes, scales, fmt, dtype=torch.bfloat16, out=None):
     """[M, K] values (fp16, bf16 or fp32) of an MX tensor."""
-    M, K, dev, sp = _mx_tensor(codes, scales, fmt, "qmoe_mx_dequant")
-    dt = _MX_DT.get(dtype)
-    if dt is None:
-        _bad("qmoe_mx_dequant", "unsupported output type %s" % dtype)
+    where = "qmoe_mx_dequant"
+    M, K = _mx_size(codes, where)
+    dt, dev = _MX_DT.get(dtype), codes.get_device()
+    if dt is None or (fmt != MXFP8 and fmt != MXFP4):
+        _bad(where, "unsupported output type %s or format %r" % (dtype, fmt))
+    _mx_check(codes, dev, _U8, M * K, where, "codes")
+    K <<= fmt
+    _mx_check(scales, dev, _U8, qmoe_mx_scale_bytes(M, K), where, "scales")
     if out is None:
         out = torch.empty((M, K), dtype=dtype, device=codes.device)
     else:
-        _mx_same(out, dev, dtype, M * K, "qmoe_mx_dequant", "out")
-    _mx_call(dev, lib().qmoe_mx_dequant, "qmoe_mx_dequant", codes.data_ptr(), sp, fmt, M, K, out.data_ptr(), dt)
+        _mx_check(out, dev, dtype, M * K, where, "out")
+    _mx_call(dev, lib().qmoe_mx_dequant, where, codes.data_ptr(), scales.data_ptr(), fmt, M, K, out.data_ptr(), dt)
     return out
 
 
@@ -466,21 +458,24 @@ def qmoe_rmsnorm_mx(x, residual=None, weight=None, eps=1e-6, fmt=MXFP8, residual
     or MXFP4; residual_out = x + residual (a new tensor unless given; it may be
     x or residual itself).  Without a residual it is None unless given."""
     where = "qmoe_rmsnorm_mx"
-    T, H, dev = _mx_rows(x, where)
-    dt = x.dtype
-    if dt != torch.float16 and dt != torch.bfloat16:
-        _bad(where, "unsupported input type %s" % dt)
+    T, H = _mx_size(x, where)
+    dtype, dev = x.dtype, x.get_device()
+    if dev < 0 or not x.is_contiguous() or (dtype is not torch.float16 and dtype is not torch.bfloat16):
+        _bad(where, "x: wants a contiguous CUDA tensor of fp16 or bf16, got %s on %s" % (dtype, x.device))
     codes, scales = _mx_out(T, H, fmt, x, dev, codes, scales, where)
     rp = wp = op = None
     if residual is not None:
-        rp = _mx_same(residual, dev, dt, T * H, where, "residual")
+        _mx_check(residual, dev, dtype, T * H, where, "residual")
+        rp = residual.data_ptr()
         if residual_out is None:
             residual_out = torch.empty_like(x)
     if residual_out is not None:
-        op = _mx_same(residual_out, dev, dt, T * H, where, "residual_out")
+        _mx_check(residual_out, dev, dtype, T * H, where, "residual_out")
+        op = residual_out.data_ptr()
     if weight is not None:
-        wp = _mx_same(weight, dev, dt, H, where, "weight")
-    _mx_call(dev, lib().qmoe_rmsnorm_mx, where, x.data_ptr(), rp, wp, _MX_DT[dt], T, H, float(eps), fmt, op,
+        _mx_check(weight, dev, dtype, H, where, "weight")
+        wp = weight.data_ptr()
+    _mx_call(dev, lib().qmoe_rmsnorm_mx, where, x.data_ptr(), rp, wp, _MX_DT[dtype], T, H, float(eps), fmt, op,
              codes.data_ptr(), scales.data_ptr())
     return codes, scales, residual_out
 
@@ -490,31 +485,38 @@ def qmoe_mx_matmul(x_codes, x_scales, x_fmt, w_codes, w_scales, dtype=torch.bflo
     weights W [N, K].  status: an int32 [1] device tensor that collects
     QMOE_ST_TIMEOUT (zero it first)."""
     where = "qmoe_mx_matmul"
-    M, K, dev, xs = _mx_tensor(x_codes, x_scales, x_fmt, where)
-    N, KW, dev_w, ws = _mx_tensor(w_codes, w_scales, MXFP4, where)
-    if K != KW or dev_w != dev:
-        _bad(where, "x has %d columns on %s, W has %d on %s" % (K, x_codes.device, KW, w_codes.device))
-    dt = _MX_DT.get(dtype)
-    if dt is None:
-        _bad(where, "unsupported output type %s" % dtype)
+    M, K = _mx_size(x_codes, where)
+    N, half = _mx_size(w_codes, where)
+    dt, dev = _MX_DT.get(dtype), x_codes.get_device()
+    if dt is None or (x_fmt != MXFP8 and x_fmt != MXFP4) or K << x_fmt != 2 * half:
+        _bad(where, "x [%d, %d] bytes in format %r, W [%d, %d] bytes, result in %s" % (M, K, x_fmt, N, half, dtype))
+    _mx_check(x_codes, dev, _U8, M * K, where, "x_codes")
+    K = 2 * half
+    _mx_check(x_scales, dev, _U8, qmoe_mx_scale_bytes(M, K), where, "x_scales")
+    _mx_check(w_codes, dev, _U8, N * half, where, "w_codes")
+    _mx_check(w_scales, dev, _U8, qmoe_mx_scale_bytes(N, K), where, "w_scales")
     if out is None:
         out = torch.empty((M, N), dtype=dtype, device=x_codes.device)
     else:
-        _mx_same(out, dev, dtype, M * N, where, "out")
-    st = None if status is None else _mx_same(status, dev, torch.int32, 1, where, "status")
-    _mx_call(dev, lib().qmoe_mx_matmul, where, x_codes.data_ptr(), xs, x_fmt, w_codes.data_ptr(), ws, M, N, K,
-             out.data_ptr(), dt, st)
+        _mx_check(out, dev, dtype, M * N, where, "out")
+    st = None
+    if status is not None:
+        _mx_check(status, dev, torch.int32, 1, where, "status")
+        st = status.data_ptr()
+    _mx_call(dev, lib().qmoe_mx_matmul, where, x_codes.data_ptr(), x_scales.data_ptr(), x_fmt, w_codes.data_ptr(),
+             w_scales.data_ptr(), M, N, K, out.data_ptr(), dt, st)
     return out
 
 
 def qmoe_mx_tile_scales(scales_rowmajor):
     """Row-major scale bytes [R, K/32] (as checkpoints store them) -> tiles."""
     where = "qmoe_mx_tile_scales"
-    R, nb, dev = _mx_rows(scales_rowmajor, where)
-    n = qmoe_mx_scale_bytes(R, 32 * nb)
-    if n == 0 or scales_rowmajor.dtype != torch.uint8:
-        _bad(where, "wants uint8 scales [R, K/32]")
-    out = torch.empty(n, dtype=torch.uint8, device=scales_rowmajor.device)
+    R, nb = _mx_size(scales_rowmajor, where)
+    dev, n = scales_rowmajor.get_device(), qmoe_mx_scale_bytes(R, 32 * nb)
+    if n == 0:
+        _bad(where, "wants scales [R, K/32]")
+    _mx_check(scales_rowmajor, dev, _U8, R * nb, where, "scales")
+    out = torch.empty(n, dtype=_U8, device=scales_rowmajor.device)
     _mx_call(dev, lib().qmoe_mx_tile_scales, where, scales_rowmajor.data_ptr(), R, 32 * nb, out.data_ptr())
     return out
 
@@ -522,10 +524,10 @@ def qmoe_mx_tile_scales(scales_rowmajor):
 def qmoe_mx_untile_scales(scales, R, K):
     """Scale tiles of an MX tensor [R, K] -> row-major bytes [R, K/32]."""
     where = "qmoe_mx_untile_scales"
-    n = qmoe_mx_scale_bytes(R, K)
-    if n == 0 or not scales.is_cuda:
-        _bad(where, "wants CUDA scale tiles of an MX tensor, got [%d, %d]" % (R, K))
-    _mx_same(scales, scales.get_device(), torch.uint8, n, where, "scales")
-    out = torch.empty((R, K // 32), dtype=torch.uint8, device=scales.device)
-    _mx_call(scales.get_device(), lib().qmoe_mx_untile_scales, where, scales.data_ptr(), R, K, out.data_ptr())
+    dev, n = scales.get_device(), qmoe_mx_scale_bytes(R, K)
+    if n == 0:
+        _bad(where, "no MX tensor is [%d, %d]" % (R, K))
+    _mx_check(scales, dev, _U8, n, where, "scales")
+    out = torch.empty((R, K // 32), dtype=_U8, device=scales.device)
+    _mx_call(dev, lib().qmoe_mx_untile_scales, where, scales.data_ptr(), R, K, out.data_ptr())
     return out
