@@ -20,7 +20,7 @@
 namespace qmoe {
 
 constexpr int kMmThreads = 352;       // warps 0 and 6 copy, warp 1 issues MMAs, warps 2-5 and 7-10 write y
-constexpr int kMmFillThreads = 608;   // + warps 11-18: weights by loads and stores (see FILL)
+constexpr int kMmFillThreads = 640;   // + warps 11-18: codes widened by loads and stores, 19: their copies (see FILL)
 constexpr uint32_t kMmSmem = 232448;  // 227 KB
 constexpr uint32_t kMmBars = 1024;
 
@@ -34,7 +34,7 @@ struct MmParams {
   int split;                     // CTAs of a cluster that share a tile's K
 };
 
-template <int XF, int BN, int CG>
+template <int XF, int BN, int CG, bool FILL = false>
 struct MmPlan {
   static constexpr int kStageK = XF == kMxfp4 ? 256 : 128;  // elements
   static constexpr int kWords = kStageK / 128;              // scale tiles of a stage along K
@@ -49,9 +49,12 @@ struct MmPlan {
   static constexpr uint32_t kPart = BN <= 64 ? (BN < 32 ? 32 : BN) * 512 : 0;
   // 2 KB per output warp: 32 tokens x 32 outputs of 16 bits, turned round there
   static constexpr uint32_t kOut = BN >= 32 ? 8 * 2048 : 0;
-  static constexpr int kStages0 = (int)((kMmSmem - kMmBars - 1024 - kPart - kOut) / (kAb + kSf));
+  // FILL: packed weight codes on their way, 128 rows x 64 bytes a stage
+  static constexpr int kRawSlots = !FILL ? 0 : BN <= 64 ? 6 : 4;
+  static constexpr uint32_t kRaw = kRawSlots * 128 * 64;
+  static constexpr int kStages0 = (int)((kMmSmem - kMmBars - 1024 - kPart - kOut - kRaw) / (kAb + kSf));
   static constexpr int kStages = kStages0 > 12 ? 12 : kStages0;
-  static constexpr uint32_t kTotal = kMmBars + kOut + kStages * (kAb + kSf) + kPart + 1024;
+  static constexpr uint32_t kTotal = kMmBars + kOut + kRaw + kStages * (kAb + kSf) + kPart + 1024;
   // tensor memory: two accumulators, then the stage's scales.  At 256 tokens
   // the two overlap by 32 columns, since the scales need 24 of the 512.
   static constexpr bool kOverlap = BN == 256;
@@ -123,14 +126,14 @@ __device__ __forceinline__ void mm_tile(const MmParams& p, int t, int& rt, int& 
 }
 
 // FILL (MXFP8 x only): the TMA copy that widens e2m1 codes wants rows of a
-// multiple of 128 codes on 32-byte boundaries; other weights are read and
-// spread by eight warps.
+// multiple of 128 codes on 32-byte boundaries; other weights come packed and
+// eight warps spread them in shared memory.
 template <int XF, int BN, int CG, bool FILL>
 __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
     mx_matmul_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                      const __grid_constant__ CUtensorMap tm_ws, const __grid_constant__ CUtensorMap tm_xs,
                      const MmParams p) {
-  using P = MmPlan<XF, BN, CG>;
+  using P = MmPlan<XF, BN, CG, FILL>;
   constexpr int S = P::kStages;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -139,10 +142,13 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
   uint64_t* acc_full = empty + S;       // [2]
   uint64_t* acc_free = acc_full + 2;    // [2]
   uint64_t* fin = acc_free + 2;
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(fin + 1);
+  uint64_t* raw_full = fin + 1;  // [kRawSlots]
+  uint64_t* raw_empty = raw_full + P::kRawSlots;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(raw_empty + P::kRawSlots);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   uint8_t* outbuf = smem + kMmBars;  // 1024-byte aligned, as the ring behind it
-  uint8_t* ring = outbuf + P::kOut;
+  uint8_t* raw = outbuf + P::kOut;
+  uint8_t* ring = raw + P::kRaw;
   uint8_t* sfring = ring + S * P::kAb;
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be the same in all lanes
@@ -157,6 +163,10 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
       mbar_init(&acc_free[b], 8 * CG);
     }
     mbar_init(fin, 1);
+    for (int s = 0; s < P::kRawSlots; ++s) {
+      mbar_init(&raw_full[s], 1);
+      mbar_init(&raw_empty[s], 4);
+    }
     *s_abort = 0;
     fence_barrier_init();
   }
@@ -372,70 +382,78 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
         if (!P::kOverlap) freed(&acc_free[b]);
       }
     }
-  } else if (FILL) {
-    // -------------------------------------- weights of ragged rows (MXFP8 x)
-    // Two groups of four warps take turns at the stages; a warp takes 32 rows,
-    // four lanes the 64 bytes of a row's stage (8 rows of two whole sectors per
-    // load; with a row per lane a load touches 32 lines).  Loads run three of
-    // the group's stages ahead of their stores.  3272 x 3655 x 3232 takes 44 us
-    // so, 47 with one group, 62 with a row per lane and one stage ahead.
-    const int group = warp >= kMmThreads / 32 + 4;
-    const int r0 = ((warp - kMmThreads / 32) & 3) * 32 + (lane >> 2), piece = lane & 3;
-    const int nc = c1 - c0, mine = first < tiles ? (tiles - 1 - first) / step + 1 : 0;
-    const long long total = (long long)mine * nc;
-    long long loaded = group;
-    int lt = first, lc = c0 + group, lrt = 0, ltt = 0;  // the next stage to load
-    auto settle = [&]() {
-      while (lc >= c1) {
-        lc -= nc;
-        lt += step;
-      }
-      if (lt < tiles) mm_tile(p, lt, lrt, ltt);
-    };
-    settle();
-    auto load = [&](uint4(&v)[4]) {
-      if (loaded >= total) return;
-      const int k = lc * 128 + piece * 32;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int nn = lrt * 128 + r0 + 8 * i;
-        v[i] = nn < p.N && k < p.K ? __ldg(reinterpret_cast<const uint4*>(p.wc + (size_t)nn * (p.K / 2) + k / 2))
-                                   : make_uint4(0, 0, 0, 0);
-      }
-      loaded += 2;
-      lc += 2;
-      if (lc >= c1) settle();
-    };
-    uint4 v[3][4];
-#pragma unroll
-    for (int q = 0; q < 3; ++q) load(v[q]);
-    int s = group;
+  } else if (FILL && warp == kMmFillThreads / 32 - 1) {
+    // ------------------------- packed weight codes, as far ahead as slots allow
+    constexpr int R = P::kRawSlots ? P::kRawSlots : 1;
+    int it = 0, s = 0;
     uint32_t ph = 0;
     bool ok = true;
-    for (long long it = group; it < total && ok; it += 6) {
-#pragma unroll
-      for (int q = 0; q < 3; ++q) {
-        const long long n = it + 2 * q;
-        if (n >= total) break;
-        if (n >= S) ok = mm_wait(&empty[s], ph ^ 1u, p.status, s_abort);
+    const uint32_t el = elect_lane();
+    for (int t = first; t < tiles && ok; t += step) {
+      int rt, tt;
+      mm_tile(p, t, rt, tt);
+      for (int c = c0; c < c1; ++c, ++it) {
+        if (it >= R) ok = mm_wait(&raw_empty[s], ph ^ 1u, p.status, s_abort);
         if (!ok) break;
-        uint8_t* st = ring + s * P::kAb;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = r0 + 8 * i;
-          *reinterpret_cast<uint4*>(st + r * 128 + (((2 * piece) ^ (r & 7)) << 4)) = make_uint4(v[q][i].x, v[q][i].y, 0, 0);
-          *reinterpret_cast<uint4*>(st + r * 128 + (((2 * piece + 1) ^ (r & 7)) << 4)) =
-              make_uint4(v[q][i].z, v[q][i].w, 0, 0);
+        if (el) {
+          mbar_arrive_expect_tx(&raw_full[s], 128 * 64);
+          tma_load_2d(raw + s * 128 * 64, &tm_w, c * 64, rt * 128, &raw_full[s]);
         }
-        load(v[q]);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(&full[s]);
-        s += 2;
-        if (s >= S) {
-          s -= S;
+        if (++s == R) {
+          s = 0;
           ph ^= 1u;
         }
+      }
+    }
+    if (*s_abort && lane == 0)
+      for (int i = 0; i < R; ++i)
+        if (it > i) mbar_wait(&raw_full[i], ((it - 1 - i) / R) & 1, nullptr);
+  } else if (FILL && warp >= kMmThreads / 32) {
+    // ---------------------- codes of ragged rows spread to 16 bytes per 8 (MXFP8 x)
+    // Two groups of four warps take turns at the stages; a warp takes 32 rows,
+    // four lanes the 64 bytes of a row.  (The codes come by TMA and not by
+    // loads of these warps, whose fence between stores and MMAs waits for loads
+    // in flight too: 16 x 8192 x 8160 takes 11.7 us so and 16.9 with loads,
+    // 512 x 8192 x 8160 40 and 49; widened by TMA, K = 8192 takes 9.0 and 24.)
+    const int group = warp >= kMmThreads / 32 + 4;
+    const int r0 = ((warp - kMmThreads / 32) & 3) * 32 + (lane >> 2), piece = lane & 3;
+    constexpr int R = P::kRawSlots ? P::kRawSlots : 1;
+    const int mine = first < tiles ? (tiles - 1 - first) / step + 1 : 0;
+    const long long total = (long long)mine * (c1 - c0);
+    int s = group, rs = group;
+    uint32_t ph = 0, rph = 0;
+    for (long long n = group; n < total; n += 2) {
+      if (!mm_wait(&raw_full[rs], rph, p.status, s_abort)) break;
+      const uint4* src = reinterpret_cast<const uint4*>(raw + rs * 128 * 64 + r0 * 64 + piece * 16);
+      uint4 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = src[32 * i];
+      if (n >= S && !mm_wait(&empty[s], ph ^ 1u, p.status, s_abort)) break;
+      // 16-byte pieces 2 piece and 2 piece + 1 of the row, swizzled by row % 8 = r0 % 8
+      uint8_t* st = ring + s * P::kAb + r0 * 128;
+      uint4* lo = reinterpret_cast<uint4*>(st + (((2 * piece) ^ (r0 & 7)) << 4));
+      uint4* hi = reinterpret_cast<uint4*>(st + (((2 * piece + 1) ^ (r0 & 7)) << 4));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        lo[64 * i] = make_uint4(v[i].x, v[i].y, 0, 0);
+        hi[64 * i] = make_uint4(v[i].z, v[i].w, 0, 0);
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&full[s]);
+        mbar_arrive(&raw_empty[rs]);  // only now: what was read has been stored
+      }
+      s += 2;
+      if (s >= S) {
+        s -= S;
+        ph ^= 1u;
+      }
+      rs += 2;
+      if (rs >= R) {
+        rs -= R;
+        rph ^= 1u;
       }
     }
   }
@@ -496,7 +514,7 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
 
 template <int XF, int BN, int CG, bool FILL>
 static cudaError_t launch_mm(MmParams p, int split, const uint8_t* xc, cudaStream_t st) {
-  using P = MmPlan<XF, BN, CG>;
+  using P = MmPlan<XF, BN, CG, FILL>;
   static_assert(P::kTotal <= kMmSmem && P::kCols0 <= 512, "plan");
   p.split = split;
   p.row_tiles = (p.N + 128 * CG - 1) / (128 * CG);
@@ -518,8 +536,13 @@ static cudaError_t launch_mm(MmParams p, int split, const uint8_t* xc, cudaStrea
   const uint64_t half = p.K / 2;
   if (!map(&tx, xc, CU_TENSOR_MAP_DATA_TYPE_UINT8, XF == kMxfp4 ? half : p.K, p.M, XF == kMxfp4 ? half : p.K, BN / CG))
     return cudaErrorNotSupported;
-  if (FILL) {
-    tw = tx;
+  if (FILL) {  // packed, 64 bytes a row
+    const cuuint64_t dims[2] = {half, (cuuint64_t)p.N}, strides[1] = {half};
+    const cuuint32_t box[2] = {64, 128};
+    if (fn(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(p.wc), dims, strides, box, es,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorNotSupported;
   } else if (XF == kMxfp4) {
     if (!map(&tw, p.wc, CU_TENSOR_MAP_DATA_TYPE_UINT8, half, p.N, half, 128)) return cudaErrorNotSupported;
   } else {
@@ -616,7 +639,7 @@ static MmChoice mm_choose(int M, int N, int chunks, bool fill) {
   for (const auto& k : kinds) {
     if (k.bn < 64 && M > k.bn) continue;  // 16 and 32 tokens: a single tile, at the head of its scale tile
     if (k.cg == 2 && fill) continue;
-    const int stage = fill ? 230 + k.bn : k.stage;  // weights by loads and stores: 240 ns at 16 tokens, 420 at 192
+    const int stage = fill ? 230 + k.bn / 2 : k.stage;  // codes widened by warps: 240 ns at 16 tokens, 340 at 192
     const long long tiles = (long long)((N + 128 * k.cg - 1) / (128 * k.cg)) * ((M + k.bn - 1) / k.bn);
     for (int split = 1; split <= 8; split *= 2) {
       if (split > 1 && (!k.exchange || split > chunks || tiles * split > mm_capacity(split))) break;
