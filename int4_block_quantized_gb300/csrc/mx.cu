@@ -8,16 +8,19 @@
 
 namespace qmoe {
 
-// grid of a grid-stride kernel over `work` threads of 256
+// Grid of a grid-stride kernel over `work` threads of 256: at most 32 CTAs an
+// SM (fp32 16384 x 8192 reads back in 102 us at 32, 108 at 16; without a cap
+// 84480 x 2048 fp16 takes 80 us instead of 63).
 static dim3 stride_grid(size_t work) {
-  const size_t cap = (size_t)device_sm_count() * 16;
+  const size_t cap = (size_t)device_sm_count() * 32;
   const size_t b = (work + 255) / 256;
   return dim3((unsigned)(b < 1 ? 1 : b > cap ? cap : b));
 }
 
 // --------------------------------------------------------------- quantise
 // s = floor(log2 max|v|) - emax, code = RN(v / 2^s): a thread takes half a
-// block (16 elements), so a block's maximum needs one shuffle.  Bound by HBM.
+// block (16 elements), so a block's maximum needs one shuffle.  Bound by HBM:
+// 84480 x 2048 fp16 to MXFP4 in 63 us, 6.9 TB/s.
 template <typename T, int FMT>
 __global__ void __launch_bounds__(256) mx_quantize_kernel(const void* __restrict__ x, int M, int K,
                                                           uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
@@ -51,7 +54,8 @@ cudaError_t launch_mx_quantize(const void* x, int x_dtype, int format, int M, in
 }
 
 // ---------------------------------------------------------------- dequant
-// code * X in fp32 (exact), rounded once to T.  Bound by HBM.
+// code * X in fp32 (exact), rounded once to T.  Bound by HBM: 84480 x 2048
+// MXFP4 to fp16 in 68 us, 6.4 TB/s.
 template <typename T, int FMT>
 __global__ void __launch_bounds__(256) mx_dequant_kernel(const uint8_t* __restrict__ codes,
                                                          const uint8_t* __restrict__ scales, int M, int K,
