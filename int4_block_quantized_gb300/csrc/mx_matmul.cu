@@ -621,6 +621,7 @@ static int mm_capacity(int split) {
 //    512 x 8192 x 8192    2x256/1 24  128/1 28  2x192/1 33  192/1 35  64/1 46
 //   2048 x 8192 x 8192    2x192/1 82  192/1 85  2x256/1 87  128/1 89  64/1 154
 //   2048 x 11264 x 2048   2x192/1 33  2x256/1 34  192/1 37  128/1 39  64/1 59
+//   4096 x 8192 x 2048 (x in MXFP4)  2x256/1 30  2x192/1 35
 //   4085 x 3895 x 512 (x in MXFP4)  128/1 13.1  192/1 13.4  64/1 13.9  2x256/1 15.4  2x192/1 16.9
 // (192 tokens: two whole accumulators fit tensor memory; at 256 the next tile's
 // first MMA waits until the epilogue has taken the shared columns.)
@@ -632,8 +633,8 @@ static MmChoice mm_choose(int M, int N, int chunks, bool fill) {
     int bn, cg, start, stage, tile, epilogue, exchange;
   } kinds[] = {{16, 1, 1900, 170, 300, 200, 1200},   {32, 1, 2000, 170, 350, 300, 1300},
                {64, 1, 2900, 165, 500, 850, 1400},   {128, 1, 3600, 185, 1200, 1350, 2900},
-               {192, 1, 3900, 250, 500, 1900, 0},    {192, 2, 4200, 240, 300, 2500, 0},
-               {256, 2, 4600, 300, 1500, 2700, 0}};
+               {192, 1, 3900, 250, 800, 1900, 0},    {192, 2, 4200, 240, 300, 3000, 0},
+               {256, 2, 4600, 300, 1250, 2700, 0}};
   MmChoice best = {128, 1, 1};
   long long least = -1;
   for (const auto& k : kinds) {
