@@ -563,12 +563,15 @@ static cudaError_t launch_mm(MmParams p, int split, const uint8_t* xc, cudaStrea
   p.wide_out = p.y_dtype != QMOE_F32 && p.N % 8 == 0 && !(reinterpret_cast<uintptr_t>(p.y) & 15);
   const int sms = device_sm_count();
   auto kernel = mx_matmul_kernel<XF, BN, CG, FILL>;
-  cudaError_t err = ensure_smem(kernel, P::kTotal);
+  // All of the SM's shared memory, used or not: the CTA takes all of its tensor
+  // memory, and a CTA of another kernel that waits for some (or has some) must
+  // not share the SM: two clusters could then wait for one another.
+  cudaError_t err = ensure_smem(kernel, kMmSmem);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.split > 1 ? tiles * p.split : CG * (tiles < sms / CG ? tiles : sms / CG)));
   cfg.blockDim = dim3(FILL ? kMmFillThreads : kMmThreads);
-  cfg.dynamicSmemBytes = P::kTotal;
+  cfg.dynamicSmemBytes = kMmSmem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -588,12 +591,11 @@ static int mm_capacity(int split) {
   int dev = 0;
   if (l == 0 || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return device_sm_count();
   if (!cached[dev][l]) {
-    using P = MmPlan<kMxfp4, 16, 1>;
     auto kernel = mx_matmul_kernel<kMxfp4, 16, 1, false>;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(split);
     cfg.blockDim = dim3(kMmThreads);
-    cfg.dynamicSmemBytes = P::kTotal;
+    cfg.dynamicSmemBytes = kMmSmem;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = split;
@@ -601,7 +603,7 @@ static int mm_capacity(int split) {
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     int n = 0;
-    if (ensure_smem(kernel, P::kTotal) != cudaSuccess || cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1)
+    if (ensure_smem(kernel, kMmSmem) != cudaSuccess || cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1)
       return split;  // not known: no more than one cluster at a time
     cached[dev][l] = n * split;
   }

@@ -432,6 +432,32 @@ def test_graphs_on_two_streams_at_once():
     assert all(torch.equal(a, b) for a, b in zip(outs, ref))
 
 
+def test_product_beside_the_layer_on_another_stream():
+    """The layer's tensor-core kernels (router, grouped GEMM) and the product each
+    take tensor memory; on two streams at once both finish with their own results."""
+    from int4_block_quantized_gb300 import synthetic as S
+    wl = S.WORKLOADS["prefill"]
+    layer = dict(S.make_layer(wl, seed=1, device=DEV))
+    ws = B.Workspace(wl.T, wl.H, wl.I, wl.E, wl.k, device=DEV)
+    _, w_ref, ids_ref = B.qmoe_forward(layer, ws=ws, return_routing=True)
+    # pairs of CTAs; clusters along K
+    cases = [(2600, 1912, 512), (40, 1408, 2048)]
+    args = [(to_dev(*random_mx(m, k, B.MXFP8, 1), B.MXFP8), to_dev(*random_mx(n, k, B.MXFP4, 2), B.MXFP4)) for m, n, k in cases]
+    refs = [B.qmoe_mx_matmul(*x, B.MXFP8, *w) for x, w in args]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got, routed = [], []
+    for i in range(30):
+        routed.append(B.qmoe_forward(layer, ws=ws, return_routing=True)[1:])
+        with torch.cuda.stream(side):
+            x, w = args[i % 2]
+            got.append(B.qmoe_mx_matmul(*x, B.MXFP8, *w))
+    torch.cuda.synchronize()
+    assert ws.status() == (0, 0)
+    assert all(torch.equal(w, w_ref) and torch.equal(i, ids_ref) for w, i in routed)
+    assert all(torch.equal(y, refs[i % 2]) for i, y in enumerate(got))
+
+
 # ------------------------------------------------------------------ together
 @pytest.mark.parametrize("T", [1, 5, 160])
 @pytest.mark.parametrize("fmt", FMT)
