@@ -273,7 +273,8 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
       // one stage: its scales, then its MMAs (the first `words` scale words and
       // `mmas` instructions: fewer only where K ends)
       auto issue = [&](int slot, bool first_stage, int words, int mmas) {
-        const uint32_t st = smem_u32(ring + slot * P::kAb) >> 4, sf = smem_u32(sfring + slot * P::kSf) >> 4;
+        const uint32_t st = (smem_u32(ring + slot * P::kAb) >> 4) & 0x3FFFu;  // a descriptor's address field
+        const uint32_t sf = (smem_u32(sfring + slot * P::kSf) >> 4) & 0x3FFFu;
 #pragma unroll
         for (int q = 0; q < P::kWords; ++q) {
           if (q >= words) break;
