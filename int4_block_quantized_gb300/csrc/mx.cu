@@ -145,9 +145,15 @@ __global__ void __launch_bounds__(1024, 2)
   __shared__ float part[32];
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = ss;
   __syncthreads();
+  // pairwise: the few large sums' roundings are all that the row's sum loses
   float tot = 0.f;
-  for (int i = 0; i < threads / 32; ++i) tot += part[i];
-  const float inv = 1.0f / sqrtf(tot / (float)H + eps);
+  for (int i = 0; i < threads / 32; i += 8) {
+    float p[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) p[j] = i + j < threads / 32 ? part[i + j] : 0.f;
+    tot += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+  }
+  const float inv = rsqrtf(__fadd_rn(__fmul_rn(tot, 1.0f / (float)H), eps));  // mean, + eps: each rounded to fp32
   for (int u = threadIdx.x; u < units; u += threads) {
     if (!KEEP) norm_load<T>(x, residual, row + u * 16, v);
     if (residual_out) store16<T>(residual_out, row + u * 16, v);

@@ -2,9 +2,10 @@
 
 Quantisation and its reading back are exact, so they are compared bit for bit.
 The norm's fp32 y carries a relative error of at most (H / 2 + 8) 2^-24 (each
-addition of the sum of squares at most 2^-24, halved by the square root; eight
-roundings around it), so each element must lie between the quantisations of
-y (1 -+ that).  A product of two elements is exact in fp32; a sum of K of them
+addition of the sum of squares at most 2^-24, halved by the square root; around
+it 1 / H, the mean and eps, halved too, the reciprocal root's two units, which
+are 4 x 2^-24, and two products), so each element must lie between the
+quantisations of y (1 -+ that).  A product of two elements is exact in fp32; a sum of K of them
 in any order, each addition off by at most a whole step, is off by at most
 K 2^-23 times the sum of magnitudes, and the result is rounded once (half a
 step of the output's type)."""
