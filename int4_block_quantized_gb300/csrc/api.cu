@@ -43,12 +43,16 @@ int check_qweight(const qmoe_qweight& q, int N, int K, int bs) {
   return QMOE_OK;
 }
 
-// codes and scales of an MX tensor [R, K]
+// sizes of an MX tensor [R, K]
+int check_mx_size(int R, int K) {
+  if (R < 1 || K < 32 || K % 32) return QMOE_ERR_INVALID_ARG;
+  return R > (1 << 30) || K > (1 << 30) ? QMOE_ERR_UNSUPPORTED : QMOE_OK;  // tile counts stay in 32 bits
+}
+// its codes and scales
 int check_mx(const uint8_t* codes, const uint8_t* scales, int format, int R, int K) {
   if (!codes || !scales || !aligned(codes, 16) || !aligned(scales, 16)) return QMOE_ERR_INVALID_ARG;
   if (format != QMOE_MXFP8 && format != QMOE_MXFP4) return QMOE_ERR_INVALID_ARG;
-  if (R < 1 || K < 32 || K % 32) return QMOE_ERR_INVALID_ARG;
-  return R > (1 << 30) || K > (1 << 30) ? QMOE_ERR_UNSUPPORTED : QMOE_OK;  // tile counts stay in 32 bits
+  return check_mx_size(R, K);
 }
 
 thread_local cudaError_t g_last_cuda_error = cudaSuccess;
@@ -582,16 +586,16 @@ int qmoe_mx_matmul(const uint8_t* x_codes, const uint8_t* x_scales, int x_format
 }
 
 int qmoe_mx_tile_scales(const uint8_t* scales_rowmajor, int R, int K, uint8_t* scales, void* stream) {
-  if (!scales_rowmajor || !scales || !aligned(scales, 16) || !qmoe_mx_scale_bytes(R, K)) return QMOE_ERR_INVALID_ARG;
-  int rc = check_device();
-  if (rc) return rc;
+  if (!scales_rowmajor || !scales || !aligned(scales, 16)) return QMOE_ERR_INVALID_ARG;
+  int rc = check_mx_size(R, K);
+  if (rc || (rc = check_device())) return rc;
   return cuda_status(launch_mx_retile(scales_rowmajor, scales, R, K, true, (cudaStream_t)stream));
 }
 
 int qmoe_mx_untile_scales(const uint8_t* scales, int R, int K, uint8_t* scales_rowmajor, void* stream) {
-  if (!scales_rowmajor || !scales || !aligned(scales, 16) || !qmoe_mx_scale_bytes(R, K)) return QMOE_ERR_INVALID_ARG;
-  int rc = check_device();
-  if (rc) return rc;
+  if (!scales_rowmajor || !scales || !aligned(scales, 16)) return QMOE_ERR_INVALID_ARG;
+  int rc = check_mx_size(R, K);
+  if (rc || (rc = check_device())) return rc;
   return cuda_status(launch_mx_retile(scales, scales_rowmajor, R, K, false, (cudaStream_t)stream));
 }
 

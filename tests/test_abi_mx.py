@@ -85,3 +85,11 @@ def test_binding_refuses_what_it_cannot_pass_on(L):
         with pytest.raises(B.QMoEError) as e:
             call()
         assert e.value.code == 1
+
+
+@pytest.mark.parametrize("R,K", [((1 << 30) + 1, 64), (2 ** 31 - 1, 32), (4, (1 << 30) + 32), (1, 2 ** 31 - 96),
+                                 (129, 2 ** 31 - 32)])
+def test_scale_adapters_beyond_2_30_are_unsupported(L, R, K):
+    """Past the limit the kernels' 32-bit tile counts would overflow."""
+    for f in (L.qmoe_mx_tile_scales, L.qmoe_mx_untile_scales):
+        assert f(FAKE, R, K, FAKE, None) == 2
