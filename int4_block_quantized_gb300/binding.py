@@ -368,6 +368,7 @@ def qmoe_unpack_zero_points(zp_packed, nb):
 # GB300's host cores), outputs from torch.empty (1.6 us; new_empty takes 3.4).
 
 _U8 = torch.uint8
+_MX_MAX = 1 << 30
 _MX_DT = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
 
 
@@ -390,9 +391,17 @@ def _mx_check(t, dev, dtype, numel, where, name):
             name, numel, dtype, tuple(t.shape), t.dtype, t.device, "" if t.is_contiguous() else ", not contiguous"))
 
 
+def _mx_bytes(R, K, where):
+    """qmoe_mx_scale_bytes, with the library's limit on R and K: what is beyond
+    32 bits would reach it as another size."""
+    if R > _MX_MAX or K > _MX_MAX:
+        raise QMoEError(2, "%s: [%d, %d], at most 2^30 rows and columns" % (where, R, K))
+    return (R + 127) // 128 * ((K + 127) // 128) * 512 if R > 0 and K > 0 and K % 32 == 0 else 0
+
+
 def _mx_out(R, K, fmt, x, dev, codes, scales, where):
     """(codes, scales) to write an MX tensor [R, K] to: the caller's, or new ones."""
-    n = qmoe_mx_scale_bytes(R, K)
+    n = _mx_bytes(R, K, where)
     if n == 0 or (fmt != MXFP8 and fmt != MXFP4):
         _bad(where, "format %r, [%d, %d]: MXFP8 or MXFP4, rows and a multiple of 32 columns are wanted" % (fmt, R, K))
     cols = K >> fmt
@@ -444,7 +453,7 @@ def qmoe_mx_dequant(codes, scales, fmt, dtype=torch.bfloat16, out=None):
         _bad(where, "unsupported output type %s or format %r" % (dtype, fmt))
     _mx_check(codes, dev, _U8, M * K, where, "codes")
     K <<= fmt
-    _mx_check(scales, dev, _U8, qmoe_mx_scale_bytes(M, K), where, "scales")
+    _mx_check(scales, dev, _U8, _mx_bytes(M, K, where), where, "scales")
     if out is None:
         out = torch.empty((M, K), dtype=dtype, device=codes.device)
     else:
@@ -492,9 +501,9 @@ def qmoe_mx_matmul(x_codes, x_scales, x_fmt, w_codes, w_scales, dtype=torch.bflo
         _bad(where, "x [%d, %d] bytes in format %r, W [%d, %d] bytes, result in %s" % (M, K, x_fmt, N, half, dtype))
     _mx_check(x_codes, dev, _U8, M * K, where, "x_codes")
     K = 2 * half
-    _mx_check(x_scales, dev, _U8, qmoe_mx_scale_bytes(M, K), where, "x_scales")
+    _mx_check(x_scales, dev, _U8, _mx_bytes(M, K, where), where, "x_scales")
     _mx_check(w_codes, dev, _U8, N * half, where, "w_codes")
-    _mx_check(w_scales, dev, _U8, qmoe_mx_scale_bytes(N, K), where, "w_scales")
+    _mx_check(w_scales, dev, _U8, _mx_bytes(N, K, where), where, "w_scales")
     if out is None:
         out = torch.empty((M, N), dtype=dtype, device=x_codes.device)
     else:
@@ -512,7 +521,7 @@ def qmoe_mx_tile_scales(scales_rowmajor):
     """Row-major scale bytes [R, K/32] (as checkpoints store them) -> tiles."""
     where = "qmoe_mx_tile_scales"
     R, nb = _mx_size(scales_rowmajor, where)
-    dev, n = scales_rowmajor.get_device(), qmoe_mx_scale_bytes(R, 32 * nb)
+    dev, n = scales_rowmajor.get_device(), _mx_bytes(R, 32 * nb, where)
     if n == 0:
         _bad(where, "wants scales [R, K/32]")
     _mx_check(scales_rowmajor, dev, _U8, R * nb, where, "scales")
@@ -524,7 +533,7 @@ def qmoe_mx_tile_scales(scales_rowmajor):
 def qmoe_mx_untile_scales(scales, R, K):
     """Scale tiles of an MX tensor [R, K] -> row-major bytes [R, K/32]."""
     where = "qmoe_mx_untile_scales"
-    dev, n = scales.get_device(), qmoe_mx_scale_bytes(R, K)
+    dev, n = scales.get_device(), _mx_bytes(R, K, where)
     if n == 0:
         _bad(where, "no MX tensor is [%d, %d]" % (R, K))
     _mx_check(scales, dev, _U8, n, where, "scales")

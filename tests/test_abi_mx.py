@@ -93,3 +93,55 @@ def test_scale_adapters_beyond_2_30_are_unsupported(L, R, K):
     """Past the limit the kernels' 32-bit tile counts would overflow."""
     for f in (L.qmoe_mx_tile_scales, L.qmoe_mx_untile_scales):
         assert f(FAKE, R, K, FAKE, None) == 2
+
+
+class Sized:
+    """What the binding asks of a tensor before a call, at a size that no host holds."""
+
+    def __init__(self, shape, dtype=torch.uint8):
+        self.shape, self.dtype, self.device = torch.Size(shape), dtype, torch.device("cuda", 0)
+
+    def numel(self):
+        return self.shape.numel()
+
+    def get_device(self):
+        return 0
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return FAKE
+
+
+def test_binding_refuses_sizes_that_the_abi_cannot_carry(L, monkeypatch):
+    """A size beyond 32 bits would reach the library as another one (2^32 + 32
+    columns as 32): it is refused before the call."""
+    from int4_block_quantized_gb300 import binding as B
+    calls = []
+    monkeypatch.setattr(B, "_mx_call", lambda dev, fn, where, *args: calls.append(where))
+    big, n = 2 ** 32 + 32, B.qmoe_mx_scale_bytes
+
+    def mx_of(R, K, fmt):
+        return Sized((R, K >> fmt)), Sized((n(R, K),))
+    for R, K in ((1, big), (big, 64), (1, 2 ** 31), (2 ** 31, 32), (2 ** 30 + 1, 32), (1, 2 ** 30 + 32)):
+        for fmt in (B.MXFP8, B.MXFP4):
+            c, s = mx_of(R, K, fmt)
+            small = mx_of(4, K, fmt)
+            x = Sized((R, K), torch.float16)
+            for call in (lambda: B.qmoe_mx_quantize(x, fmt, c, s),
+                         lambda: B.qmoe_mx_dequant(c, s, fmt, torch.float16, x),
+                         lambda: B.qmoe_rmsnorm_mx(x, fmt=fmt, codes=c, scales=s),
+                         lambda: B.qmoe_mx_matmul(c, s, fmt, *mx_of(4, K, B.MXFP4), torch.float16, Sized((R, 4), torch.float16)),
+                         lambda: B.qmoe_mx_matmul(*small, fmt, *mx_of(R, K, B.MXFP4), torch.float16, Sized((4, R), torch.float16))):
+                with pytest.raises(B.QMoEError) as e:
+                    call()
+                assert e.value.code == 2
+        for call in (lambda: B.qmoe_mx_tile_scales(Sized((R, K // 32))), lambda: B.qmoe_mx_untile_scales(Sized((n(R, K),)), R, K)):
+            with pytest.raises(B.QMoEError) as e:
+                call()
+            assert e.value.code == 2
+    assert not calls
+    # the largest that passes reaches the library
+    B.qmoe_mx_quantize(Sized((1, 2 ** 30), torch.float16), B.MXFP8, *mx_of(1, 2 ** 30, B.MXFP8))
+    assert calls == ["qmoe_mx_quantize"]
