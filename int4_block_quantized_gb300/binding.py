@@ -391,6 +391,13 @@ def _mx_check(t, dev, dtype, numel, where, name):
             name, numel, dtype, tuple(t.shape), t.dtype, t.device, "" if t.is_contiguous() else ", not contiguous"))
 
 
+def _mx_check2(t, dev, dtype, shape, where, name):
+    """The same, for a tensor whose shape says which element is which."""
+    if dev < 0 or t.get_device() != dev or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _bad(where, "%s: wants contiguous %s %s on one CUDA device, got %s %s on %s%s" % (
+            name, tuple(shape), dtype, tuple(t.shape), t.dtype, t.device, "" if t.is_contiguous() else ", not contiguous"))
+
+
 def _mx_bytes(R, K, where):
     """qmoe_mx_scale_bytes, with the library's limit on R and K: what is beyond
     32 bits would reach it as another size."""
@@ -408,7 +415,7 @@ def _mx_out(R, K, fmt, x, dev, codes, scales, where):
     if codes is None:
         codes = torch.empty((R, cols), dtype=_U8, device=x.device)
     else:
-        _mx_check(codes, dev, _U8, R * cols, where, "codes")
+        _mx_check2(codes, dev, _U8, (R, cols), where, "codes")
     if scales is None:
         scales = torch.empty(n, dtype=_U8, device=x.device)
     else:
@@ -457,7 +464,7 @@ def qmoe_mx_dequant(codes, scales, fmt, dtype=torch.bfloat16, out=None):
     if out is None:
         out = torch.empty((M, K), dtype=dtype, device=codes.device)
     else:
-        _mx_check(out, dev, dtype, M * K, where, "out")
+        _mx_check2(out, dev, dtype, (M, K), where, "out")
     _mx_call(dev, lib().qmoe_mx_dequant, where, codes.data_ptr(), scales.data_ptr(), fmt, M, K, out.data_ptr(), dt)
     return out
 
@@ -474,15 +481,17 @@ def qmoe_rmsnorm_mx(x, residual=None, weight=None, eps=1e-6, fmt=MXFP8, residual
     codes, scales = _mx_out(T, H, fmt, x, dev, codes, scales, where)
     rp = wp = op = None
     if residual is not None:
-        _mx_check(residual, dev, dtype, T * H, where, "residual")
+        _mx_check2(residual, dev, dtype, x.shape, where, "residual")
         rp = residual.data_ptr()
         if residual_out is None:
             residual_out = torch.empty_like(x)
     if residual_out is not None:
-        _mx_check(residual_out, dev, dtype, T * H, where, "residual_out")
+        _mx_check2(residual_out, dev, dtype, x.shape, where, "residual_out")
         op = residual_out.data_ptr()
     if weight is not None:
         _mx_check(weight, dev, dtype, H, where, "weight")
+        if weight.shape[-1:] != (H,):  # [H], or [1, H] as broadcasting has it
+            _bad(where, "weight: wants [%d], got %s" % (H, tuple(weight.shape)))
         wp = weight.data_ptr()
     _mx_call(dev, lib().qmoe_rmsnorm_mx, where, x.data_ptr(), rp, wp, _MX_DT[dtype], T, H, float(eps), fmt, op,
              codes.data_ptr(), scales.data_ptr())
@@ -507,7 +516,7 @@ def qmoe_mx_matmul(x_codes, x_scales, x_fmt, w_codes, w_scales, dtype=torch.bflo
     if out is None:
         out = torch.empty((M, N), dtype=dtype, device=x_codes.device)
     else:
-        _mx_check(out, dev, dtype, M * N, where, "out")
+        _mx_check2(out, dev, dtype, (M, N), where, "out")
     st = None
     if status is not None:
         _mx_check(status, dev, torch.int32, 1, where, "status")

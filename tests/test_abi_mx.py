@@ -145,3 +145,39 @@ def test_binding_refuses_sizes_that_the_abi_cannot_carry(L, monkeypatch):
     # the largest that passes reaches the library
     B.qmoe_mx_quantize(Sized((1, 2 ** 30), torch.float16), B.MXFP8, *mx_of(1, 2 ** 30, B.MXFP8))
     assert calls == ["qmoe_mx_quantize"]
+
+
+def test_binding_refuses_shapes_that_only_count_right(L, monkeypatch):
+    """As many elements in another shape would be read or written in another
+    order than the caller's shape says."""
+    from int4_block_quantized_gb300 import binding as B
+    calls = []
+    monkeypatch.setattr(B, "_mx_call", lambda dev, fn, where, *args: calls.append(where))
+    f16, M, N, K = torch.float16, 4, 8, 64
+    s, ws, wc = Sized((512,)), Sized((512,)), Sized((N, K // 2))
+    x, c = Sized((M, K), f16), Sized((M, K))
+    for shape in ((K, M), (M * K,), (2, M // 2, K), (M, K, 1)):
+        t, u = Sized(shape, f16), Sized(shape)
+        for call in (lambda: B.qmoe_mx_quantize(x, B.MXFP8, u, s), lambda: B.qmoe_mx_dequant(c, s, B.MXFP8, f16, t),
+                     lambda: B.qmoe_rmsnorm_mx(x, t, codes=c, scales=s, residual_out=x),
+                     lambda: B.qmoe_rmsnorm_mx(x, x, codes=c, scales=s, residual_out=t),
+                     lambda: B.qmoe_rmsnorm_mx(x, codes=u, scales=s)):
+            with pytest.raises(B.QMoEError) as e:
+                call()
+            assert e.value.code == 1
+    for shape in ((N, M), (M * N,), (M // 2, 2 * N)):
+        with pytest.raises(B.QMoEError) as e:
+            B.qmoe_mx_matmul(c, s, B.MXFP8, wc, ws, f16, Sized(shape, f16))
+        assert e.value.code == 1
+    for shape in ((K, 1), (2, K // 2)):
+        with pytest.raises(B.QMoEError) as e:
+            B.qmoe_rmsnorm_mx(x, weight=Sized(shape, f16), codes=c, scales=s)
+        assert e.value.code == 1
+    assert not calls
+    B.qmoe_mx_quantize(x, B.MXFP8, c, s)
+    B.qmoe_mx_quantize(x, B.MXFP4, Sized((M, K // 2)), s)
+    B.qmoe_mx_dequant(c, s, B.MXFP8, f16, x)
+    for w in (None, Sized((K,), f16), Sized((1, K), f16)):  # a weight per column: broadcasting's shapes
+        B.qmoe_rmsnorm_mx(x, x, w, codes=c, scales=s, residual_out=x)
+    B.qmoe_mx_matmul(c, s, B.MXFP8, wc, ws, f16, Sized((M, N), f16))
+    assert len(calls) == 7
