@@ -354,6 +354,14 @@ __device__ __forceinline__ void mma_commit_mx(uint32_t e, uint64_t* bar) {
         "r"(e), "h"((uint16_t)3)
         : "memory");
 }
+// CG = 2: the leader's barrier alone
+__device__ __forceinline__ void mma_commit_mx2_own(uint32_t e, uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred e;\n setp.ne.b32 e, %1, 0;\n"
+      " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(smem_u32(bar)),
+      "r"(e)
+      : "memory");
+}
 // Instruction descriptor of the block-scaled kinds, e8m0 scales, both operands
 // K-major; the formats' codes depend on the kind, sf_a / sf_b name the byte of
 // a scale word that the instruction starts at.

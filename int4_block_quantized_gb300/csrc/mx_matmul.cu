@@ -247,6 +247,11 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
         }
       }
     }
+    // The commits to empty[] arrive in both CTAs of a pair: neither leaves
+    // before it has seen those of the last use of each slot.
+    if (CG == 2)
+      for (int i = 0; i < S && ok; ++i)
+        if (it > i) ok = mm_wait(&empty[i], ((it - 1 - i) / S) & 1, p.status, s_abort);
     if (*s_abort && half == 0 && lane == 0)  // let the copies in flight land before the CTA exits
       for (int i = 0; i < S; ++i)
         if (it > i) mbar_wait(&full[i], ((it - 1 - i) / S) & 1, nullptr);
@@ -315,7 +320,8 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
       if (ok) mma_commit_mx<CG>(el, &acc_full[b]);
     }
     if (issued) {  // all MMAs have finished before tensor memory is freed
-      mma_commit_mx<CG>(el, fin);
+      if (CG == 1) mma_commit_mx<1>(el, fin);
+      else mma_commit_mx2_own(el, fin);  // a commit to the peer's barrier too could arrive there when it has left
       mbar_wait(fin, 0, nullptr);
     }
   } else if (warp >= 2 && warp < 11) {
