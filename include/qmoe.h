@@ -454,6 +454,27 @@ int qmoe_mx_matmul(const uint8_t* x_codes, const uint8_t* x_scales, int x_format
                    const uint8_t* w_scales, int M, int N, int K, void* y, int y_dtype, uint32_t* status_dev,
                    void* stream);
 
+/* qmoe_mx_matmul with diagnostics of its failure path (all zero: the same).
+ *   wait_limit_kilocycles  the kernel's bounded waits give up after this many
+ *                          x 1024 SM cycles; 0: the default, about 2 s.
+ *   flags                  the named role waits for what cannot arrive before
+ *                          its first step, so that waits run out: the copies
+ *                          of codes or of scales, the MMAs, the output, the
+ *                          spreading of ragged rows' codes (MXFP8 x with K
+ *                          not a multiple of 128 or w_codes off a 32-byte
+ *                          boundary; else there is no such role).
+ * The roles then drain, free tensor memory and return (no trap, no hang), and
+ * status_dev reads QMOE_ST_TIMEOUT; the next call computes normally.
+ * QMOE_ERR_INVALID_ARG for unknown flags. */
+#define QMOE_DIAG_STALL_MX_CODES 1u
+#define QMOE_DIAG_STALL_MX_SCALES 2u
+#define QMOE_DIAG_STALL_MX_MMA 4u
+#define QMOE_DIAG_STALL_MX_OUTPUT 8u
+#define QMOE_DIAG_STALL_MX_SPREAD 16u
+int qmoe_mx_matmul_diagnosed(const uint8_t* x_codes, const uint8_t* x_scales, int x_format, const uint8_t* w_codes,
+                             const uint8_t* w_scales, int M, int N, int K, void* y, int y_dtype, uint32_t* status_dev,
+                             uint32_t wait_limit_kilocycles, uint32_t flags, void* stream);
+
 /* Scale-layout adapters (one-time conversion at model load): row-major
  * scales [R, K/32], as checkpoints store them, into the tiles above, and
  * back.  in and out are separate buffers of any alignment on the row-major

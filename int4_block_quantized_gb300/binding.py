@@ -20,6 +20,7 @@ AUTO_DECODE_MAX_TOKENS = 5
 DIAG_STALL_GEMM = 1
 F32 = 2                      # the microscaled entry points that say so
 MXFP8, MXFP4 = 0, 1
+DIAG_STALL_MX_CODES, DIAG_STALL_MX_SCALES, DIAG_STALL_MX_MMA, DIAG_STALL_MX_OUTPUT, DIAG_STALL_MX_SPREAD = 1, 2, 4, 8, 16
 _STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported device or shape",
            3: "workspace missing or too small", 4: "CUDA runtime error",
            5: "device wait timed out", 6: "device index check failed"}
@@ -102,6 +103,9 @@ def lib():
         L.qmoe_rmsnorm_mx.argtypes = [vp, vp, vp, i32, i32, i32, ctypes.c_float, i32, vp, vp, vp, vp]
         L.qmoe_mx_matmul.restype = i32
         L.qmoe_mx_matmul.argtypes = [vp, vp, i32, vp, vp, i32, i32, i32, vp, i32, vp, vp]
+        L.qmoe_mx_matmul_diagnosed.restype = i32
+        L.qmoe_mx_matmul_diagnosed.argtypes = [vp, vp, i32, vp, vp, i32, i32, i32, vp, i32, vp, ctypes.c_uint32,
+                                               ctypes.c_uint32, vp]
         for f in (L.qmoe_mx_tile_scales, L.qmoe_mx_untile_scales):
             f.restype = i32
             f.argtypes = [vp, i32, i32, vp, vp]
@@ -498,10 +502,12 @@ def qmoe_rmsnorm_mx(x, residual=None, weight=None, eps=1e-6, fmt=MXFP8, residual
     return codes, scales, residual_out
 
 
-def qmoe_mx_matmul(x_codes, x_scales, x_fmt, w_codes, w_scales, dtype=torch.bfloat16, out=None, status=None):
+def qmoe_mx_matmul(x_codes, x_scales, x_fmt, w_codes, w_scales, dtype=torch.bfloat16, out=None, status=None,
+                   diagnostics=None):
     """y [M, N] (fp16, bf16 or fp32) = x . W^T for an MX tensor x [M, K] and MXFP4
     weights W [N, K].  status: an int32 [1] device tensor that collects
-    QMOE_ST_TIMEOUT (zero it first)."""
+    QMOE_ST_TIMEOUT (zero it first).  diagnostics: (wait_limit_kilocycles,
+    DIAG_STALL_MX_* flags) of qmoe_mx_matmul_diagnosed."""
     where = "qmoe_mx_matmul"
     M, K = _mx_size(x_codes, where)
     N, half = _mx_size(w_codes, where)
@@ -521,8 +527,12 @@ def qmoe_mx_matmul(x_codes, x_scales, x_fmt, w_codes, w_scales, dtype=torch.bflo
     if status is not None:
         _mx_check(status, dev, torch.int32, 1, where, "status")
         st = status.data_ptr()
-    _mx_call(dev, lib().qmoe_mx_matmul, where, x_codes.data_ptr(), x_scales.data_ptr(), x_fmt, w_codes.data_ptr(),
-             w_scales.data_ptr(), M, N, K, out.data_ptr(), dt, st)
+    if diagnostics is None:
+        _mx_call(dev, lib().qmoe_mx_matmul, where, x_codes.data_ptr(), x_scales.data_ptr(), x_fmt, w_codes.data_ptr(),
+                 w_scales.data_ptr(), M, N, K, out.data_ptr(), dt, st)
+    else:
+        _mx_call(dev, lib().qmoe_mx_matmul_diagnosed, where, x_codes.data_ptr(), x_scales.data_ptr(), x_fmt,
+                 w_codes.data_ptr(), w_scales.data_ptr(), M, N, K, out.data_ptr(), dt, st, *diagnostics)
     return out
 
 

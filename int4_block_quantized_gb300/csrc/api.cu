@@ -577,12 +577,22 @@ int qmoe_rmsnorm_mx(const void* x, const void* residual, const void* weight, int
 int qmoe_mx_matmul(const uint8_t* x_codes, const uint8_t* x_scales, int x_format, const uint8_t* w_codes,
                    const uint8_t* w_scales, int M, int N, int K, void* y, int y_dtype, uint32_t* status_dev,
                    void* stream) {
+  return qmoe_mx_matmul_diagnosed(x_codes, x_scales, x_format, w_codes, w_scales, M, N, K, y, y_dtype, status_dev, 0, 0,
+                                  stream);
+}
+
+int qmoe_mx_matmul_diagnosed(const uint8_t* x_codes, const uint8_t* x_scales, int x_format, const uint8_t* w_codes,
+                             const uint8_t* w_scales, int M, int N, int K, void* y, int y_dtype, uint32_t* status_dev,
+                             uint32_t wait_limit_kilocycles, uint32_t flags, void* stream) {
+  if (flags & ~(QMOE_DIAG_STALL_MX_CODES | QMOE_DIAG_STALL_MX_SCALES | QMOE_DIAG_STALL_MX_MMA |
+                QMOE_DIAG_STALL_MX_OUTPUT | QMOE_DIAG_STALL_MX_SPREAD))
+    return QMOE_ERR_INVALID_ARG;
   if (!valid_dtype_or_f32(y_dtype) || !y || !aligned(y, y_dtype == QMOE_F32 ? 4 : 2) || !aligned(status_dev, 4))
     return QMOE_ERR_INVALID_ARG;
   int rc = check_mx(x_codes, x_scales, x_format, M, K);
   if (rc || (rc = check_mx(w_codes, w_scales, QMOE_MXFP4, N, K)) || (rc = check_device())) return rc;
   return cuda_status(launch_mx_matmul(x_codes, x_scales, x_format, w_codes, w_scales, M, N, K, y, y_dtype, status_dev,
-                                      (cudaStream_t)stream));
+                                      wait_limit_kilocycles, flags, (cudaStream_t)stream));
 }
 
 int qmoe_mx_tile_scales(const uint8_t* scales_rowmajor, int R, int K, uint8_t* scales, void* stream) {

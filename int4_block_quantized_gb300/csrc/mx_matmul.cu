@@ -32,6 +32,8 @@ struct MmParams {
   int row_tiles, tok_tiles, kt;  // tiles of 128 weight rows, of BN tokens; scale tiles along K
   int wide_out;                  // y: 16 bits, rows on 16-byte boundaries
   int split;                     // CTAs of a cluster that share a tile's K
+  uint32_t stall;                // QMOE_DIAG_STALL_MX_*: this role waits for what cannot arrive
+  long long wait_limit;          // SM cycles
 };
 
 template <int XF, int BN, int CG, bool FILL = false>
@@ -64,14 +66,20 @@ struct MmPlan {
   static constexpr uint32_t kCols0 = kSfb + 4 * kWords * kTokSf;
 };
 
-// Bounded wait; gives up when another role has (about 2 s, status bit).
-__device__ __forceinline__ bool mm_wait(uint64_t* bar, uint32_t parity, uint32_t* status, volatile int* abort) {
-  if (mbar_try_wait(bar, parity)) return true;
+// Has the phase ended?  One answer for the warp, all of whose lanes ask: each
+// may see the end at another poll, and a warp goes on or gives up as one.
+__device__ __forceinline__ bool mm_poll(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_try_wait(bar, parity));
+}
+// Bounded wait of a whole warp; gives up when another role has, or after the
+// limit (about 2 s) with the status bit.
+__device__ __forceinline__ bool mm_wait(uint64_t* bar, uint32_t parity, const MmParams& p, volatile int* abort) {
+  if (mm_poll(bar, parity)) return true;
   const long long t0 = clock64();
-  while (!mbar_try_wait_sleep(bar, parity, 20000u)) {
-    if (*abort) return false;
-    if (clock64() - t0 > kWaitLimitCycles) {
-      set_status(status, QMOE_ST_TIMEOUT);
+  while (!__all_sync(0xffffffffu, mbar_try_wait_sleep(bar, parity, 20000u))) {
+    const bool late = clock64() - t0 > p.wait_limit;
+    if (__any_sync(0xffffffffu, late || *abort)) {
+      if (late) set_status(p.status, QMOE_ST_TIMEOUT);
       *abort = 1;
       return false;
     }
@@ -144,7 +152,8 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
   uint64_t* fin = acc_free + 2;
   uint64_t* raw_full = fin + 1;  // [kRawSlots]
   uint64_t* raw_empty = raw_full + P::kRawSlots;
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(raw_empty + P::kRawSlots);
+  uint64_t* never = raw_empty + P::kRawSlots;  // nothing arrives here (p.stall)
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(never + 1);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   uint8_t* outbuf = smem + kMmBars;  // 1024-byte aligned, as the ring behind it
   uint8_t* raw = outbuf + P::kOut;
@@ -163,6 +172,7 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
       mbar_init(&acc_free[b], 8 * CG);
     }
     mbar_init(fin, 1);
+    mbar_init(never, 1);
     for (int s = 0; s < P::kRawSlots; ++s) {
       mbar_init(&raw_full[s], 1);
       mbar_init(&raw_empty[s], 4);
@@ -195,13 +205,14 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
   const int tiles = p.row_tiles * p.tok_tiles;
   const int first = blockIdx.x / (CG * p.split), step = p.split > 1 ? tiles : gridDim.x / CG;
   const int chunks = (p.K + P::kStageK - 1) / P::kStageK;
+  auto stalled = [&](uint32_t role) { return (p.stall & role) && !mm_wait(never, 0, p, s_abort); };
   const int c0 = (int)((long long)chunks * rank / p.split), c1 = (int)((long long)chunks * (rank + 1) / p.split);
 
   if (warp == 0 || warp == 6) {
     // ------------------------------ copies: warp 0 the codes, warp 6 the scales
     int it = 0, s = 0;
     uint32_t ph = 0;
-    bool ok = true;
+    bool ok = !stalled(warp == 0 ? QMOE_DIAG_STALL_MX_CODES : QMOE_DIAG_STALL_MX_SCALES);
     const uint32_t el = elect_lane();
     for (int t = first; t < tiles && ok; t += step) {
       int rt, tt;
@@ -210,7 +221,7 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
       // scale tiles of the tokens: those that exist (128-row tiles m0 / 128 ..)
       const int t0 = m0 >> 7, nt = min(P::kTokSf, ((p.M + 127) >> 7) - t0);
       for (int c = c0; c < c1; ++c, ++it) {
-        if (it >= S) ok = mm_wait(&empty[s], ph ^ 1u, p.status, s_abort);
+        if (it >= S) ok = mm_wait(&empty[s], ph ^ 1u, p, s_abort);
         if (!ok) break;
         if (el) {
           const int q0 = c * P::kWords, nq = min(P::kWords, p.kt - q0);
@@ -251,7 +262,7 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
     // before it has seen those of the last use of each slot.
     if (CG == 2)
       for (int i = 0; i < S && ok; ++i)
-        if (it > i) ok = mm_wait(&empty[i], ((it - 1 - i) / S) & 1, p.status, s_abort);
+        if (it > i) ok = mm_wait(&empty[i], ((it - 1 - i) / S) & 1, p, s_abort);
     if (*s_abort && half == 0 && lane == 0)  // let the copies in flight land before the CTA exits
       for (int i = 0; i < S; ++i)
         if (it > i) mbar_wait(&full[i], ((it - 1 - i) / S) & 1, nullptr);
@@ -259,16 +270,16 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
     // --------------------------------------------------------------- MMAs
     int n = 0, s = 0;
     uint32_t ph = 0;
-    bool ok = true, issued = false;
+    bool ok = !stalled(QMOE_DIAG_STALL_MX_MMA), issued = false;
     const uint32_t el = elect_lane();
     for (int t = first; t < tiles && ok; t += step, ++n) {
       const int b = n & 1;
       int rt, tt;
       mm_tile(p, t, rt, tt);
       if (P::kOverlap) {
-        if (n >= 1) ok = mm_wait(&acc_free[0], (n - 1) & 1, p.status, s_abort);
+        if (n >= 1) ok = mm_wait(&acc_free[0], (n - 1) & 1, p, s_abort);
       } else {
-        if (n >= 2) ok = mm_wait(&acc_free[b], ((n >> 1) - 1) & 1, p.status, s_abort);
+        if (n >= 2) ok = mm_wait(&acc_free[b], ((n >> 1) - 1) & 1, p, s_abort);
       }
       if (!ok) break;
       tc_fence_after();
@@ -301,16 +312,16 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
         }
         mma_commit_mx<CG>(el, &empty[slot]);
       };
-      bool ready = mbar_try_wait(&full[s], ph);
+      bool ready = mm_poll(&full[s], ph);
       for (int c = c0; c < c1; ++c) {
-        if (!ready) ok = mm_wait(&full[s], ph, p.status, s_abort);
+        if (!ready) ok = mm_wait(&full[s], ph, p, s_abort);
         if (!ok) break;
         const int slot = s;
         if (++s == S) {
           s = 0;
           ph ^= 1u;
         }
-        ready = c + 1 < c1 && mbar_try_wait(&full[s], ph);  // the next stage's answer arrives meanwhile
+        ready = c + 1 < c1 && mm_poll(&full[s], ph);  // the next stage's answer arrives meanwhile
         tc_fence_after();
         const int left = p.K - c * P::kStageK;  // elements from here on
         if (left >= P::kStageK) issue(slot, c == c0, P::kWords, 4);
@@ -331,11 +342,12 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
     const int qd = warp & 3, row = qd * 32 + lane, set = warp > 6;
     uint8_t* buf = outbuf + (warp - 2 - set) * 2048;
     int n = 0;
-    for (int t = first; t < tiles; t += step, ++n) {
+    const bool ok = !stalled(QMOE_DIAG_STALL_MX_OUTPUT);
+    for (int t = first; t < tiles && ok; t += step, ++n) {
       const int b = n & 1;
       int rt, tt;
       mm_tile(p, t, rt, tt);
-      if (!mm_wait(&acc_full[b], (n >> 1) & 1, p.status, s_abort)) break;
+      if (!mm_wait(&acc_full[b], (n >> 1) & 1, p, s_abort)) break;
       tc_fence_after();
       const uint32_t d = tmem + ((uint32_t)(qd * 32) << 16) + (b ? P::kAcc1 : 0);
       const int m0 = tt * BN, nn = (rt * CG + half) * 128 + row;
@@ -400,7 +412,7 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
       int rt, tt;
       mm_tile(p, t, rt, tt);
       for (int c = c0; c < c1; ++c, ++it) {
-        if (it >= R) ok = mm_wait(&raw_empty[s], ph ^ 1u, p.status, s_abort);
+        if (it >= R) ok = mm_wait(&raw_empty[s], ph ^ 1u, p, s_abort);
         if (!ok) break;
         if (el) {
           mbar_arrive_expect_tx(&raw_full[s], 128 * 64);
@@ -430,13 +442,14 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
     const long long total = (long long)mine * (c1 - c0);
     int s = group, rs = group;
     uint32_t ph = 0, rph = 0;
-    for (long long n = group; n < total; n += 2) {
-      if (!mm_wait(&raw_full[rs], rph, p.status, s_abort)) break;
+    const bool ok = !stalled(QMOE_DIAG_STALL_MX_SPREAD);
+    for (long long n = group; n < total && ok; n += 2) {
+      if (!mm_wait(&raw_full[rs], rph, p, s_abort)) break;
       const uint4* src = reinterpret_cast<const uint4*>(raw + rs * 128 * 64 + r0 * 64 + piece * 16);
       uint4 v[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = src[32 * i];
-      if (n >= S && !mm_wait(&empty[s], ph ^ 1u, p.status, s_abort)) break;
+      if (n >= S && !mm_wait(&empty[s], ph ^ 1u, p, s_abort)) break;
       // 16-byte pieces 2 piece and 2 piece + 1 of the row, swizzled by row % 8 = r0 % 8
       uint8_t* st = ring + s * P::kAb + r0 * 128;
       uint4* lo = reinterpret_cast<uint4*>(st + (((2 * piece) ^ (r0 & 7)) << 4));
@@ -685,8 +698,11 @@ static cudaError_t launch_mm_bn(const MmParams& p, const uint8_t* xc, cudaStream
 }
 
 cudaError_t launch_mx_matmul(const uint8_t* xc, const uint8_t* xs, int x_format, const uint8_t* wc, const uint8_t* ws,
-                             int M, int N, int K, void* y, int y_dtype, uint32_t* status, cudaStream_t st) {
+                             int M, int N, int K, void* y, int y_dtype, uint32_t* status,
+                             uint32_t wait_limit_kilocycles, uint32_t stall, cudaStream_t st) {
   MmParams p = {};
+  p.stall = stall;
+  p.wait_limit = wait_limit_kilocycles ? (long long)wait_limit_kilocycles << 10 : kWaitLimitCycles;
   p.xs = xs;
   p.ws = ws;
   p.wc = wc;

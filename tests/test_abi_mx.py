@@ -181,3 +181,9 @@ def test_binding_refuses_shapes_that_only_count_right(L, monkeypatch):
         B.qmoe_rmsnorm_mx(x, x, w, codes=c, scales=s, residual_out=x)
     B.qmoe_mx_matmul(c, s, B.MXFP8, wc, ws, f16, Sized((M, N), f16))
     assert len(calls) == 7
+
+
+def test_diagnosed_product_refuses_unknown_flags(L):
+    for flags in (32, 63, 1 << 31):
+        assert L.qmoe_mx_matmul_diagnosed(FAKE, FAKE, 0, FAKE, FAKE, 4, 8, 64, FAKE, 0, None, 1, flags, None) == 1
+    assert L.qmoe_mx_matmul_diagnosed(FAKE, FAKE, 0, FAKE, FAKE, 4, 8, 65, FAKE, 0, None, 1, 1, None) == 1
