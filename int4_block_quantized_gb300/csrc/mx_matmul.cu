@@ -66,25 +66,47 @@ struct MmPlan {
   static constexpr uint32_t kCols0 = kSfb + 4 * kWords * kTokSf;
 };
 
-// Has the phase ended?  One answer for the warp, all of whose lanes ask: each
-// may see the end at another poll, and a warp goes on or gives up as one.
-__device__ __forceinline__ bool mm_poll(uint64_t* bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, mbar_try_wait(bar, parity));
-}
-// Bounded wait of a whole warp; gives up when another role has, or after the
-// limit (about 2 s) with the status bit.
+// Bounded wait; gives up when another role has, or after the limit (about 2 s)
+// with the status bit.  WARP: all lanes of the warp wait, and they agree on the
+// answer (each may see the phase end at another poll, and aligned instructions
+// or warp barriers follow).  The warp that issues MMAs has neither: what its
+// elected lane sees decides all that it does, and the other lanes only follow.
+// (With votes there, 16 x 8192 x 8192 takes 0.1 us more.)
+template <bool WARP = true>
 __device__ __forceinline__ bool mm_wait(uint64_t* bar, uint32_t parity, const MmParams& p, volatile int* abort) {
-  if (mm_poll(bar, parity)) return true;
+  auto all = [](bool v) { return WARP ? __all_sync(0xffffffffu, v) != 0 : v; };
+  if (all(mbar_try_wait(bar, parity))) return true;
   const long long t0 = clock64();
-  while (!__all_sync(0xffffffffu, mbar_try_wait_sleep(bar, parity, 20000u))) {
+  while (!all(mbar_try_wait_sleep(bar, parity, 20000u))) {
     const bool late = clock64() - t0 > p.wait_limit;
-    if (__any_sync(0xffffffffu, late || *abort)) {
+    if (!all(!(late || *abort))) {
       if (late) set_status(p.status, QMOE_ST_TIMEOUT);
       *abort = 1;
       return false;
     }
   }
   return true;
+}
+
+// The end of a warp that has issued `it` copies into a ring of S slots: it
+// waits for the last use of each, time-out or not (a role that gives up does so
+// at any time, also after this warp's last step), so that no copy lands in
+// shared memory that is another CTA's by then.  After a time-out slots may stay
+// as they are; a copy lands within microseconds, so 10 ms for all of them do.
+constexpr long long kMmSettleCycles = 20000000;
+template <int S>
+__device__ __forceinline__ void mm_settle(uint64_t* bars, int it, const MmParams& p, volatile int* abort) {
+  const long long t0 = clock64();
+  for (int n = max(it - S, 0); n < it; ++n)  // the oldest first: no poll is left when the last has come
+    while (!mbar_try_wait_sleep(&bars[n % S], (n / S) & 1, 20000u)) {
+      const long long t = clock64() - t0;
+      if (*abort) {
+        if (t > kMmSettleCycles) break;
+      } else if (t > p.wait_limit) {
+        set_status(p.status, QMOE_ST_TIMEOUT);
+        *abort = 1;
+      }
+    }
 }
 
 __device__ __forceinline__ void mm_store(const MmParams& p, size_t i, float v) {
@@ -258,14 +280,9 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
         }
       }
     }
-    // The commits to empty[] arrive in both CTAs of a pair: neither leaves
-    // before it has seen those of the last use of each slot.
-    if (CG == 2)
-      for (int i = 0; i < S && ok; ++i)
-        if (it > i) ok = mm_wait(&empty[i], ((it - 1 - i) / S) & 1, p, s_abort);
-    if (*s_abort && half == 0 && lane == 0)  // let the copies in flight land before the CTA exits
-      for (int i = 0; i < S; ++i)
-        if (it > i) mbar_wait(&full[i], ((it - 1 - i) / S) & 1, nullptr);
+    // A pair's stages are counted in the leader alone, but both CTAs see the
+    // commits that give slots back (and stay until these have arrived).
+    if (lane == 0) mm_settle<S>(CG == 1 ? full : empty, it, p, s_abort);
   } else if (warp == 1 && half == 0) {
     // --------------------------------------------------------------- MMAs
     int n = 0, s = 0;
@@ -277,9 +294,9 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
       int rt, tt;
       mm_tile(p, t, rt, tt);
       if (P::kOverlap) {
-        if (n >= 1) ok = mm_wait(&acc_free[0], (n - 1) & 1, p, s_abort);
+        if (n >= 1) ok = mm_wait<false>(&acc_free[0], (n - 1) & 1, p, s_abort);
       } else {
-        if (n >= 2) ok = mm_wait(&acc_free[b], ((n >> 1) - 1) & 1, p, s_abort);
+        if (n >= 2) ok = mm_wait<false>(&acc_free[b], ((n >> 1) - 1) & 1, p, s_abort);
       }
       if (!ok) break;
       tc_fence_after();
@@ -312,16 +329,16 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
         }
         mma_commit_mx<CG>(el, &empty[slot]);
       };
-      bool ready = mm_poll(&full[s], ph);
+      bool ready = mbar_try_wait(&full[s], ph);
       for (int c = c0; c < c1; ++c) {
-        if (!ready) ok = mm_wait(&full[s], ph, p, s_abort);
+        if (!ready) ok = mm_wait<false>(&full[s], ph, p, s_abort);
         if (!ok) break;
         const int slot = s;
         if (++s == S) {
           s = 0;
           ph ^= 1u;
         }
-        ready = c + 1 < c1 && mm_poll(&full[s], ph);  // the next stage's answer arrives meanwhile
+        ready = c + 1 < c1 && mbar_try_wait(&full[s], ph);  // the next stage's answer arrives meanwhile
         tc_fence_after();
         const int left = p.K - c * P::kStageK;  // elements from here on
         if (left >= P::kStageK) issue(slot, c == c0, P::kWords, 4);
@@ -333,7 +350,7 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
     if (issued) {  // all MMAs have finished before tensor memory is freed
       if (CG == 1) mma_commit_mx<1>(el, fin);
       else mma_commit_mx2_own(el, fin);  // a commit to the peer's barrier too could arrive there when it has left
-      mbar_wait(fin, 0, nullptr);
+      if (el) mbar_wait(fin, 0, nullptr);
     }
   } else if (warp >= 2 && warp < 11) {
     // ------------------------------------------------------------- outputs
@@ -425,9 +442,7 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
         }
       }
     }
-    if (*s_abort && lane == 0)
-      for (int i = 0; i < R; ++i)
-        if (it > i) mbar_wait(&raw_full[i], ((it - 1 - i) / R) & 1, nullptr);
+    if (lane == 0) mm_settle<R>(raw_full, it, p, s_abort);
   } else if (FILL && warp >= kMmThreads / 32) {
     // ---------------------- codes of ragged rows spread to 16 bytes per 8 (MXFP8 x)
     // Two groups of four warps take turns at the stages; a warp takes 32 rows,

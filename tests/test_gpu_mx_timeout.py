@@ -55,3 +55,24 @@ def test_a_stalled_mma_is_reported(name):
     for diagnostics in (None, (0, 0)):
         assert torch.equal(B.qmoe_mx_matmul(*x, xf, *w, status=status, diagnostics=diagnostics), ref)
     assert int(status.item()) == 0
+
+
+ROLES = {"codes": B.DIAG_STALL_MX_CODES, "scales": B.DIAG_STALL_MX_SCALES, "mma": B.DIAG_STALL_MX_MMA,
+         "output": B.DIAG_STALL_MX_OUTPUT, "spread": B.DIAG_STALL_MX_SPREAD}
+
+
+SPREADS = ("spread", "spread, split", "split in the ring")  # the sizes whose codes are spread
+
+
+@pytest.mark.parametrize("name,role", [(n, r) for n in SHAPES for r in ROLES if r != "spread" or n in SPREADS])
+def test_a_stalled_role_drains_against_one_deadline(name, role):
+    """However many slots are in flight, and whichever role it is: the limit of
+    0.5 ms and the 10 ms that copies get, not 2 s per slot.  Every CTA of a grid
+    runs at once, so a second is generous."""
+    M, N, K, xf = SHAPES[name]
+    x, w = tensors(M, N, K, xf)
+    ref = B.qmoe_mx_matmul(*x, xf, *w)
+    bits, seconds, _ = run_out(x, xf, w, ROLES[role])
+    assert bits == 1 and seconds < 1.0, seconds
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    assert torch.equal(B.qmoe_mx_matmul(*x, xf, *w, status=status), ref) and int(status.item()) == 0
