@@ -447,12 +447,19 @@ int qmoe_rmsnorm_mx(const void* x, const void* residual, const void* weight, int
  * calls here write it so), that behind the last row may be anything.
  * One kernel; the choice of its tile and the split of K go by M, N and K
  * alone, and results are the same in every call.  status_dev (a 4-byte device word that the caller
- * set to 0, or NULL): a bounded wait of the kernel that ran out sets
- * QMOE_ST_TIMEOUT there (y is then undefined); read it with
- * qmoe_get_device_status(status_dev, ...). */
+ * set to 0): a bounded wait of the kernel that ran out sets QMOE_ST_TIMEOUT
+ * there (y is then undefined); read it with qmoe_get_device_status(status_dev,
+ * ...).  NULL: the same in a word of the library's, one per device
+ * (qmoe_mx_status). */
 int qmoe_mx_matmul(const uint8_t* x_codes, const uint8_t* x_scales, int x_format, const uint8_t* w_codes,
                    const uint8_t* w_scales, int M, int N, int K, void* y, int y_dtype, uint32_t* status_dev,
                    void* stream);
+
+/* The status word, on the current device, of the products that were given
+ * none: read and cleared like qmoe_get_device_status (blocking: synchronises
+ * `stream`, on which those products should have run).  QMOE_ERR_TIMEOUT: a
+ * product since the last read is not valid. */
+int qmoe_mx_status(uint32_t* bits_out, void* stream);
 
 /* qmoe_mx_matmul with diagnostics of its failure path (all zero: the same).
  *   wait_limit_kilocycles  the kernel's bounded waits give up after this many
@@ -464,7 +471,7 @@ int qmoe_mx_matmul(const uint8_t* x_codes, const uint8_t* x_scales, int x_format
  *                          not a multiple of 128 or w_codes off a 32-byte
  *                          boundary; else there is no such role).
  * The roles then drain, free tensor memory and return (no trap, no hang), and
- * status_dev reads QMOE_ST_TIMEOUT; the next call computes normally.
+ * the status reads QMOE_ST_TIMEOUT; the next call computes normally.
  * QMOE_ERR_INVALID_ARG for unknown flags. */
 #define QMOE_DIAG_STALL_MX_CODES 1u
 #define QMOE_DIAG_STALL_MX_SCALES 2u

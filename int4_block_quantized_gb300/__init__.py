@@ -13,7 +13,7 @@ def __getattr__(name):
     if name in ("qmoe_route", "matmul_nbits", "qmoe_forward", "qmoe_dequant", "qmoe_rmsnorm",
                 "qmoe_workspace_size", "qmoe_status_string", "QMoEError", "Workspace",
                 "qmoe_mx_quantize", "qmoe_mx_dequant", "qmoe_rmsnorm_mx", "qmoe_mx_matmul",
-                "qmoe_mx_tile_scales", "qmoe_mx_untile_scales", "qmoe_mx_scale_bytes", "MXFP8", "MXFP4"):
+                "qmoe_mx_tile_scales", "qmoe_mx_untile_scales", "qmoe_mx_scale_bytes", "qmoe_mx_status", "MXFP8", "MXFP4"):
         from . import binding
         return getattr(binding, name)
     raise AttributeError(name)

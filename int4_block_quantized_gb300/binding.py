@@ -106,6 +106,8 @@ def lib():
         L.qmoe_mx_matmul_diagnosed.restype = i32
         L.qmoe_mx_matmul_diagnosed.argtypes = [vp, vp, i32, vp, vp, i32, i32, i32, vp, i32, vp, ctypes.c_uint32,
                                                ctypes.c_uint32, vp]
+        L.qmoe_mx_status.restype = i32
+        L.qmoe_mx_status.argtypes = [ctypes.POINTER(ctypes.c_uint32), vp]
         for f in (L.qmoe_mx_tile_scales, L.qmoe_mx_untile_scales):
             f.restype = i32
             f.argtypes = [vp, i32, i32, vp, vp]
@@ -506,7 +508,7 @@ def qmoe_mx_matmul(x_codes, x_scales, x_fmt, w_codes, w_scales, dtype=torch.bflo
                    diagnostics=None):
     """y [M, N] (fp16, bf16 or fp32) = x . W^T for an MX tensor x [M, K] and MXFP4
     weights W [N, K].  status: an int32 [1] device tensor that collects
-    QMOE_ST_TIMEOUT (zero it first).  diagnostics: (wait_limit_kilocycles,
+    QMOE_ST_TIMEOUT (zero it first); without one qmoe_mx_status() tells.  diagnostics: (wait_limit_kilocycles,
     DIAG_STALL_MX_* flags) of qmoe_mx_matmul_diagnosed."""
     where = "qmoe_mx_matmul"
     M, K = _mx_size(x_codes, where)
@@ -534,6 +536,17 @@ def qmoe_mx_matmul(x_codes, x_scales, x_fmt, w_codes, w_scales, dtype=torch.bflo
         _mx_call(dev, lib().qmoe_mx_matmul_diagnosed, where, x_codes.data_ptr(), x_scales.data_ptr(), x_fmt,
                  w_codes.data_ptr(), w_scales.data_ptr(), M, N, K, out.data_ptr(), dt, st, *diagnostics)
     return out
+
+
+def qmoe_mx_status():
+    """(code, bits) of the products on the current device that were given no
+    status tensor, and cleared: code 5 where one of them timed out.  Waits for
+    the current stream."""
+    bits = ctypes.c_uint32(0)
+    rc = lib().qmoe_mx_status(ctypes.byref(bits), _stream())
+    if rc not in (0, 5):
+        _check(rc, "qmoe_mx_status")
+    return rc, bits.value
 
 
 def qmoe_mx_tile_scales(scales_rowmajor):

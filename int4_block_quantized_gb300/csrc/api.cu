@@ -595,6 +595,14 @@ int qmoe_mx_matmul_diagnosed(const uint8_t* x_codes, const uint8_t* x_scales, in
                                       wait_limit_kilocycles, flags, (cudaStream_t)stream));
 }
 
+int qmoe_mx_status(uint32_t* bits_out, void* stream) {
+  int rc = check_device();
+  if (rc) return rc;
+  void* word = nullptr;
+  if ((rc = cuda_status(mx_status_word(&word)))) return rc;
+  return qmoe_get_device_status(word, bits_out, stream);
+}
+
 int qmoe_mx_tile_scales(const uint8_t* scales_rowmajor, int R, int K, uint8_t* scales, void* stream) {
   if (!scales_rowmajor || !scales || !aligned(scales, 16)) return QMOE_ERR_INVALID_ARG;
   int rc = check_mx_size(R, K);

@@ -66,6 +66,12 @@ struct MmPlan {
   static constexpr uint32_t kCols0 = kSfb + 4 * kWords * kTokSf;
 };
 
+// The status word of the calls that bring none.
+__device__ uint32_t g_mx_status;
+__device__ __forceinline__ void mm_timed_out(const MmParams& p) {
+  set_status(p.status ? p.status : &g_mx_status, QMOE_ST_TIMEOUT);
+}
+
 // Bounded wait; gives up when another role has, or after the limit (about 2 s)
 // with the status bit.  WARP: all lanes of the warp wait, and they agree on the
 // answer (each may see the phase end at another poll, and aligned instructions
@@ -80,7 +86,7 @@ __device__ __forceinline__ bool mm_wait(uint64_t* bar, uint32_t parity, const Mm
   while (!all(mbar_try_wait_sleep(bar, parity, 20000u))) {
     const bool late = clock64() - t0 > p.wait_limit;
     if (!all(!(late || *abort))) {
-      if (late) set_status(p.status, QMOE_ST_TIMEOUT);
+      if (late) mm_timed_out(p);
       *abort = 1;
       return false;
     }
@@ -103,7 +109,7 @@ __device__ __forceinline__ void mm_settle(uint64_t* bars, int it, const MmParams
       if (*abort) {
         if (t > kMmSettleCycles) break;
       } else if (t > p.wait_limit) {
-        set_status(p.status, QMOE_ST_TIMEOUT);
+        mm_timed_out(p);
         *abort = 1;
       }
     }
@@ -711,6 +717,8 @@ static cudaError_t launch_mm_bn(const MmParams& p, const uint8_t* xc, cudaStream
   }
   return launch_mm<XF, 192, 1, FILL>(p, 1, xc, st);
 }
+
+cudaError_t mx_status_word(void** word) { return cudaGetSymbolAddress(word, g_mx_status); }
 
 cudaError_t launch_mx_matmul(const uint8_t* xc, const uint8_t* xs, int x_format, const uint8_t* wc, const uint8_t* ws,
                              int M, int N, int K, void* y, int y_dtype, uint32_t* status,

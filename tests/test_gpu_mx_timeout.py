@@ -76,3 +76,23 @@ def test_a_stalled_role_drains_against_one_deadline(name, role):
     assert bits == 1 and seconds < 1.0, seconds
     status = torch.zeros(1, dtype=torch.int32, device=DEV)
     assert torch.equal(B.qmoe_mx_matmul(*x, xf, *w, status=status), ref) and int(status.item()) == 0
+
+
+def test_a_call_without_a_status_word_is_reported_too():
+    """In the library's own word: read once, then clear; a call with a word of
+    its own does not set it, and a captured call does."""
+    M, N, K, xf = SHAPES["split"]
+    x, w = tensors(M, N, K, xf)
+    assert B.qmoe_mx_status() == (0, 0)
+    B.qmoe_mx_matmul(*x, xf, *w, diagnostics=(LIMIT, B.DIAG_STALL_MX_MMA))
+    assert B.qmoe_mx_status() == (5, 1)
+    assert B.qmoe_mx_status() == (0, 0)
+    assert run_out(x, xf, w, B.DIAG_STALL_MX_MMA)[0] == 1 and B.qmoe_mx_status() == (0, 0)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        B.qmoe_mx_matmul(*x, xf, *w, diagnostics=(LIMIT, B.DIAG_STALL_MX_MMA))
+    assert B.qmoe_mx_status() == (0, 0)
+    g.replay()
+    assert B.qmoe_mx_status() == (5, 1)
+    B.qmoe_mx_matmul(*x, xf, *w)
+    assert B.qmoe_mx_status() == (0, 0)
