@@ -445,9 +445,10 @@ int qmoe_rmsnorm_mx(const void* x, const void* residual, const void* weight, int
  * y aligned to its element size).  Any M and N >= 1.  A NaN scale makes the
  * outputs of its row NaN; the scales' padding behind K has to be zeros (the
  * calls here write it so), that behind the last row may be anything.
- * One kernel; the choice of its tile and the split of K go by M, N and K
- * alone, and results are the same in every call.  status_dev (a 4-byte device word that the caller
- * set to 0): a bounded wait of the kernel that ran out sets QMOE_ST_TIMEOUT
+ * One kernel.  Its tile and the split of K are chosen by M, N, K, x_format,
+ * whether w_codes lies on a 32-byte boundary (MXFP8 x), and the device: calls
+ * that agree in these give the same bits, others sum in another order.
+ * status_dev (a 4-byte device word that the caller set to 0): a bounded wait of the kernel that ran out sets QMOE_ST_TIMEOUT
  * there (y is then undefined); read it with qmoe_get_device_status(status_dev,
  * ...).  NULL: the same in a word of the library's, one per device
  * (qmoe_mx_status). */

@@ -625,12 +625,16 @@ static cudaError_t launch_mm(MmParams p, int split, const uint8_t* xc, cudaStrea
   return cudaLaunchKernelEx(&cfg, kernel, tw, tx, tws, txs, p);
 }
 
-// CTAs of clusters of `split` that the device holds at once, one CTA to an SM.
-static int mm_capacity(int split) {
-  static int cached[64][4] = {};
-  const int l = split == 8 ? 3 : split == 4 ? 2 : split == 2 ? 1 : 0;
+// CTAs of clusters of `split` (2, 4, 8) that the device holds at once, one CTA
+// to an SM.  A query that fails fails the call: with a guess in its place, the
+// same call would sum in another order another time.
+static cudaError_t mm_capacity(int split, int* ctas) {
+  static int cached[64][4] = {};  // CTAs + 1
+  const int l = split == 8 ? 3 : split == 4 ? 2 : 1;
   int dev = 0;
-  if (l == 0 || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return device_sm_count();
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!cached[dev][l]) {
     auto kernel = mx_matmul_kernel<kMxfp4, 16, 1, false>;
     cudaLaunchConfig_t cfg = {};
@@ -644,11 +648,13 @@ static int mm_capacity(int split) {
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     int n = 0;
-    if (ensure_smem(kernel, kMmSmem) != cudaSuccess || cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1)
-      return split;  // not known: no more than one cluster at a time
-    cached[dev][l] = n * split;
+    if ((err = ensure_smem(kernel, kMmSmem)) != cudaSuccess ||
+        (err = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg)) != cudaSuccess)
+      return err;
+    cached[dev][l] = n * split + 1;
   }
-  return cached[dev][l];
+  *ctas = cached[dev][l] - 1;
+  return cudaSuccess;
 }
 
 // Tokens per tile (and a pair of CTAs or one) and CTAs per tile along K, by an
@@ -671,14 +677,18 @@ static int mm_capacity(int split) {
 struct MmChoice {
   int bn, cg, split;
 };
-static MmChoice mm_choose(int M, int N, int chunks, bool fill) {
+static cudaError_t mm_choose(int M, int N, int chunks, bool fill, MmChoice* choice) {
   static const struct {
     int bn, cg, start, stage, tile, epilogue, exchange;
   } kinds[] = {{16, 1, 1900, 170, 300, 200, 1200},   {32, 1, 2000, 170, 350, 300, 1300},
                {64, 1, 2900, 165, 500, 850, 1400},   {128, 1, 3600, 185, 1200, 1350, 2900},
                {192, 1, 3900, 250, 800, 1900, 0},    {192, 2, 4200, 240, 300, 3000, 0},
                {256, 2, 4600, 300, 1250, 2700, 0}};
-  MmChoice best = {128, 1, 1};
+  int capacity[9] = {};
+  for (int split = 2; split <= 8; split *= 2) {
+    const cudaError_t err = mm_capacity(split, &capacity[split]);
+    if (err != cudaSuccess) return err;
+  }
   long long least = -1;
   for (const auto& k : kinds) {
     if (k.bn < 64 && M > k.bn) continue;  // 16 and 32 tokens: a single tile, at the head of its scale tile
@@ -686,7 +696,7 @@ static MmChoice mm_choose(int M, int N, int chunks, bool fill) {
     const int stage = fill ? 230 + k.bn / 2 : k.stage;  // codes widened by warps: 240 ns at 16 tokens, 340 at 192
     const long long tiles = (long long)((N + 128 * k.cg - 1) / (128 * k.cg)) * ((M + k.bn - 1) / k.bn);
     for (int split = 1; split <= 8; split *= 2) {
-      if (split > 1 && (!k.exchange || split > chunks || tiles * split > mm_capacity(split))) break;
+      if (split > 1 && (!k.exchange || split > chunks || tiles * split > capacity[split])) break;
       const long long slots = split > 1 ? tiles : device_sm_count() / k.cg;
       const long long rounds = (tiles + slots - 1) / slots;
       const long long one = (long long)((chunks + split - 1) / split) * stage, more = one + k.tile;
@@ -694,17 +704,19 @@ static MmChoice mm_choose(int M, int N, int chunks, bool fill) {
                           (split > 1 ? k.exchange : 0);
       if (least < 0 || t < least) {
         least = t;
-        best = {k.bn, k.cg, split};
+        *choice = {k.bn, k.cg, split};
       }
     }
   }
-  return best;
+  return cudaSuccess;
 }
 
 template <int XF, bool FILL>
 static cudaError_t launch_mm_bn(const MmParams& p, const uint8_t* xc, cudaStream_t st) {
   const int stage = MmPlan<XF, 128, 1>::kStageK;
-  const MmChoice c = mm_choose(p.M, p.N, (p.K + stage - 1) / stage, FILL);
+  MmChoice c = {};
+  const cudaError_t err = mm_choose(p.M, p.N, (p.K + stage - 1) / stage, FILL, &c);
+  if (err != cudaSuccess) return err;
   switch (c.bn) {
     case 16: return launch_mm<XF, 16, 1, FILL>(p, c.split, xc, st);
     case 32: return launch_mm<XF, 32, 1, FILL>(p, c.split, xc, st);
