@@ -456,6 +456,12 @@ int qmoe_mx_matmul(const uint8_t* x_codes, const uint8_t* x_scales, int x_format
                    const uint8_t* w_scales, int M, int N, int K, void* y, int y_dtype, uint32_t* status_dev,
                    void* stream);
 
+/* The form of the kernel that qmoe_mx_matmul runs for such a call on the
+ * current device (no launch): variant_out[0] tokens per tile, [1] 1 for pairs
+ * of CTAs, [2] CTAs that share a tile's K, [3] 1 where warps spread the
+ * weights' codes.  w_codes is looked at for its alignment alone. */
+int qmoe_mx_matmul_variant(int x_format, const uint8_t* w_codes, int M, int N, int K, int variant_out[4]);
+
 /* The status word, on the current device, of the products that were given
  * none: read and cleared like qmoe_get_device_status (blocking: synchronises
  * `stream`, on which those products should have run).  QMOE_ERR_TIMEOUT: a

@@ -106,6 +106,8 @@ def lib():
         L.qmoe_mx_matmul_diagnosed.restype = i32
         L.qmoe_mx_matmul_diagnosed.argtypes = [vp, vp, i32, vp, vp, i32, i32, i32, vp, i32, vp, ctypes.c_uint32,
                                                ctypes.c_uint32, vp]
+        L.qmoe_mx_matmul_variant.restype = i32
+        L.qmoe_mx_matmul_variant.argtypes = [i32, vp, i32, i32, i32, ctypes.POINTER(ctypes.c_int)]
         L.qmoe_mx_status.restype = i32
         L.qmoe_mx_status.argtypes = [ctypes.POINTER(ctypes.c_uint32), vp]
         for f in (L.qmoe_mx_tile_scales, L.qmoe_mx_untile_scales):
@@ -536,6 +538,20 @@ def qmoe_mx_matmul(x_codes, x_scales, x_fmt, w_codes, w_scales, dtype=torch.bflo
         _mx_call(dev, lib().qmoe_mx_matmul_diagnosed, where, x_codes.data_ptr(), x_scales.data_ptr(), x_fmt,
                  w_codes.data_ptr(), w_scales.data_ptr(), M, N, K, out.data_ptr(), dt, st, *diagnostics)
     return out
+
+
+def qmoe_mx_matmul_variant(x_fmt, w_codes, M):
+    """(tokens per tile, pairs of CTAs, CTAs along K, codes spread by warps) of
+    the kernel that a product of M tokens with w_codes [N, K/2] runs."""
+    where = "qmoe_mx_matmul_variant"
+    N, half = _mx_size(w_codes, where)
+    _mx_bytes(N, 2 * half, where), _mx_bytes(M, 2 * half, where)
+    dev = w_codes.get_device()
+    _mx_check(w_codes, dev, _U8, N * half, where, "w_codes")
+    v = (ctypes.c_int * 4)()
+    with torch.cuda.device(dev):
+        _check(lib().qmoe_mx_matmul_variant(x_fmt, w_codes.data_ptr(), M, N, 2 * half, v), where)
+    return tuple(v)
 
 
 def qmoe_mx_status():

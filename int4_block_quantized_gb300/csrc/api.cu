@@ -595,6 +595,15 @@ int qmoe_mx_matmul_diagnosed(const uint8_t* x_codes, const uint8_t* x_scales, in
                                       wait_limit_kilocycles, flags, (cudaStream_t)stream));
 }
 
+int qmoe_mx_matmul_variant(int x_format, const uint8_t* w_codes, int M, int N, int K, int variant_out[4]) {
+  if (!variant_out || !w_codes || !aligned(w_codes, 16) || (x_format != QMOE_MXFP8 && x_format != QMOE_MXFP4) || N < 1)
+    return QMOE_ERR_INVALID_ARG;
+  int rc = check_mx_size(M, K);
+  if (rc || (rc = check_mx_size(N, K)) || (rc = check_device())) return rc;
+  return cuda_status(mx_matmul_variant(x_format, w_codes, M, N, K, variant_out, variant_out + 1, variant_out + 2,
+                                       variant_out + 3));
+}
+
 int qmoe_mx_status(uint32_t* bits_out, void* stream) {
   int rc = check_device();
   if (rc) return rc;

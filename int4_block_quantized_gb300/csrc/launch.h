@@ -87,6 +87,8 @@ cudaError_t launch_mx_retile(const uint8_t* in, uint8_t* out, int R, int K, bool
 cudaError_t launch_mx_matmul(const uint8_t* xc, const uint8_t* xs, int x_format, const uint8_t* wc, const uint8_t* ws,
                              int M, int N, int K, void* y, int y_dtype, uint32_t* status,
                              uint32_t wait_limit_kilocycles, uint32_t stall, cudaStream_t st);
+cudaError_t mx_matmul_variant(int x_format, const uint8_t* wc, int M, int N, int K, int* tokens, int* pair, int* split,
+                              int* spread);
 cudaError_t mx_status_word(void** word);  // the current device's, for calls without one
 
 cudaError_t launch_rmsnorm(const void* x, void* out, int act_dtype, int T, int H, float eps,

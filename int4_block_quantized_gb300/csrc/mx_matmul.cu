@@ -711,11 +711,31 @@ static cudaError_t mm_choose(int M, int N, int chunks, bool fill, MmChoice* choi
   return cudaSuccess;
 }
 
+// MXFP8 x: codes that TMA cannot widen (mx_matmul_kernel)
+static bool mm_fill(int x_format, int K, const uint8_t* wc) {
+  return x_format == kMxfp8 && (K % 128 || (reinterpret_cast<uintptr_t>(wc) & 31));
+}
+static cudaError_t mm_choose(int x_format, int M, int N, int K, bool fill, MmChoice* choice) {
+  const int stage = x_format == kMxfp4 ? MmPlan<kMxfp4, 128, 1>::kStageK : MmPlan<kMxfp8, 128, 1>::kStageK;
+  return mm_choose(M, N, (K + stage - 1) / stage, fill, choice);
+}
+
+cudaError_t mx_matmul_variant(int x_format, const uint8_t* wc, int M, int N, int K, int* tokens, int* pair, int* split,
+                              int* spread) {
+  MmChoice c = {};
+  const bool fill = mm_fill(x_format, K, wc);
+  const cudaError_t err = mm_choose(x_format, M, N, K, fill, &c);
+  *tokens = c.bn;
+  *pair = c.cg == 2;
+  *split = c.split;
+  *spread = fill;
+  return err;
+}
+
 template <int XF, bool FILL>
 static cudaError_t launch_mm_bn(const MmParams& p, const uint8_t* xc, cudaStream_t st) {
-  const int stage = MmPlan<XF, 128, 1>::kStageK;
   MmChoice c = {};
-  const cudaError_t err = mm_choose(p.M, p.N, (p.K + stage - 1) / stage, FILL, &c);
+  const cudaError_t err = mm_choose(XF, p.M, p.N, p.K, FILL, &c);
   if (err != cudaSuccess) return err;
   switch (c.bn) {
     case 16: return launch_mm<XF, 16, 1, FILL>(p, c.split, xc, st);
@@ -749,7 +769,7 @@ cudaError_t launch_mx_matmul(const uint8_t* xc, const uint8_t* xs, int x_format,
   p.y_dtype = y_dtype;
   p.kt = (K + 127) / 128;
   if (x_format == kMxfp4) return launch_mm_bn<kMxfp4, false>(p, xc, st);
-  if (K % 128 || (reinterpret_cast<uintptr_t>(wc) & 31)) return launch_mm_bn<kMxfp8, true>(p, xc, st);
+  if (mm_fill(x_format, K, wc)) return launch_mm_bn<kMxfp8, true>(p, xc, st);
   return launch_mm_bn<kMxfp8, false>(p, xc, st);
 }
 

@@ -187,3 +187,13 @@ def test_diagnosed_product_refuses_unknown_flags(L):
     for flags in (32, 63, 1 << 31):
         assert L.qmoe_mx_matmul_diagnosed(FAKE, FAKE, 0, FAKE, FAKE, 4, 8, 64, FAKE, 0, None, 1, flags, None) == 1
     assert L.qmoe_mx_matmul_diagnosed(FAKE, FAKE, 0, FAKE, FAKE, 4, 8, 65, FAKE, 0, None, 1, 1, None) == 1
+
+
+def test_variant_query_refuses(L):
+    import ctypes
+    v = (ctypes.c_int * 4)()
+    for a in ((2, FAKE, 4, 8, 64), (0, None, 4, 8, 64), (0, FAKE + 8, 4, 8, 64), (0, FAKE, 0, 8, 64), (0, FAKE, 4, 0, 64),
+              (0, FAKE, 4, 8, 48)):
+        assert L.qmoe_mx_matmul_variant(*a, v) == 1
+    assert L.qmoe_mx_matmul_variant(0, FAKE, 4, 8, 64, None) == 1
+    assert L.qmoe_mx_matmul_variant(0, FAKE, (1 << 30) + 1, 8, 64, v) == 2
