@@ -482,23 +482,24 @@ def qmoe_rmsnorm_mx(x, residual=None, weight=None, eps=1e-6, fmt=MXFP8, residual
     or MXFP4; residual_out = x + residual (a new tensor unless given; it may be
     x or residual itself).  Without a residual it is None unless given."""
     where = "qmoe_rmsnorm_mx"
-    T, H = _mx_size(x, where)
+    T, H = shape = _mx_size(x, where)
     dtype, dev = x.dtype, x.get_device()
     if dev < 0 or not x.is_contiguous() or (dtype is not torch.float16 and dtype is not torch.bfloat16):
         _bad(where, "x: wants a contiguous CUDA tensor of fp16 or bf16, got %s on %s" % (dtype, x.device))
     codes, scales = _mx_out(T, H, fmt, x, dev, codes, scales, where)
     rp = wp = op = None
     if residual is not None:
-        _mx_check2(residual, dev, dtype, x.shape, where, "residual")
+        _mx_check2(residual, dev, dtype, shape, where, "residual")
         rp = residual.data_ptr()
-        if residual_out is None:
-            residual_out = torch.empty_like(x)
     if residual_out is not None:
-        _mx_check2(residual_out, dev, dtype, x.shape, where, "residual_out")
+        _mx_check2(residual_out, dev, dtype, shape, where, "residual_out")
+        op = residual_out.data_ptr()
+    elif residual is not None:
+        residual_out = torch.empty_like(x)
         op = residual_out.data_ptr()
     if weight is not None:
         _mx_check(weight, dev, dtype, H, where, "weight")
-        if weight.shape[-1:] != (H,):  # [H], or [1, H] as broadcasting has it
+        if weight.shape[-1] != H:  # [H], or [1, H] as broadcasting has it
             _bad(where, "weight: wants [%d], got %s" % (H, tuple(weight.shape)))
         wp = weight.data_ptr()
     _mx_call(dev, lib().qmoe_rmsnorm_mx, where, x.data_ptr(), rp, wp, _MX_DT[dtype], T, H, float(eps), fmt, op,
