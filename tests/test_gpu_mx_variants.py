@@ -157,3 +157,17 @@ def test_pairs_beside_the_layer_on_another_stream():
     assert ws.status() == (0, 0) and B.qmoe_mx_status() == (0, 0)
     assert all(torch.equal(w, w_ref) and torch.equal(i, ids_ref) for w, i in routed)
     assert all(torch.equal(y, refs[i % 2]) for i, y in enumerate(got))
+
+
+def test_outputs_beyond_32_bit_offsets():
+    """More than 2^32 outputs, whichever way they are written: the last tokens as
+    computed alone (K = 32 is one instruction, so the sums are the same ones)."""
+    M, N, K = 66001, 65608, 32
+    x, w = random_mx(M, K, B.MXFP8, 1), random_mx(N, K, B.MXFP4, 2)
+    wd = to_dev(*w, B.MXFP4)
+    tail = to_dev(x[0][-300:], x[1][-300:], B.MXFP8)
+    for dtype, n in ((torch.bfloat16, N), (torch.bfloat16, N - 1), (torch.float32, N)):
+        wn = wd if n == N else to_dev(w[0][:n], w[1][:n], B.MXFP4)
+        y = B.qmoe_mx_matmul(*to_dev(*x, B.MXFP8), B.MXFP8, *wn, dtype)
+        assert torch.equal(y[-300:], B.qmoe_mx_matmul(*tail, B.MXFP8, *wn, dtype))
+        del y
