@@ -402,7 +402,8 @@ int qmoe_unpack_zero_points(const uint8_t* zp_packed, int rows, int nb, uint8_t*
  *           blocks >= K/32 are padding: the calls below write zeros there.
  *           qmoe_mx_scale_bytes(R, K) gives the size.
  * An element's value is code * X.  R and K are at most 2^30
- * (QMOE_ERR_UNSUPPORTED).  Every codes and scales pointer is 16-byte aligned; codes, scales, inputs and outputs of one call must not overlap
+ * (QMOE_ERR_UNSUPPORTED).  Every codes and scales pointer is 16-byte aligned;
+ * codes, scales, inputs and outputs of one call must not overlap
  * (qmoe_rmsnorm_mx's residual_out is the exception). */
 typedef enum { QMOE_MXFP8 = 0, QMOE_MXFP4 = 1 } qmoe_mx_format;
 
@@ -435,7 +436,9 @@ int qmoe_mx_dequant(const uint8_t* codes, const uint8_t* scales, int format, int
  * weight), residual_out may be NULL (not wanted) and may be x or residual
  * itself.  Requires H a multiple of 32; pointers 16-byte aligned.  A NaN makes
  * its whole row read as NaN; an infinity makes its own block NaN and the rest
- * of its row 0 (also where the sum of squares leaves fp32's range). */
+ * of its row 0 (also where the sum of squares leaves fp32's range).  With eps
+ * = 0, rows whose largest |h| is below 2^-60 lose accuracy, and read as NaN
+ * where their squares vanish in fp32. */
 int qmoe_rmsnorm_mx(const void* x, const void* residual, const void* weight, int act_dtype, int T, int H, float eps,
                     int format, void* residual_out, uint8_t* codes, uint8_t* scales, void* stream);
 

@@ -454,8 +454,8 @@ __global__ void __launch_bounds__(FILL ? kMmFillThreads : kMmThreads, 1)
     // Two groups of four warps take turns at the stages; a warp takes 32 rows,
     // four lanes the 64 bytes of a row.  (The codes come by TMA and not by
     // loads of these warps, whose fence between stores and MMAs waits for loads
-    // in flight too: 16 x 8192 x 8160 takes 11.7 us so and 16.9 with loads,
-    // 512 x 8192 x 8160 40 and 49; widened by TMA, K = 8192 takes 9.0 and 24.)
+    // in flight too: 16 x 8192 x 8160 takes 11.8 us so, and 512 x 8192 x 8160
+    // 41.6; with loads 16.9 and 49.  Widened by TMA, K = 8192 takes 9.3 and 24.)
     const int group = warp >= kMmThreads / 32 + 4;
     const int r0 = ((warp - kMmThreads / 32) & 3) * 32 + (lane >> 2), piece = lane & 3;
     constexpr int R = P::kRawSlots ? P::kRawSlots : 1;
@@ -672,6 +672,7 @@ static cudaError_t mm_capacity(int split, int* ctas) {
 //   2048 x 11264 x 2048   2x192/1 33  2x256/1 34  192/1 37  128/1 39  64/1 59
 //   4096 x 8192 x 2048 (x in MXFP4)  2x256/1 30  2x192/1 35
 //   4085 x 3895 x 512 (x in MXFP4)  128/1 13.1  192/1 13.4  64/1 13.9  2x256/1 15.4  2x192/1 16.9
+//   8192 x 8192 x 8192 (x in MXFP4)  2x256/1 156 to 166  2x192/1 155 to 169 (the power limit's doing)
 // (192 tokens: two whole accumulators fit tensor memory; at 256 the next tile's
 // first MMA waits until the epilogue has taken the shared columns.)
 struct MmChoice {
