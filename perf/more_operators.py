@@ -237,7 +237,7 @@ def run(state):
         from int4_block_quantized_gb300 import binding as B
         if c["op"] == "rows":
             if c["k"]:
-                codes, scales = B.qmoe_fp8_quantize(st["x"], st["perm"], c["k"], codes=st["codes"], scales=st["scales"])
+                codes, scales = B.qmoe_fp8_quantize(st["x"], st["pos"], codes=st["codes"], scales=st["scales"])
             else:
                 codes, scales = B.qmoe_fp8_quantize(st["x"])
             return {"scales": scales, "values": B.qmoe_fp8_dequant(codes, scales, torch.bfloat16)}
@@ -252,7 +252,7 @@ def run(state):
                                            offsets=st.get("offsets"), out=st.get("out"))}
         if c["op"] == "dispatch":
             offsets, perm, pos = B.qmoe_sort_experts(st["ids"], c["E"])
-            return {"offsets": offsets, "perm": perm, "pos": pos, "xs": B.qmoe_dispatch(st["x"], perm, c["k"], out=st["xs"])}
+            return {"offsets": offsets, "perm": perm, "pos": pos, "xs": B.qmoe_dispatch(st["x"], pos, out=st["xs"])}
         if not c["back"]:
             return {"out": B.qmoe_combine(st["ys"], st["pos"], st["weights"], st["residual"])}
         dys, dw = B.qmoe_combine_backward(st["dout"], st["ys"], st["pos"], st["weights"], dys=st["dys"])
