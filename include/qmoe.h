@@ -71,7 +71,7 @@ typedef enum {
   QMOE_ST_RANGE = 4    /* a value outside a format's or accumulator's range       -> QMOE_ERR_DEVICE_CHECK */
 } qmoe_status_bit;
 
-/* QMOE_F32 is taken by the microscaled entry points that say so, no others. */
+/* QMOE_F32 is taken by the microscaled and FP8 entry points that say so, no others. */
 typedef enum { QMOE_F16 = 0, QMOE_BF16 = 1, QMOE_F32 = 2 } qmoe_dtype;
 
 /* Path selection for qmoe_forward_ex.
@@ -498,6 +498,123 @@ int qmoe_mx_matmul_diagnosed(const uint8_t* x_codes, const uint8_t* x_scales, in
  * side. */
 int qmoe_mx_tile_scales(const uint8_t* scales_rowmajor, int R, int K, uint8_t* scales, void* stream);
 int qmoe_mx_untile_scales(const uint8_t* scales, int R, int K, uint8_t* scales_rowmajor, void* stream);
+
+/* ---- FP8 tensors with a scale for each block of 128 (e4m3), and experts in
+ * that format: quantisation, products (dense or grouped by expert), tokens put
+ * in the order of their experts and brought back.  A layer of them:
+ *   qmoe_route                    topk_w, topk_ids
+ *   qmoe_sort_experts             offsets, pos
+ *   qmoe_fp8_quantize (pos)       the tokens in 8 bits, in the experts' order
+ *   qmoe_fp8_matmul (offsets)     gate and up: weights [E, 2 I, H]
+ *   qmoe_fp8_quantize_swiglu      silu(gate) * up in 8 bits
+ *   qmoe_fp8_matmul (offsets)     down: weights [E, H, I]
+ *   qmoe_combine (pos, topk_w)    the weighted sum, onto a residual
+ *
+ * An FP8 tensor is two device buffers:
+ *   codes   uint8, one e4m3 code per element (largest 448; 127 and 255: NaN);
+ *           activations [M, K], weights [E, N, K], K a multiple of 16; 16-byte
+ *           aligned;
+ *   scales  fp32, row-major; activations [M, ceil(K/128)]: one per row and 128
+ *           columns; weights [E, ceil(N/128), ceil(K/128)]: one per 128 rows of
+ *           an expert and 128 columns.  The last block of a row or column may be
+ *           shorter.  4-byte aligned.
+ * An element's value is code * scale.  Quantisation, with a the largest
+ * magnitude of the block, at least 2^-100:
+ *   scale = fp32(a / 448),  code = v * fp32(448 / a) rounded to nearest even
+ * (the product rounded once, as if it were exact before).  A block with a NaN
+ * or an infinity gets a NaN scale and zero codes.
+ * K is at most 2^30 and so are M and E * N (QMOE_ERR_UNSUPPORTED).  Inputs and
+ * outputs of one call must not overlap (qmoe_combine's out is the exception).
+ *
+ * pos int32 [T, k] gives the place of each assignment t * k + j among the rows
+ * of the experts' order, T * k of them: row pos[t, j] belongs to token t.  An
+ * entry outside 0 .. T * k - 1 goes nowhere; no row may be named twice.  Rows
+ * that no entry names are left as they were. */
+
+/* Tokens to FP8.  x [T, K] (fp16, bf16 or fp32; 16-byte aligned).  pos NULL (k
+ * then 0): codes and scales of T rows.  Else pos [T, k] and T * k rows: token
+ * t is quantised once and written to each row pos[t, j].  Bound by HBM. */
+int qmoe_fp8_quantize(const void* x, int x_dtype, int T, int K, const int32_t* pos, int k, uint8_t* codes, float* scales,
+                      void* stream);
+
+/* silu(gate) * up = gate / (1 + exp(-gate)) * up of h [M, 2 I] (gate in the
+ * first I columns; fp16, bf16 or fp32; 16-byte aligned), computed in fp32 and
+ * quantised to codes [M, I] without a rounding in between.  I a multiple of 16.
+ * Bound by HBM. */
+int qmoe_fp8_quantize_swiglu(const void* h, int h_dtype, int M, int I, uint8_t* codes, float* scales, void* stream);
+
+/* Weights w [E, N, K] (fp16, bf16 or fp32; 16-byte aligned) to FP8, a scale for
+ * each 128 x 128 elements of an expert.  (The transposed weights' codes and
+ * scales are the transposed ones, so the gradient of a product with respect to
+ * x is a product with them.)  Bound by HBM. */
+int qmoe_fp8_quantize_weights(const void* w, int w_dtype, int E, int N, int K, uint8_t* codes, float* scales, void* stream);
+
+/* Values of an FP8 tensor: out (fp16, bf16 or fp32; 16-byte aligned) = code *
+ * scale in fp32, rounded once to out_dtype.  block_rows 1: activations [E * N,
+ * K]; 128: weights [E, N, K]. */
+int qmoe_fp8_dequant(const uint8_t* codes, const float* scales, int E, int N, int K, int block_rows, void* out,
+                     int out_dtype, void* stream);
+
+/* Product of FP8 tensors: y[m, n] = sum_k x[m, k] W[n, k], the codes' products
+ * summed in fp32 over each block of 128 k, these sums times their scales summed
+ * in fp32, y rounded once to y_dtype (fp16, bf16 or fp32; aligned to its
+ * element size).
+ *   offsets NULL  dense: E is 1, y [M, N] = x [M, K] . W [N, K]^T.
+ *   offsets       int32 [E + 1] on the device, as qmoe_sort_experts and
+ *                 qmoe_route give them: rows offsets[e] .. offsets[e + 1] - 1 of
+ *                 x and y belong to expert e, whose weights are W[e]; rows
+ *                 outside every expert's are not read, and y's are left as they
+ *                 were.  The offsets have to increase within 0 .. M: what lies
+ *                 outside is cut off there, and QMOE_ST_INDEX is set.  At most
+ *                 QMOE_MAX_EXPERTS experts.
+ * A NaN scale or code makes the outputs that it enters NaN, and no others.
+ * status_dev (a 4-byte device word that the caller set to 0, or NULL): collects
+ * QMOE_ST_INDEX, and QMOE_ST_TIMEOUT where a bounded wait ran out (y is then
+ * undefined); read it with qmoe_get_device_status(status_dev, ...).  NULL: the
+ * same in a word of the library's, one per device (qmoe_fp8_status). */
+int qmoe_fp8_matmul(const uint8_t* x_codes, const float* x_scales, const uint8_t* w_codes, const float* w_scales,
+                    const int32_t* offsets, int E, int M, int N, int K, void* y, int y_dtype, uint32_t* status_dev,
+                    void* stream);
+
+/* The status word, on the current device, of the FP8 products that were given
+ * none: as qmoe_mx_status. */
+int qmoe_fp8_status(uint32_t* bits_out, void* stream);
+
+/* Assignments by expert: ids int32 [T, k] (from any router; the same expert may
+ * come twice in a row), those outside 0 .. E - 1 (padding) go nowhere.
+ *   offsets  int32 [E + 1] out or NULL: assignments to experts < e
+ *   perm     int32 [T * k] out or NULL: assignments t * k + j by expert,
+ *            increasing within an expert; -1 behind the last
+ *   pos      int32 [T, k] out or NULL: the place of each in perm, or -1
+ * 1 <= E <= QMOE_MAX_EXPERTS, 1 <= T * k <= 2^30.  One kernel, no workspace. */
+int qmoe_sort_experts(const int32_t* ids, int T, int k, int E, int32_t* offsets, int32_t* perm, int32_t* pos,
+                      void* stream);
+
+/* Tokens in the experts' order: xs[pos[t, j]] = x[t].  x [T, H] and xs [T * k,
+ * H] of dtype (fp16, bf16 or fp32), 16-byte aligned, H a multiple of 8.  Bound
+ * by HBM. */
+int qmoe_dispatch(const void* x, int dtype, int T, int H, int k, const int32_t* pos, void* xs, void* stream);
+
+/* Its gradient: dx[t] = sum_j dxs[pos[t, j]], summed in fp32 in the order of j
+ * and rounded once; qmoe_combine without weights and residual. */
+int qmoe_dispatch_backward(const void* dxs, int dtype, const int32_t* pos, int T, int H, int k, void* dx, void* stream);
+
+/* The experts' outputs back to their tokens:
+ *   out[t] = residual[t] + sum_j w[t, j] ys[pos[t, j]]
+ * in fp32, in this order, rounded once.  ys [T * k, H] of ys_dtype, residual
+ * (NULL: none) and out [T, H] of out_dtype (each fp16, bf16 or fp32), w fp32 [T,
+ * k] (NULL: ones).  out may be residual.  H a multiple of 8, tensors 16-byte
+ * aligned.  Rows that go nowhere are not read.  Bound by HBM. */
+int qmoe_combine(const void* ys, int ys_dtype, const int32_t* pos, const float* w, const void* residual, int T, int H, int k,
+                 void* out, int out_dtype, void* stream);
+
+/* Its gradients, from dout [T, H] of dout_dtype:
+ *   dys[pos[t, j]] = w[t, j] dout[t]                 [T * k, H], ys_dtype; NULL: not wanted
+ *   dw[t, j] = sum_h dout[t, h] ys[pos[t, j], h]     fp32 [T, k]; 0 where j goes nowhere; NULL: not wanted
+ * (the residual's gradient is dout).  ys may be NULL where dw is.  Sums are
+ * fp32, in a fixed order.  H a multiple of 8.  Bound by HBM. */
+int qmoe_combine_backward(const void* dout, int dout_dtype, const void* ys, int ys_dtype, const int32_t* pos,
+                          const float* w, int T, int H, int k, void* dys, float* dw, void* stream);
 
 /* Read (blocking: synchronises `stream`) and clear the device status word
  * of `workspace` (its first 4 bytes; also any 4-byte status word such as

@@ -113,6 +113,28 @@ def lib():
         for f in (L.qmoe_mx_tile_scales, L.qmoe_mx_untile_scales):
             f.restype = i32
             f.argtypes = [vp, i32, i32, vp, vp]
+        L.qmoe_fp8_quantize.restype = i32
+        L.qmoe_fp8_quantize.argtypes = [vp, i32, i32, i32, vp, i32, vp, vp, vp]
+        L.qmoe_fp8_quantize_swiglu.restype = i32
+        L.qmoe_fp8_quantize_swiglu.argtypes = [vp, i32, i32, i32, vp, vp, vp]
+        L.qmoe_fp8_quantize_weights.restype = i32
+        L.qmoe_fp8_quantize_weights.argtypes = [vp, i32, i32, i32, i32, vp, vp, vp]
+        L.qmoe_fp8_dequant.restype = i32
+        L.qmoe_fp8_dequant.argtypes = [vp, vp, i32, i32, i32, i32, vp, i32, vp]
+        L.qmoe_fp8_matmul.restype = i32
+        L.qmoe_fp8_matmul.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, i32, vp, vp]
+        L.qmoe_fp8_status.restype = i32
+        L.qmoe_fp8_status.argtypes = [ctypes.POINTER(ctypes.c_uint32), vp]
+        L.qmoe_sort_experts.restype = i32
+        L.qmoe_sort_experts.argtypes = [vp, i32, i32, i32, vp, vp, vp, vp]
+        L.qmoe_dispatch.restype = i32
+        L.qmoe_dispatch.argtypes = [vp, i32, i32, i32, i32, vp, vp, vp]
+        L.qmoe_dispatch_backward.restype = i32
+        L.qmoe_dispatch_backward.argtypes = [vp, i32, vp, i32, i32, i32, vp, vp]
+        L.qmoe_combine.restype = i32
+        L.qmoe_combine.argtypes = [vp, i32, vp, vp, vp, i32, i32, i32, vp, i32, vp]
+        L.qmoe_combine_backward.restype = i32
+        L.qmoe_combine_backward.argtypes = [vp, i32, vp, i32, vp, vp, i32, i32, i32, vp, vp, vp]
         L.qmoe_get_device_status.restype = i32
         L.qmoe_get_device_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32), vp]
         _lib = L
@@ -589,3 +611,288 @@ def qmoe_mx_untile_scales(scales, R, K):
     out = torch.empty((R, K // 32), dtype=_U8, device=scales.device)
     _mx_call(dev, lib().qmoe_mx_untile_scales, where, scales.data_ptr(), R, K, out.data_ptr())
     return out
+
+
+# ---- FP8 tensors with a scale for each block of 128, and experts in that format.
+# An FP8 tensor is (codes, scales): codes uint8 [M, K] (or [E, N, K], weights),
+# scales fp32 [M, ceil(K/128)] ([E, ceil(N/128), ceil(K/128)]); qmoe.h has the
+# formulas.  pos int32 [T, k] is each assignment's place in the experts' order
+# (qmoe_sort_experts); rows that it does not name are left as they were, so a
+# call that makes its own output leaves them undefined.  Checked and run like the
+# microscaled calls above.
+
+_F32 = torch.float32
+_I32 = torch.int32
+_ROWS_MAX = 1 << 30
+
+
+def _fp8_in(x, dev, where, name):
+    """qmoe_dtype of a contiguous fp16, bf16 or fp32 tensor on device dev."""
+    dt = _MX_DT.get(x.dtype)
+    if dt is None or dev < 0 or x.get_device() != dev or not x.is_contiguous():
+        _bad(where, "%s: wants a contiguous fp16, bf16 or fp32 tensor on one CUDA device, got %s on %s%s" % (
+            name, x.dtype, x.device, "" if x.is_contiguous() else ", not contiguous"))
+    return dt
+
+
+def _fp8_size(rows, K, where):
+    if rows > _ROWS_MAX or K > _ROWS_MAX:
+        raise QMoEError(2, "%s: %d rows of %d, at most 2^30 of each" % (where, rows, K))
+    if rows < 1 or K < 16 or K % 16:
+        _bad(where, "%d rows of %d: rows and a multiple of 16 columns are wanted" % (rows, K))
+
+
+def _fp8_out(codes, scales, shape, sshape, x, dev, where):
+    """(codes, scales) to write to: the caller's, or new ones."""
+    if codes is None:
+        codes = torch.empty(shape, dtype=_U8, device=x.device)
+    else:
+        _mx_check2(codes, dev, _U8, shape, where, "codes")
+    if scales is None:
+        scales = torch.empty(sshape, dtype=_F32, device=x.device)
+    else:
+        _mx_check2(scales, dev, _F32, sshape, where, "scales")
+    return codes, scales
+
+
+def _places(pos, T, dev, where):
+    """k of pos [T, k], checked."""
+    shape = pos.shape
+    if len(shape) != 2 or shape[0] != T or shape[1] < 1:
+        _bad(where, "pos: wants [%d, k], got %s" % (T, tuple(shape)))
+    k = shape[1]
+    if T * k > _ROWS_MAX:
+        raise QMoEError(2, "%s: %d x %d assignments, at most 2^30" % (where, T, k))
+    _mx_check2(pos, dev, _I32, shape, where, "pos")
+    return k
+
+
+def qmoe_fp8_quantize(x, pos=None, codes=None, scales=None):
+    """(codes, scales) of x [T, K] (fp16, bf16 or fp32).  With pos [T, k] they have
+    T * k rows, and token t is written to each row pos[t, j]."""
+    where = "qmoe_fp8_quantize"
+    T, K = _mx_size(x, where)
+    dev = x.get_device()
+    dt = _fp8_in(x, dev, where, "x")
+    rows, k, pp = T, 0, None
+    if pos is not None:
+        k = _places(pos, T, dev, where)
+        rows, pp = T * k, pos.data_ptr()
+    _fp8_size(rows, K, where)
+    codes, scales = _fp8_out(codes, scales, (rows, K), (rows, (K + 127) // 128), x, dev, where)
+    _mx_call(dev, lib().qmoe_fp8_quantize, where, x.data_ptr(), dt, T, K, pp, k, codes.data_ptr(), scales.data_ptr())
+    return codes, scales
+
+
+def qmoe_fp8_quantize_swiglu(h, codes=None, scales=None):
+    """(codes, scales) of silu(gate) * up [M, I] for h = [gate | up] [M, 2 I]."""
+    where = "qmoe_fp8_quantize_swiglu"
+    M, I = _mx_size(h, where)
+    dev = h.get_device()
+    dt = _fp8_in(h, dev, where, "h")
+    if I % 2:
+        _bad(where, "h: wants gate and up side by side, got %d columns" % I)
+    I //= 2
+    _fp8_size(M, I, where)
+    codes, scales = _fp8_out(codes, scales, (M, I), (M, (I + 127) // 128), h, dev, where)
+    _mx_call(dev, lib().qmoe_fp8_quantize_swiglu, where, h.data_ptr(), dt, M, I, codes.data_ptr(), scales.data_ptr())
+    return codes, scales
+
+
+def qmoe_fp8_quantize_weights(w, codes=None, scales=None):
+    """(codes, scales) of weights [E, N, K] or [N, K], a scale per 128 x 128."""
+    where = "qmoe_fp8_quantize_weights"
+    shape = tuple(w.shape)
+    if len(shape) not in (2, 3):
+        _bad(where, "w: wants [E, N, K] or [N, K], got %s" % (shape,))
+    E, N, K = (1,) * (3 - len(shape)) + shape
+    dev = w.get_device()
+    dt = _fp8_in(w, dev, where, "w")
+    _fp8_size(E * N, K, where)
+    codes, scales = _fp8_out(codes, scales, shape, shape[:-2] + ((N + 127) // 128, (K + 127) // 128), w, dev, where)
+    _mx_call(dev, lib().qmoe_fp8_quantize_weights, where, w.data_ptr(), dt, E, N, K, codes.data_ptr(), scales.data_ptr())
+    return codes, scales
+
+
+def qmoe_fp8_dequant(codes, scales, dtype=torch.bfloat16, out=None):
+    """Values (fp16, bf16 or fp32) of an FP8 tensor; whether a scale covers one row
+    or 128 is read from the scales' shape."""
+    where = "qmoe_fp8_dequant"
+    shape = tuple(codes.shape)
+    if len(shape) not in (2, 3) or len(scales.shape) != len(shape):
+        _bad(where, "codes %s with scales %s" % (shape, tuple(scales.shape)))
+    E, N, K = (1,) * (3 - len(shape)) + shape
+    dev, dt = codes.get_device(), _MX_DT.get(dtype)
+    if dt is None:
+        _bad(where, "unsupported output type %s" % dtype)
+    _fp8_size(E * N, K, where)
+    _mx_check2(codes, dev, _U8, shape, where, "codes")
+    rows = 1 if scales.shape[-2] == N else 128
+    _mx_check2(scales, dev, _F32, shape[:-2] + ((N + rows - 1) // rows, (K + 127) // 128), where, "scales")
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=codes.device)
+    else:
+        _mx_check2(out, dev, dtype, shape, where, "out")
+    _mx_call(dev, lib().qmoe_fp8_dequant, where, codes.data_ptr(), scales.data_ptr(), E, N, K, rows, out.data_ptr(), dt)
+    return out
+
+
+def qmoe_fp8_matmul(x_codes, x_scales, w_codes, w_scales, dtype=torch.bfloat16, offsets=None, out=None, status=None):
+    """y [M, N] (fp16, bf16 or fp32) = x . W^T for FP8 tensors x [M, K] and W [N, K];
+    with offsets int32 [E + 1] and W [E, N, K], rows offsets[e] .. offsets[e + 1] - 1
+    meet W[e], and the rows of y outside every expert's are left as they were.
+    status: an int32 [1] device tensor that collects QMOE_ST_* bits (zero it
+    first); without one qmoe_fp8_status() tells."""
+    where = "qmoe_fp8_matmul"
+    M, K = _mx_size(x_codes, where)
+    dev, dt = x_codes.get_device(), _MX_DT.get(dtype)
+    shape = w_codes.shape
+    E = 1 if offsets is None else offsets.numel() - 1
+    N = shape[-2] if len(shape) in (2, 3) else 0
+    if dt is None or N < 1 or E < 1 or (E,) + tuple(shape[-2:]) != (E, N, K) or tuple(shape[:-2]) not in ((E,), () if E == 1 else (E,)):
+        _bad(where, "x %s, W %s, %s experts, result in %s" % (tuple(x_codes.shape), tuple(shape), E, dtype))
+    if E > 256:
+        raise QMoEError(2, "%s: %d experts, at most 256" % (where, E))
+    _fp8_size(M, K, where)
+    _fp8_size(E * N, K, where)
+    nb = (K + 127) // 128
+    _mx_check2(x_codes, dev, _U8, (M, K), where, "x_codes")
+    _mx_check2(x_scales, dev, _F32, (M, nb), where, "x_scales")
+    _mx_check2(w_codes, dev, _U8, shape, where, "w_codes")
+    _mx_check2(w_scales, dev, _F32, tuple(shape[:-2]) + ((N + 127) // 128, nb), where, "w_scales")
+    op = st = None
+    if offsets is not None:
+        _mx_check2(offsets, dev, _I32, (E + 1,), where, "offsets")
+        op = offsets.data_ptr()
+    if out is None:
+        out = torch.empty((M, N), dtype=dtype, device=x_codes.device)
+    else:
+        _mx_check2(out, dev, dtype, (M, N), where, "out")
+    if status is not None:
+        _mx_check(status, dev, _I32, 1, where, "status")
+        st = status.data_ptr()
+    _mx_call(dev, lib().qmoe_fp8_matmul, where, x_codes.data_ptr(), x_scales.data_ptr(), w_codes.data_ptr(),
+             w_scales.data_ptr(), op, E, M, N, K, out.data_ptr(), dt, st)
+    return out
+
+
+def qmoe_fp8_status():
+    """(code, bits) of the FP8 products on the current device that were given no
+    status tensor, and cleared.  Waits for the current stream."""
+    bits = ctypes.c_uint32(0)
+    rc = lib().qmoe_fp8_status(ctypes.byref(bits), _stream())
+    if rc not in (0, 5, 6):
+        _check(rc, "qmoe_fp8_status")
+    return rc, bits.value
+
+
+def qmoe_sort_experts(ids, E):
+    """(offsets [E + 1], perm [T * k], pos [T, k]), int32, of ids int32 [T, k]: the
+    assignments by expert, stably; an id outside 0 .. E - 1 goes nowhere (pos -1,
+    and perm -1 behind the last)."""
+    where = "qmoe_sort_experts"
+    T, k = _mx_size(ids, where)
+    dev = ids.get_device()
+    if E > 256 or T * k > _ROWS_MAX:
+        raise QMoEError(2, "%s: %d experts, %d assignments: at most 256 and 2^30" % (where, E, T * k))
+    if E < 1 or T < 1 or k < 1:
+        _bad(where, "ids %s, %d experts" % ((T, k), E))
+    _mx_check2(ids, dev, _I32, (T, k), where, "ids")
+    offsets = torch.empty(E + 1, dtype=_I32, device=ids.device)
+    perm = torch.empty(T * k, dtype=_I32, device=ids.device)
+    pos = torch.empty((T, k), dtype=_I32, device=ids.device)
+    _mx_call(dev, lib().qmoe_sort_experts, where, ids.data_ptr(), T, k, E, offsets.data_ptr(), perm.data_ptr(),
+             pos.data_ptr())
+    return offsets, perm, pos
+
+
+def _fp8_rows(T, H, where):
+    if T < 1 or H < 8 or H % 8:
+        _bad(where, "[%d, %d]: rows and a multiple of 8 columns are wanted" % (T, H))
+    if H > 1 << 28:
+        raise QMoEError(2, "%s: %d columns, at most 2^28" % (where, H))
+
+
+def qmoe_dispatch(x, pos, out=None):
+    """xs [T * k, H] with xs[pos[t, j]] = x[t]."""
+    where = "qmoe_dispatch"
+    T, H = _mx_size(x, where)
+    dev = x.get_device()
+    dt = _fp8_in(x, dev, where, "x")
+    _fp8_rows(T, H, where)
+    k = _places(pos, T, dev, where)
+    if out is None:
+        out = torch.empty((T * k, H), dtype=x.dtype, device=x.device)
+    else:
+        _mx_check2(out, dev, x.dtype, (T * k, H), where, "out")
+    _mx_call(dev, lib().qmoe_dispatch, where, x.data_ptr(), dt, T, H, k, pos.data_ptr(), out.data_ptr())
+    return out
+
+
+def _combine(where, ys, pos, w, residual, out):
+    rows, H = _mx_size(ys, where)
+    dev = ys.get_device()
+    dt = _fp8_in(ys, dev, where, "ys")
+    if len(pos.shape) != 2:
+        _bad(where, "pos: wants [T, k], got %s" % (tuple(pos.shape),))
+    T = pos.shape[0]
+    _fp8_rows(T, H, where)
+    k = _places(pos, T, dev, where)
+    if rows != T * k:
+        _bad(where, "ys: wants %d rows, got %d" % (T * k, rows))
+    wp = rp = None
+    if w is not None:
+        _mx_check2(w, dev, _F32, (T, k), where, "w")
+        wp = w.data_ptr()
+    if residual is not None:
+        ot = _fp8_in(residual, dev, where, "residual")
+        _mx_check2(residual, dev, residual.dtype, (T, H), where, "residual")
+        rp = residual.data_ptr()
+    else:
+        ot = dt if out is None else _fp8_in(out, dev, where, "out")
+    if out is None:
+        out = torch.empty((T, H), dtype=ys.dtype if residual is None else residual.dtype, device=ys.device)
+    else:
+        _mx_check2(out, dev, out.dtype if residual is None else residual.dtype, (T, H), where, "out")
+    _mx_call(dev, lib().qmoe_combine, where, ys.data_ptr(), dt, pos.data_ptr(), wp, rp, T, H, k, out.data_ptr(), ot)
+    return out
+
+
+def qmoe_combine(ys, pos, w=None, residual=None, out=None):
+    """out [T, H] = residual + sum_j w[t, j] ys[pos[t, j]]: of the residual's type
+    (without one, of out's or of ys').  w fp32 [T, k]; None: ones.  out may be
+    residual."""
+    return _combine("qmoe_combine", ys, pos, w, residual, out)
+
+
+def qmoe_dispatch_backward(dxs, pos, out=None):
+    """dx [T, H] = sum_j dxs[pos[t, j]], the gradient of qmoe_dispatch."""
+    if out is not None and out.dtype is not dxs.dtype:
+        _bad("qmoe_dispatch_backward", "out: wants %s, got %s" % (dxs.dtype, out.dtype))
+    return _combine("qmoe_dispatch_backward", dxs, pos, None, None, out)
+
+
+def qmoe_combine_backward(dout, ys, pos, w=None, dys=None, dw=None):
+    """(dys [T * k, H], dw [T, k] fp32) of qmoe_combine for dout [T, H]."""
+    where = "qmoe_combine_backward"
+    T, H = _mx_size(dout, where)
+    dev = dout.get_device()
+    dt, yt = _fp8_in(dout, dev, where, "dout"), _fp8_in(ys, dev, where, "ys")
+    _fp8_rows(T, H, where)
+    k = _places(pos, T, dev, where)
+    _mx_check2(ys, dev, ys.dtype, (T * k, H), where, "ys")
+    wp = None
+    if w is not None:
+        _mx_check2(w, dev, _F32, (T, k), where, "w")
+        wp = w.data_ptr()
+    if dys is None:
+        dys = torch.empty_like(ys)
+    else:
+        _mx_check2(dys, dev, ys.dtype, (T * k, H), where, "dys")
+    if dw is None:
+        dw = torch.empty((T, k), dtype=_F32, device=dout.device)
+    else:
+        _mx_check2(dw, dev, _F32, (T, k), where, "dw")
+    _mx_call(dev, lib().qmoe_combine_backward, where, dout.data_ptr(), dt, ys.data_ptr(), yt, pos.data_ptr(), wp, T, H, k,
+             dys.data_ptr(), dw.data_ptr())
+    return dys, dw

@@ -55,6 +55,22 @@ int check_mx(const uint8_t* codes, const uint8_t* scales, int format, int R, int
   return check_mx_size(R, K);
 }
 
+// sizes of an FP8 tensor of E times R rows
+int check_fp8_size(int E, int R, int K) {
+  if (E < 1 || R < 1 || K < 16 || K % 16) return QMOE_ERR_INVALID_ARG;
+  return (long long)E * R > (1LL << 30) || K > (1 << 30) ? QMOE_ERR_UNSUPPORTED : QMOE_OK;
+}
+// its codes and scales
+int check_fp8(const uint8_t* codes, const float* scales, int E, int R, int K) {
+  if (!codes || !scales || !aligned(codes, 16) || !aligned(scales, 4)) return QMOE_ERR_INVALID_ARG;
+  return check_fp8_size(E, R, K);
+}
+// T tokens with k assignments each, their places, rows of H elements
+int check_places(const int32_t* pos, int T, int H, int k) {
+  if (!pos || !aligned(pos, 4) || T < 1 || k < 1 || H < 8 || H % 8) return QMOE_ERR_INVALID_ARG;
+  return (long long)T * k > (1LL << 30) || H > (1 << 28) ? QMOE_ERR_UNSUPPORTED : QMOE_OK;
+}
+
 thread_local cudaError_t g_last_cuda_error = cudaSuccess;
 
 int cuda_status(cudaError_t e) {
@@ -624,6 +640,106 @@ int qmoe_mx_untile_scales(const uint8_t* scales, int R, int K, uint8_t* scales_r
   int rc = check_mx_size(R, K);
   if (rc || (rc = check_device())) return rc;
   return cuda_status(launch_mx_retile(scales, scales_rowmajor, R, K, false, (cudaStream_t)stream));
+}
+
+// --------------------------------------------------------------- FP8 experts
+
+int qmoe_fp8_quantize(const void* x, int x_dtype, int T, int K, const int32_t* pos, int k, uint8_t* codes, float* scales,
+                      void* stream) {
+  if (!valid_dtype_or_f32(x_dtype) || !x || !aligned(x, 16) || !aligned(pos, 4)) return QMOE_ERR_INVALID_ARG;
+  if (pos ? k < 1 : k != 0) return QMOE_ERR_INVALID_ARG;
+  int rc = check_fp8(codes, scales, 1, T, K);
+  if (rc) return rc;
+  if (pos && (long long)T * k > (1LL << 30)) return QMOE_ERR_UNSUPPORTED;
+  if ((rc = check_device())) return rc;
+  return cuda_status(launch_fp8_quantize(x, x_dtype, T, K, pos, k, codes, scales, (cudaStream_t)stream));
+}
+
+int qmoe_fp8_quantize_swiglu(const void* h, int h_dtype, int M, int I, uint8_t* codes, float* scales, void* stream) {
+  if (!valid_dtype_or_f32(h_dtype) || !h || !aligned(h, 16)) return QMOE_ERR_INVALID_ARG;
+  int rc = check_fp8(codes, scales, 1, M, I);
+  if (rc || (rc = check_device())) return rc;
+  return cuda_status(launch_fp8_swiglu(h, h_dtype, M, I, codes, scales, (cudaStream_t)stream));
+}
+
+int qmoe_fp8_quantize_weights(const void* w, int w_dtype, int E, int N, int K, uint8_t* codes, float* scales, void* stream) {
+  if (!valid_dtype_or_f32(w_dtype) || !w || !aligned(w, 16)) return QMOE_ERR_INVALID_ARG;
+  int rc = check_fp8(codes, scales, E, N, K);
+  if (rc || (rc = check_device())) return rc;
+  return cuda_status(launch_fp8_weights(w, w_dtype, E, N, K, codes, scales, (cudaStream_t)stream));
+}
+
+int qmoe_fp8_dequant(const uint8_t* codes, const float* scales, int E, int N, int K, int block_rows, void* out,
+                     int out_dtype, void* stream) {
+  if (!valid_dtype_or_f32(out_dtype) || !out || !aligned(out, 16) || (block_rows != 1 && block_rows != 128))
+    return QMOE_ERR_INVALID_ARG;
+  int rc = check_fp8(codes, scales, E, N, K);
+  if (rc || (rc = check_device())) return rc;
+  return cuda_status(launch_fp8_dequant(codes, scales, E, N, K, block_rows, out, out_dtype, (cudaStream_t)stream));
+}
+
+int qmoe_fp8_matmul(const uint8_t* x_codes, const float* x_scales, const uint8_t* w_codes, const float* w_scales,
+                    const int32_t* offsets, int E, int M, int N, int K, void* y, int y_dtype, uint32_t* status_dev,
+                    void* stream) {
+  if (!valid_dtype_or_f32(y_dtype) || !y || !aligned(y, y_dtype == QMOE_F32 ? 4 : 2) || !aligned(status_dev, 4) ||
+      !aligned(offsets, 4) || (!offsets && E != 1))
+    return QMOE_ERR_INVALID_ARG;
+  int rc = check_fp8(x_codes, x_scales, 1, M, K);
+  if (rc || (rc = check_fp8(w_codes, w_scales, E, N, K))) return rc;
+  if (E > QMOE_MAX_EXPERTS) return QMOE_ERR_UNSUPPORTED;
+  if ((rc = check_device())) return rc;
+  return cuda_status(launch_fp8_matmul(x_codes, x_scales, w_codes, w_scales, offsets, E, M, N, K, y, y_dtype, status_dev,
+                                       (cudaStream_t)stream));
+}
+
+int qmoe_fp8_status(uint32_t* bits_out, void* stream) {
+  int rc = check_device();
+  if (rc) return rc;
+  void* word = nullptr;
+  if ((rc = cuda_status(fp8_status_word(&word)))) return rc;
+  return qmoe_get_device_status(word, bits_out, stream);
+}
+
+int qmoe_sort_experts(const int32_t* ids, int T, int k, int E, int32_t* offsets, int32_t* perm, int32_t* pos,
+                      void* stream) {
+  if (!ids || !aligned(ids, 4) || !aligned(offsets, 4) || !aligned(perm, 4) || !aligned(pos, 4) || T < 1 || k < 1 || E < 1)
+    return QMOE_ERR_INVALID_ARG;
+  if (E > QMOE_MAX_EXPERTS || (long long)T * k > (1LL << 30)) return QMOE_ERR_UNSUPPORTED;
+  const int rc = check_device();
+  if (rc) return rc;
+  return cuda_status(launch_sort_experts(ids, T * k, E, offsets, perm, pos, (cudaStream_t)stream));
+}
+
+int qmoe_dispatch(const void* x, int dtype, int T, int H, int k, const int32_t* pos, void* xs, void* stream) {
+  if (!valid_dtype_or_f32(dtype) || !x || !xs || !aligned(x, 16) || !aligned(xs, 16)) return QMOE_ERR_INVALID_ARG;
+  int rc = check_places(pos, T, H, k);
+  if (rc || (rc = check_device())) return rc;
+  return cuda_status(launch_dispatch(x, H * (dtype == QMOE_F32 ? 4 : 2), T, k, pos, xs, (cudaStream_t)stream));
+}
+
+int qmoe_dispatch_backward(const void* dxs, int dtype, const int32_t* pos, int T, int H, int k, void* dx, void* stream) {
+  return qmoe_combine(dxs, dtype, pos, nullptr, nullptr, T, H, k, dx, dtype, stream);
+}
+
+int qmoe_combine(const void* ys, int ys_dtype, const int32_t* pos, const float* w, const void* residual, int T, int H, int k,
+                 void* out, int out_dtype, void* stream) {
+  if (!valid_dtype_or_f32(ys_dtype) || !valid_dtype_or_f32(out_dtype) || !ys || !out || !aligned(ys, 16) ||
+      !aligned(w, 4) || !aligned(residual, 16) || !aligned(out, 16))
+    return QMOE_ERR_INVALID_ARG;
+  int rc = check_places(pos, T, H, k);
+  if (rc || (rc = check_device())) return rc;
+  return cuda_status(launch_combine(ys, ys_dtype, pos, w, residual, T, H, k, out, out_dtype, (cudaStream_t)stream));
+}
+
+int qmoe_combine_backward(const void* dout, int dout_dtype, const void* ys, int ys_dtype, const int32_t* pos,
+                          const float* w, int T, int H, int k, void* dys, float* dw, void* stream) {
+  if (!valid_dtype_or_f32(dout_dtype) || !valid_dtype_or_f32(ys_dtype) || !dout || (!dys && !dw) || (dw && !ys) ||
+      !aligned(dout, 16) || !aligned(ys, 16) || !aligned(w, 4) || !aligned(dys, 16) || !aligned(dw, 4))
+    return QMOE_ERR_INVALID_ARG;
+  int rc = check_places(pos, T, H, k);
+  if (rc || (rc = check_device())) return rc;
+  return cuda_status(launch_combine_backward(dout, dout_dtype, ys, ys_dtype, pos, w, T, H, k, dys, dw,
+                                             (cudaStream_t)stream));
 }
 
 int qmoe_get_device_status(void* workspace, uint32_t* bits_out, void* stream) {

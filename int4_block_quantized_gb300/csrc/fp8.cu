@@ -1,0 +1,204 @@
+// fp8.cu -- FP8 tensors with a scale for each block of 128: quantisation of
+// activations (a row's 128 columns share a scale; in token order, or written to
+// the places that the experts' order gives; of SwiGLU's output) and of weights
+// (128 x 128 elements share one), and the reader.
+//
+//   a = max(2^-100, largest magnitude of the block)
+//   scale = RN(a / 448), code = RN_e4m3(v * RN(448 / a)), value = code * scale
+//
+// The product v * RN(448 / a) is rounded once, to the code: it is first cut to
+// fp32 towards zero with its last bit set where something was cut off ("round to
+// odd"), which no border between codes can be mistaken for.  Rounding it to fp32
+// in between would move the elements whose fp32 product happens to be such a
+// border: one in a million.
+#include "fp8.cuh"
+#include "launch.h"
+
+namespace qmoe {
+
+static dim3 fp8_grid(size_t work) {
+  const size_t cap = (size_t)device_sm_count() * 32;
+  const size_t b = (work + 255) / 256;
+  return dim3((unsigned)(b < 1 ? 1 : b > cap ? cap : b));
+}
+
+// -------------------------------------------------------------- activations
+// Eight lanes take a block, 16 elements each (a row's last block may have
+// fewer: its other lanes bring zeros).  With places, a token is quantised once
+// and written to each of its k rows.  Bound by HBM.
+template <typename T, bool PLACES>
+__global__ void __launch_bounds__(256) fp8_rows_kernel(const void* __restrict__ x, int M, int K,
+                                                       const int32_t* __restrict__ pos, int k,
+                                                       uint8_t* __restrict__ codes, float* __restrict__ scales) {
+  pdl_wait();
+  const uint32_t nb = (uint32_t)(K + 127) / 128, rows = PLACES ? (uint32_t)M * k : (uint32_t)M;
+  for (RowWalk w(blockIdx.x * 256 + threadIdx.x, gridDim.x * 256, nb * 8); w.r < (uint32_t)M; w.next()) {
+    const bool in = 16 * w.u < (uint32_t)K;
+    float v[16] = {};
+    if (in) load16<T>(x, (size_t)w.r * K + 16 * w.u, v);
+    const Fp8Block b(fp8_group_max(fp8_max16(v)));
+    const uint4 c = b.codes16(v);
+    if (!PLACES) {
+      if (in) *reinterpret_cast<uint4*>(codes + (size_t)w.r * K + 16 * w.u) = c;
+      if (!(w.u & 7)) scales[(size_t)w.r * nb + w.u / 8] = b.scale;
+    } else {
+      for (int j = 0; j < k; ++j) {
+        const uint32_t p = (uint32_t)pos[(size_t)w.r * k + j];
+        if (p >= rows) continue;  // this assignment goes nowhere
+        if (in) *reinterpret_cast<uint4*>(codes + (size_t)p * K + 16 * w.u) = c;
+        if (!(w.u & 7)) scales[(size_t)p * nb + w.u / 8] = b.scale;
+      }
+    }
+  }
+}
+
+// silu(g) * u of h [M, 2 I] (gate, then up), in fp32, quantised as above.
+template <typename T>
+__global__ void __launch_bounds__(256) fp8_swiglu_kernel(const void* __restrict__ h, int M, int I,
+                                                         uint8_t* __restrict__ codes, float* __restrict__ scales) {
+  pdl_wait();
+  const uint32_t nb = (uint32_t)(I + 127) / 128;
+  for (RowWalk w(blockIdx.x * 256 + threadIdx.x, gridDim.x * 256, nb * 8); w.r < (uint32_t)M; w.next()) {
+    const bool in = 16 * w.u < (uint32_t)I;
+    float v[16] = {};
+    if (in) {
+      float g[16];
+      load16<T>(h, (size_t)w.r * 2 * I + 16 * w.u, g);
+      load16<T>(h, (size_t)w.r * 2 * I + I + 16 * w.u, v);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] *= g[j] / (1.f + expf(-g[j]));
+    }
+    const Fp8Block b(fp8_group_max(fp8_max16(v)));
+    const uint4 c = b.codes16(v);
+    if (in) *reinterpret_cast<uint4*>(codes + (size_t)w.r * I + 16 * w.u) = c;
+    if (!(w.u & 7)) scales[(size_t)w.r * nb + w.u / 8] = b.scale;
+  }
+}
+
+// ------------------------------------------------------------------ weights
+// One CTA per 128 x 128 block: a thread takes 16 columns of four rows, which it
+// keeps as they came until the block's maximum is known.  Bound by HBM.
+template <typename T>
+__global__ void __launch_bounds__(256) fp8_weights_kernel(const void* __restrict__ w, int N, int K,
+                                                          uint8_t* __restrict__ codes, float* __restrict__ scales) {
+  pdl_wait();
+  constexpr int W = sizeof(T) / 2;  // 32-byte pieces of 16 elements
+  const uint32_t nb = (uint32_t)(K + 127) / 128, rb = (uint32_t)(N + 127) / 128;
+  const uint32_t b = blockIdx.x % nb, q = blockIdx.x / nb, r = q % rb, e = q / rb;
+  const uint32_t col = b * 128 + (threadIdx.x & 7) * 16, row = r * 128 + threadIdx.x / 8;
+  const size_t at = ((size_t)e * N + row) * K + col;
+  uint32_t raw[4][W][8] = {};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (col < (uint32_t)K && row + 32 * i < (uint32_t)N)
+#pragma unroll
+      for (int p = 0; p < W; ++p) load32(static_cast<const uint8_t*>(w) + (at + (size_t)32 * i * K) * sizeof(T) + 32 * p, raw[i][p]);
+  auto values = [&](int i, float(&v)[16]) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      if constexpr (sizeof(T) == 4) v[j] = __uint_as_float(raw[i][j / 8][j % 8]);
+      else v[j] = Half<T>::to_float((uint16_t)(raw[i][0][j / 2] >> (16 * (j & 1))));
+    }
+  };
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float v[16];
+    values(i, v);
+    m = max(m, fp8_max16(v));
+  }
+  m = __reduce_max_sync(0xffffffffu, m);
+  __shared__ uint32_t part[8];
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x / 32] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, part[i]);
+  const Fp8Block blk(m);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (col < (uint32_t)K && row + 32 * i < (uint32_t)N) {
+      float v[16];
+      values(i, v);
+      *reinterpret_cast<uint4*>(codes + at + (size_t)32 * i * K) = blk.codes16(v);
+    }
+  if (threadIdx.x == 0) scales[blockIdx.x] = blk.scale;
+}
+
+// ------------------------------------------------------------------- reader
+// code * scale in fp32, rounded once to T.  BR: rows that share a scale.
+template <typename T, int BR>
+__global__ void __launch_bounds__(256) fp8_dequant_kernel(const uint8_t* __restrict__ codes,
+                                                          const float* __restrict__ scales, int E, int N, int K,
+                                                          void* __restrict__ out) {
+  pdl_wait();
+  const uint32_t nb = (uint32_t)(K + 127) / 128, rb = (uint32_t)(N + BR - 1) / BR, rows = (uint32_t)E * N;
+  for (RowWalk w(blockIdx.x * 256 + threadIdx.x, gridDim.x * 256, (uint32_t)K / 16); w.r < rows; w.next()) {
+    const size_t i = (size_t)w.r * K + 16 * w.u;
+    uint32_t sr = w.r;
+    if constexpr (BR > 1) {
+      const uint32_t e = w.r / N;
+      sr = e * rb + (w.r - e * N) / BR;
+    }
+    const float s = scales[(size_t)sr * nb + w.u / 8];
+    const uint4 c = *reinterpret_cast<const uint4*>(codes + i);
+    float v[16];
+    mx_from_e4m3x4(c.x, v);
+    mx_from_e4m3x4(c.y, v + 4);
+    mx_from_e4m3x4(c.z, v + 8);
+    mx_from_e4m3x4(c.w, v + 12);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] *= s;
+    store16<T>(out, i, v);
+  }
+}
+
+template <typename T>
+static cudaError_t quantize_t(const void* x, int M, int K, const int32_t* pos, int k, uint8_t* codes, float* scales,
+                              cudaStream_t st) {
+  const dim3 g = fp8_grid((size_t)M * ((K + 127) / 128) * 8);
+  return launch_kernel(pos ? fp8_rows_kernel<T, true> : fp8_rows_kernel<T, false>, g, dim3(256), 0, st, true, x, M, K, pos,
+                       k, codes, scales);
+}
+template <typename T>
+static cudaError_t swiglu_t(const void* h, int M, int I, uint8_t* codes, float* scales, cudaStream_t st) {
+  return launch_kernel(fp8_swiglu_kernel<T>, fp8_grid((size_t)M * ((I + 127) / 128) * 8), dim3(256), 0, st, true, h, M, I,
+                       codes, scales);
+}
+template <typename T>
+static cudaError_t weights_t(const void* w, int E, int N, int K, uint8_t* codes, float* scales, cudaStream_t st) {
+  const long long blocks = (long long)E * ((N + 127) / 128) * ((K + 127) / 128);
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  return launch_kernel(fp8_weights_kernel<T>, dim3((unsigned)blocks), dim3(256), 0, st, true, w, N, K, codes, scales);
+}
+template <typename T>
+static cudaError_t dequant_t(const uint8_t* codes, const float* scales, int E, int N, int K, int block_rows, void* out,
+                             cudaStream_t st) {
+  const dim3 g = fp8_grid((size_t)E * N * (K / 16));
+  return launch_kernel(block_rows == 1 ? fp8_dequant_kernel<T, 1> : fp8_dequant_kernel<T, 128>, g, dim3(256), 0, st, true,
+                       codes, scales, E, N, K, out);
+}
+// fn(T{}) with the element type of a qmoe_dtype
+template <typename F>
+static cudaError_t by_type(int dtype, F fn) {
+  if (dtype == QMOE_F32) return fn(float{});
+  if (dtype == QMOE_BF16) return fn(__nv_bfloat16{});
+  return fn(__half{});
+}
+
+cudaError_t launch_fp8_quantize(const void* x, int x_dtype, int T, int K, const int32_t* pos, int k, uint8_t* codes,
+                                float* scales, cudaStream_t st) {
+  return by_type(x_dtype, [&](auto t) { return quantize_t<decltype(t)>(x, T, K, pos, k, codes, scales, st); });
+}
+cudaError_t launch_fp8_swiglu(const void* h, int h_dtype, int M, int I, uint8_t* codes, float* scales, cudaStream_t st) {
+  return by_type(h_dtype, [&](auto t) { return swiglu_t<decltype(t)>(h, M, I, codes, scales, st); });
+}
+cudaError_t launch_fp8_weights(const void* w, int w_dtype, int E, int N, int K, uint8_t* codes, float* scales,
+                               cudaStream_t st) {
+  return by_type(w_dtype, [&](auto t) { return weights_t<decltype(t)>(w, E, N, K, codes, scales, st); });
+}
+cudaError_t launch_fp8_dequant(const uint8_t* codes, const float* scales, int E, int N, int K, int block_rows, void* out,
+                               int out_dtype, cudaStream_t st) {
+  return by_type(out_dtype, [&](auto t) { return dequant_t<decltype(t)>(codes, scales, E, N, K, block_rows, out, st); });
+}
+
+}  // namespace qmoe

@@ -91,6 +91,26 @@ cudaError_t mx_matmul_variant(int x_format, const uint8_t* wc, int M, int N, int
                               int* spread);
 cudaError_t mx_status_word(void** word);  // the current device's, for calls without one
 
+// FP8 tensors (fp8.cu), their product (fp8_matmul.cu), tokens by expert (dispatch.cu)
+cudaError_t launch_fp8_quantize(const void* x, int x_dtype, int T, int K, const int32_t* pos, int k, uint8_t* codes,
+                                float* scales, cudaStream_t st);
+cudaError_t launch_fp8_swiglu(const void* h, int h_dtype, int M, int I, uint8_t* codes, float* scales, cudaStream_t st);
+cudaError_t launch_fp8_weights(const void* w, int w_dtype, int E, int N, int K, uint8_t* codes, float* scales,
+                               cudaStream_t st);
+cudaError_t launch_fp8_dequant(const uint8_t* codes, const float* scales, int E, int N, int K, int block_rows, void* out,
+                               int out_dtype, cudaStream_t st);
+cudaError_t launch_fp8_matmul(const uint8_t* xc, const float* xs, const uint8_t* wc, const float* ws,
+                              const int32_t* offsets, int E, int M, int N, int K, void* y, int y_dtype, uint32_t* status,
+                              cudaStream_t st);
+cudaError_t fp8_status_word(void** word);  // the current device's, for calls without one
+cudaError_t launch_sort_experts(const int32_t* ids, int A, int E, int32_t* offsets, int32_t* perm, int32_t* pos,
+                                cudaStream_t st);
+cudaError_t launch_dispatch(const void* x, int row_bytes, int T, int k, const int32_t* pos, void* xs, cudaStream_t st);
+cudaError_t launch_combine(const void* ys, int ys_dtype, const int32_t* pos, const float* w, const void* residual, int T,
+                           int H, int k, void* out, int out_dtype, cudaStream_t st);
+cudaError_t launch_combine_backward(const void* dout, int dout_dtype, const void* ys, int ys_dtype, const int32_t* pos,
+                                    const float* w, int T, int H, int k, void* dys, float* dw, cudaStream_t st);
+
 cudaError_t launch_rmsnorm(const void* x, void* out, int act_dtype, int T, int H, float eps,
                            cudaStream_t st);
 
