@@ -564,10 +564,13 @@ int qmoe_fp8_dequant(const uint8_t* codes, const float* scales, int E, int N, in
  *                 qmoe_route give them: rows offsets[e] .. offsets[e + 1] - 1 of
  *                 x and y belong to expert e, whose weights are W[e]; rows
  *                 outside every expert's are not read, and y's are left as they
- *                 were.  The offsets have to increase within 0 .. M: what lies
- *                 outside is cut off there, and QMOE_ST_INDEX is set.  At most
- *                 QMOE_MAX_EXPERTS experts.
+ *                 were.  Offsets that decrease or leave 0 .. M set QMOE_ST_INDEX,
+ *                 and all of y is left as it was.  At most QMOE_MAX_EXPERTS
+ *                 experts.
  * A NaN scale or code makes the outputs that it enters NaN, and no others.
+ * One kernel.  Its tile and the split of K are chosen by E, M, N, K, whether
+ * there are offsets, and the device: calls that agree in these give the same
+ * bits, others sum in another order.
  * status_dev (a 4-byte device word that the caller set to 0, or NULL): collects
  * QMOE_ST_INDEX, and QMOE_ST_TIMEOUT where a bounded wait ran out (y is then
  * undefined); read it with qmoe_get_device_status(status_dev, ...).  NULL: the
@@ -575,6 +578,26 @@ int qmoe_fp8_dequant(const uint8_t* codes, const float* scales, int E, int N, in
 int qmoe_fp8_matmul(const uint8_t* x_codes, const float* x_scales, const uint8_t* w_codes, const float* w_scales,
                     const int32_t* offsets, int E, int M, int N, int K, void* y, int y_dtype, uint32_t* status_dev,
                     void* stream);
+
+/* The form of the kernel that qmoe_fp8_matmul runs for such a call on the
+ * current device (no launch): variant_out[0] tokens per tile, [1] 1 for pairs
+ * of CTAs, [2] CTAs that share a tile's K. */
+int qmoe_fp8_matmul_variant(int grouped, int E, int M, int N, int K, int variant_out[3]);
+
+/* qmoe_fp8_matmul with diagnostics of its failure path, as
+ * qmoe_mx_matmul_diagnosed: the named roles (the copies of codes, the scales,
+ * the MMAs, the sums and outputs) wait for what cannot arrive before their
+ * first step, the waits give up after wait_limit_kilocycles x 1024 SM cycles (0:
+ * about 2 s), and the status reads QMOE_ST_TIMEOUT.  QMOE_ERR_INVALID_ARG for
+ * unknown flags. */
+#define QMOE_DIAG_STALL_FP8_CODES 1u
+#define QMOE_DIAG_STALL_FP8_SCALES 2u
+#define QMOE_DIAG_STALL_FP8_MMA 4u
+#define QMOE_DIAG_STALL_FP8_OUTPUT 8u
+int qmoe_fp8_matmul_diagnosed(const uint8_t* x_codes, const float* x_scales, const uint8_t* w_codes,
+                              const float* w_scales, const int32_t* offsets, int E, int M, int N, int K, void* y,
+                              int y_dtype, uint32_t* status_dev, uint32_t wait_limit_kilocycles, uint32_t flags,
+                              void* stream);
 
 /* The status word, on the current device, of the FP8 products that were given
  * none: as qmoe_mx_status. */

@@ -20,6 +20,7 @@ AUTO_DECODE_MAX_TOKENS = 5
 DIAG_STALL_GEMM = 1
 F32 = 2                      # the microscaled entry points that say so
 MXFP8, MXFP4 = 0, 1
+DIAG_STALL_FP8_CODES, DIAG_STALL_FP8_SCALES, DIAG_STALL_FP8_MMA, DIAG_STALL_FP8_OUTPUT = 1, 2, 4, 8
 DIAG_STALL_MX_CODES, DIAG_STALL_MX_SCALES, DIAG_STALL_MX_MMA, DIAG_STALL_MX_OUTPUT, DIAG_STALL_MX_SPREAD = 1, 2, 4, 8, 16
 _STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported device or shape",
            3: "workspace missing or too small", 4: "CUDA runtime error",
@@ -123,6 +124,11 @@ def lib():
         L.qmoe_fp8_dequant.argtypes = [vp, vp, i32, i32, i32, i32, vp, i32, vp]
         L.qmoe_fp8_matmul.restype = i32
         L.qmoe_fp8_matmul.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, i32, vp, vp]
+        L.qmoe_fp8_matmul_diagnosed.restype = i32
+        L.qmoe_fp8_matmul_diagnosed.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, i32, vp, ctypes.c_uint32,
+                                                ctypes.c_uint32, vp]
+        L.qmoe_fp8_matmul_variant.restype = i32
+        L.qmoe_fp8_matmul_variant.argtypes = [i32, i32, i32, i32, i32, ctypes.POINTER(ctypes.c_int)]
         L.qmoe_fp8_status.restype = i32
         L.qmoe_fp8_status.argtypes = [ctypes.POINTER(ctypes.c_uint32), vp]
         L.qmoe_sort_experts.restype = i32
@@ -737,12 +743,14 @@ def qmoe_fp8_dequant(codes, scales, dtype=torch.bfloat16, out=None):
     return out
 
 
-def qmoe_fp8_matmul(x_codes, x_scales, w_codes, w_scales, dtype=torch.bfloat16, offsets=None, out=None, status=None):
+def qmoe_fp8_matmul(x_codes, x_scales, w_codes, w_scales, dtype=torch.bfloat16, offsets=None, out=None, status=None,
+                    diagnostics=None):
     """y [M, N] (fp16, bf16 or fp32) = x . W^T for FP8 tensors x [M, K] and W [N, K];
     with offsets int32 [E + 1] and W [E, N, K], rows offsets[e] .. offsets[e + 1] - 1
     meet W[e], and the rows of y outside every expert's are left as they were.
     status: an int32 [1] device tensor that collects QMOE_ST_* bits (zero it
-    first); without one qmoe_fp8_status() tells."""
+    first); without one qmoe_fp8_status() tells.  diagnostics: (wait_limit_kilocycles,
+    DIAG_STALL_FP8_* flags) of qmoe_fp8_matmul_diagnosed."""
     where = "qmoe_fp8_matmul"
     M, K = _mx_size(x_codes, where)
     dev, dt = x_codes.get_device(), _MX_DT.get(dtype)
@@ -771,9 +779,22 @@ def qmoe_fp8_matmul(x_codes, x_scales, w_codes, w_scales, dtype=torch.bfloat16, 
     if status is not None:
         _mx_check(status, dev, _I32, 1, where, "status")
         st = status.data_ptr()
-    _mx_call(dev, lib().qmoe_fp8_matmul, where, x_codes.data_ptr(), x_scales.data_ptr(), w_codes.data_ptr(),
-             w_scales.data_ptr(), op, E, M, N, K, out.data_ptr(), dt, st)
+    if diagnostics is None:
+        _mx_call(dev, lib().qmoe_fp8_matmul, where, x_codes.data_ptr(), x_scales.data_ptr(), w_codes.data_ptr(),
+                 w_scales.data_ptr(), op, E, M, N, K, out.data_ptr(), dt, st)
+    else:
+        _mx_call(dev, lib().qmoe_fp8_matmul_diagnosed, where, x_codes.data_ptr(), x_scales.data_ptr(), w_codes.data_ptr(),
+                 w_scales.data_ptr(), op, E, M, N, K, out.data_ptr(), dt, st, *diagnostics)
     return out
+
+
+def qmoe_fp8_matmul_variant(M, N, K, E=None):
+    """(tokens per tile, pairs of CTAs, CTAs along K) of the kernel that a product
+    of these sizes runs on the current device; E: grouped, over so many experts."""
+    v = (ctypes.c_int * 3)()
+    _fp8_size(M, K, "qmoe_fp8_matmul_variant"), _fp8_size(N * (E or 1), K, "qmoe_fp8_matmul_variant")
+    _check(lib().qmoe_fp8_matmul_variant(E is not None, 1 if E is None else E, M, N, K, v), "qmoe_fp8_matmul_variant")
+    return tuple(v)
 
 
 def qmoe_fp8_status():

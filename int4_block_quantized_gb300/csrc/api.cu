@@ -681,6 +681,17 @@ int qmoe_fp8_dequant(const uint8_t* codes, const float* scales, int E, int N, in
 int qmoe_fp8_matmul(const uint8_t* x_codes, const float* x_scales, const uint8_t* w_codes, const float* w_scales,
                     const int32_t* offsets, int E, int M, int N, int K, void* y, int y_dtype, uint32_t* status_dev,
                     void* stream) {
+  return qmoe_fp8_matmul_diagnosed(x_codes, x_scales, w_codes, w_scales, offsets, E, M, N, K, y, y_dtype, status_dev, 0, 0,
+                                   stream);
+}
+
+int qmoe_fp8_matmul_diagnosed(const uint8_t* x_codes, const float* x_scales, const uint8_t* w_codes,
+                              const float* w_scales, const int32_t* offsets, int E, int M, int N, int K, void* y,
+                              int y_dtype, uint32_t* status_dev, uint32_t wait_limit_kilocycles, uint32_t flags,
+                              void* stream) {
+  if (flags & ~(QMOE_DIAG_STALL_FP8_CODES | QMOE_DIAG_STALL_FP8_SCALES | QMOE_DIAG_STALL_FP8_MMA |
+                QMOE_DIAG_STALL_FP8_OUTPUT))
+    return QMOE_ERR_INVALID_ARG;
   if (!valid_dtype_or_f32(y_dtype) || !y || !aligned(y, y_dtype == QMOE_F32 ? 4 : 2) || !aligned(status_dev, 4) ||
       !aligned(offsets, 4) || (!offsets && E != 1))
     return QMOE_ERR_INVALID_ARG;
@@ -689,7 +700,16 @@ int qmoe_fp8_matmul(const uint8_t* x_codes, const float* x_scales, const uint8_t
   if (E > QMOE_MAX_EXPERTS) return QMOE_ERR_UNSUPPORTED;
   if ((rc = check_device())) return rc;
   return cuda_status(launch_fp8_matmul(x_codes, x_scales, w_codes, w_scales, offsets, E, M, N, K, y, y_dtype, status_dev,
-                                       (cudaStream_t)stream));
+                                       wait_limit_kilocycles, flags, (cudaStream_t)stream));
+}
+
+int qmoe_fp8_matmul_variant(int grouped, int E, int M, int N, int K, int variant_out[3]) {
+  if (!variant_out || (!grouped && E != 1)) return QMOE_ERR_INVALID_ARG;
+  int rc = check_fp8_size(1, M, K);
+  if (rc || (rc = check_fp8_size(E, N, K))) return rc;
+  if (E > QMOE_MAX_EXPERTS) return QMOE_ERR_UNSUPPORTED;
+  if ((rc = check_device())) return rc;
+  return cuda_status(fp8_matmul_variant(grouped != 0, E, M, N, K, variant_out, variant_out + 1, variant_out + 2));
 }
 
 int qmoe_fp8_status(uint32_t* bits_out, void* stream) {

@@ -3,83 +3,727 @@
 //   y[m, n] = sum over blocks b of sx[m, b] sw[n / 128, b] sum_{k in b} x[m, k] w[n, k]
 // with fp32 sums, rounded once to the output's type.  Grouped: row m meets the
 // weights of the expert e with offsets[e] <= m < offsets[e + 1].
+//
+// The scales are any fp32 numbers, so the tensor cores (kind::f8f6f4) sum one
+// block of 128 k at a time into a buffer of tensor memory of its own; eight warps
+// read it from there, multiply with the block's scales and add to sums that they
+// keep in registers, while the next block is multiplied into the next buffer.
+// Weight rows are the MMA's M = 128 operand and tokens its N, so that a few
+// tokens cost a narrow MMA; a tile of weight rows lies within one scale block,
+// so a block's scales are a vector over the tokens, which two warps put together
+// in shared memory.  Tensor memory is read in the layout of 8 x 8 fragments, in
+// which a thread's neighbouring values are neighbouring tokens: one pair of
+// scales serves eight values, and packed fp32 arithmetic does two at a time.
+#include <cuda.h>
+
 #include "fp8.cuh"
 #include "launch.h"
+#include "tmap.h"
 
 namespace qmoe {
 
-// The status word of the calls that bring none.
-__device__ uint32_t g_fp8_status;
+// Warp 0 copies codes, 1 issues MMAs, 2 and 3 prepare scales, 4 to 11 scale and
+// add the blocks' sums and write y.
+constexpr int kFmThreads = 384;
+constexpr uint32_t kFmSmem = 232448;  // 227 KB
+constexpr uint32_t kFmBars = 1024;
+constexpr uint32_t kFmTable = 3328;  // experts' first token tile, first and last row
 
 struct FmParams {
-  const uint8_t *xc, *wc;
   const float *xs, *ws;
   const int32_t* offsets;
   void* y;
   uint32_t* status;
   int E, M, N, K, y_dtype;
+  int row_tiles;        // tiles of 128 CG weight rows of an expert
+  int wide_out;         // y: 16 bits, rows on 16-byte boundaries
+  int wide_scales;      // four of a row's scales on 16 bytes
+  int split;            // CTAs of a cluster that share a tile's K
+  uint32_t stall;       // QMOE_DIAG_STALL_FP8_*: this role waits for what cannot arrive
+  long long wait_limit; // SM cycles
 };
+
+template <int BN, int CG>
+struct FmPlan {
+  static constexpr uint32_t kA = 128 * 128, kB = BN / CG * 128;  // one CTA's share of a block's codes
+  static constexpr int kBox = BN / CG < 64 ? BN / CG : 64;       // tokens of a copy
+  // buffers of tensor memory for the blocks' sums
+  static constexpr int kBufs = BN >= 64 ? 512 / BN : 8;
+  // tokens that a warp reads at once, and how often: two warps per lane quadrant take turns
+  static constexpr int kW = BN >= 64 ? 32 : BN / 2, kQ = BN / 2 / kW, kG = kW / 8;
+  static constexpr uint32_t kOut = 8 * kW * 64;                  // 32 outputs of kW tokens a warp, turned round there
+  static constexpr int kQuads = BN == 256 ? 3 : 4;               // scales: slots of four blocks
+  static constexpr uint32_t kScales = kQuads * 4 * BN * 4;
+  // a split tile's partial sums [split][tokens of a CTA / 2][128][2]: a place of
+  // their own where they are small, else the ring once the cluster is done with it
+  static constexpr uint32_t kPart = BN <= 64 ? BN * 512 : 0;
+  static constexpr uint32_t kFixed = kFmBars + kFmTable + kOut + kScales + kPart;
+  static constexpr uint32_t kAt = (kFixed + 1023) & ~1023u;      // the ring's place
+  static constexpr uint32_t kStage = (kA + kB + 1023) & ~1023u;
+  static constexpr int kStages0 = (int)((kFmSmem - 1024 - kAt) / kStage);
+  static constexpr int kStages = kStages0 > 12 ? 12 : kStages0;
+};
+
+// The status word of the calls that bring none.
+__device__ uint32_t g_fp8_status;
+__device__ __forceinline__ void fm_status(const FmParams& p, uint32_t bit) {
+  set_status(p.status ? p.status : &g_fp8_status, bit);
+}
+
+// Bounded wait; gives up when another role has, or after the limit (about 2 s)
+// with the status bit.  WARP: all lanes of the warp wait and agree on the answer
+// by a vote (each may see the phase end at another poll).  The warp that issues
+// MMAs has no votes: what its elected lane sees decides all that it does.
+template <bool WARP = true>
+__device__ __forceinline__ bool fm_wait(uint64_t* bar, uint32_t parity, const FmParams& p, volatile int* abort) {
+  auto all = [](bool v) { return WARP ? __all_sync(0xffffffffu, v) != 0 : v; };
+  if (all(mbar_try_wait(bar, parity))) return true;
+  const long long t0 = clock64();
+  while (!all(mbar_try_wait_sleep(bar, parity, 20000u))) {
+    const bool late = clock64() - t0 > p.wait_limit;
+    if (!all(!(late || *abort))) {
+      if (late) fm_status(p, QMOE_ST_TIMEOUT);
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
+// The end of a warp that has issued `it` copies into a ring of S slots: it waits
+// for the last use of each, time-out or not, so that no copy lands in shared
+// memory that is another CTA's by then.  After a time-out slots may stay as they
+// are; a copy lands within microseconds, so 10 ms for all of them do.
+constexpr long long kFmSettleCycles = 20000000;
+template <int S>
+__device__ __forceinline__ void fm_settle(uint64_t* bars, int it, const FmParams& p, volatile int* abort) {
+  const long long t0 = clock64();
+  for (int n = max(it - S, 0); n < it; ++n)
+    while (!mbar_try_wait_sleep(&bars[n % S], (n / S) & 1, 20000u)) {
+      const long long t = clock64() - t0;
+      if (*abort) {
+        if (t > kFmSettleCycles) break;
+      } else if (t > p.wait_limit) {
+        fm_status(p, QMOE_ST_TIMEOUT);
+        *abort = 1;
+      }
+    }
+}
 
 __device__ __forceinline__ void fm_store(const FmParams& p, size_t i, float v) {
   if (p.y_dtype == QMOE_F32) static_cast<float*>(p.y)[i] = v;
   else static_cast<uint16_t*>(p.y)[i] = p.y_dtype == QMOE_BF16 ? Half<__nv_bfloat16>::from_float(v) : Half<__half>::from_float(v);
 }
+// two results to the output's 16-bit type
+__device__ __forceinline__ uint32_t fm_pack(const FmParams& p, f2 v) {
+  if (p.y_dtype == QMOE_BF16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __half2 h = __floats2half2_rn(v.x, v.y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
 
-// A simple form: 64 x 64 outputs a CTA, 4 x 4 a thread, 32 k at a time.
-__global__ void __launch_bounds__(256) fp8_matmul_kernel(const FmParams p) {
-  pdl_wait();
-  __shared__ float sx[32][68], sw[32][68];
-  const int e = blockIdx.z, n0 = blockIdx.x * 64;
-  int m0 = 0, m1 = p.M;
-  if (p.offsets) {
-    const int o0 = p.offsets[e], o1 = p.offsets[e + 1];
-    m0 = min(max(o0, 0), p.M);
-    m1 = min(max(o1, 0), p.M);
-    if (m0 != o0 || m1 != o1 || m1 < m0) set_status(p.status ? p.status : &g_fp8_status, QMOE_ST_INDEX);
+// 32 lanes x 8 G columns of tensor memory as fragments: r[i][j] holds columns
+// 8 i + 2 (lane % 4) + {0, 1} of row lane / 4 + 8 j.
+template <int G>
+__device__ __forceinline__ void fm_load(uint32_t taddr, f2 (&r)[G][4]) {
+  uint32_t lo[4 * G], hi[4 * G];
+  if constexpr (G == 4) {
+    tmem_ld_frag(taddr, lo, hi);
+  } else if constexpr (G == 2) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%16];\n"
+        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%17];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(lo[0]), "=r"(lo[1]), "=r"(lo[2]), "=r"(lo[3]), "=r"(lo[4]), "=r"(lo[5]), "=r"(lo[6]), "=r"(lo[7]),
+          "=r"(hi[0]), "=r"(hi[1]), "=r"(hi[2]), "=r"(hi[3]), "=r"(hi[4]), "=r"(hi[5]), "=r"(hi[6]), "=r"(hi[7])
+        : "r"(taddr), "r"(taddr + (16u << 16))
+        : "memory");
+  } else {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%8];\n"
+        "tcgen05.ld.sync.aligned.16x256b.x1.b32 {%4,%5,%6,%7}, [%9];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(lo[0]), "=r"(lo[1]), "=r"(lo[2]), "=r"(lo[3]), "=r"(hi[0]), "=r"(hi[1]), "=r"(hi[2]), "=r"(hi[3])
+        : "r"(taddr), "r"(taddr + (16u << 16))
+        : "memory");
   }
-  const int nb = (p.K + 127) / 128, rb = (p.N + 127) / 128;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int lr = threadIdx.x >> 2, lk = (threadIdx.x & 3) * 8;
-  for (int m = m0 + blockIdx.y * 64; m < m1; m += gridDim.y * 64) {
-    float acc[4][4] = {};
-    for (int k = 0; k < p.K; k += 32) {
-      float v[8];
-      auto fetch = [&](const uint8_t* base, size_t row, bool ok) {
-        uint2 c = make_uint2(0, 0);
-        if (ok && k + lk < p.K) c = *reinterpret_cast<const uint2*>(base + row * p.K + k + lk);
-        mx_from_e4m3x4(c.x, v);
-        mx_from_e4m3x4(c.y, v + 4);
-      };
-      fetch(p.xc, m + lr, m + lr < m1);
-      const float s = m + lr < m1 ? p.xs[(size_t)(m + lr) * nb + k / 128] : 0.f;
-      for (int j = 0; j < 8; ++j) sx[lk + j][lr] = v[j] * s;
-      fetch(p.wc, (size_t)e * p.N + n0 + lr, n0 + lr < p.N);
-      const float t = n0 + lr < p.N ? p.ws[((size_t)e * rb + (n0 + lr) / 128) * nb + k / 128] : 0.f;
-      for (int j = 0; j < 8; ++j) sw[lk + j][lr] = v[j] * t;
-      __syncthreads();
-#pragma unroll 8
-      for (int kk = 0; kk < 32; ++kk) {
-        float a[4], b[4];
-        for (int j = 0; j < 4; ++j) a[j] = sx[kk][ty * 4 + j], b[j] = sw[kk][tx * 4 + j];
-        for (int i = 0; i < 4; ++i)
-          for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
-      }
-      __syncthreads();
+#pragma unroll
+  for (int i = 0; i < G; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      r[i][j] = make_float2(__uint_as_float(lo[4 * i + 2 * j]), __uint_as_float(lo[4 * i + 2 * j + 1]));
+      r[i][j + 2] = make_float2(__uint_as_float(hi[4 * i + 2 * j]), __uint_as_float(hi[4 * i + 2 * j + 1]));
     }
-    for (int i = 0; i < 4; ++i)
-      for (int j = 0; j < 4; ++j)
-        if (m + ty * 4 + i < m1 && n0 + tx * 4 + j < p.N) fm_store(p, (size_t)(m + ty * 4 + i) * p.N + n0 + tx * 4 + j, acc[i][j]);
+}
+
+// D[tmem] (+)= A x B^T of e4m3 codes (shared-memory descriptors as sw128_desc,
+// low words), 32 k, by the lane of a converged warp whose e is 1.
+#define QMOE_MMA_F8(CGS)                                                                                 \
+  asm volatile(                                                                                          \
+      "{\n .reg .pred p, e;\n .reg .b64 a, b;\n mov.b64 a, {%1, %6};\n mov.b64 b, {%2, %6};\n"            \
+      " setp.ne.b32 e, %5, 0;\n setp.ne.b32 p, %4, 0;\n"                                                 \
+      " @e tcgen05.mma.cta_group::" CGS ".kind::f8f6f4 [%0], a, b, %3, p;\n}" ::"r"(d),                  \
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(e), "n"((1024u >> 4) | 1u << 14 | 2u << 29)       \
+      : "memory")
+template <int CG>
+__device__ __forceinline__ void mma_f8(uint32_t e, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  if constexpr (CG == 1) QMOE_MMA_F8("1");
+  else QMOE_MMA_F8("2");
+}
+#undef QMOE_MMA_F8
+
+// A tile: 128 CG weight rows of an expert from row rt, tokens m0 .. m1 - 1.
+struct FmTile {
+  int e, rt, m0, m1;
+};
+struct FmTable {
+  int first[kMaxExperts + 1];  // token tiles of the experts before
+  int start[kMaxExperts], end[kMaxExperts];
+};
+static_assert(sizeof(FmTable) <= kFmTable, "table");
+
+// Tile t: by expert, within it in groups of 8 row tiles, so that the tiles in
+// flight share weights and tokens in L2.
+template <int BN>
+__device__ __forceinline__ FmTile fm_tile(const FmParams& p, const FmTable& tab, int t) {
+  FmTile f;
+  const int q = t / p.row_tiles;
+  int lo = 0, hi = p.E;  // first[lo] <= q < first[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (tab.first[mid] <= q) lo = mid;
+    else hi = mid;
   }
+  const int tok = tab.first[lo + 1] - tab.first[lo];
+  t -= tab.first[lo] * p.row_tiles;
+  const int per = 8 * tok, g = t / per, r = t - g * per, rows = min(8, p.row_tiles - g * 8);
+  f.e = lo;
+  f.rt = g * 8 + r % rows;
+  f.m0 = tab.start[lo] + r / rows * BN;
+  f.m1 = min(f.m0 + BN, tab.end[lo]);
+  return f;
+}
+
+template <int BN, int CG>
+__global__ void __launch_bounds__(kFmThreads, 1)
+    fp8_matmul_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
+                      const FmParams p) {
+  using P = FmPlan<BN, CG>;
+  constexpr int S = P::kStages, NB = P::kBufs, SQ = P::kQuads;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem);
+  uint64_t* empty = full + S;
+  uint64_t* acc_full = empty + S;      // [NB]
+  uint64_t* acc_free = acc_full + NB;  // [NB]
+  uint64_t* sc_full = acc_free + NB;   // [SQ]
+  uint64_t* sc_free = sc_full + SQ;    // [SQ]
+  uint64_t* fin = sc_free + SQ;
+  uint64_t* never = fin + 1;  // nothing arrives here (p.stall)
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(never + 1);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+  int* s_sum = reinterpret_cast<int*>(s_tmem + 2);  // [8]
+  FmTable& tab = *reinterpret_cast<FmTable*>(smem + kFmBars);
+  uint8_t* outbuf = smem + kFmBars + kFmTable;
+  float* scales = reinterpret_cast<float*>(outbuf + P::kOut);
+  float* part_own = scales + P::kScales / 4;
+  uint8_t* ring = smem + P::kAt;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be the same in all lanes
+
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < NB; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_free[b], 8 * CG);
+    }
+    for (int b = 0; b < SQ; ++b) {
+      mbar_init(&sc_full[b], 2);
+      mbar_init(&sc_free[b], 8);
+    }
+    mbar_init(fin, 1);
+    mbar_init(never, 1);
+    *s_abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    if (CG == 1) {
+      tmem_alloc(s_tmem, 512);
+      tmem_relinquish();
+    } else {
+      tmem_alloc2(s_tmem, 512);
+      tmem_relinquish2();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (CG == 2) cluster_sync_all();  // the pair's barriers are set up
+  tc_fence_after();
+  // all 512 columns are this CTA's, so they start at 0
+  constexpr uint32_t tmem = 0;
+  if (P::kPart && p.split > 1) cluster_arrive();  // this CTA runs: its shared memory may be written
+  pdl_wait();
+  pdl_trigger();
+
+  // the experts' rows and token tiles; none where the offsets are no offsets
+  if (!p.offsets) {
+    if (tid == 0) tab.first[0] = 0, tab.first[1] = (p.M + BN - 1) / BN, tab.start[0] = 0, tab.end[0] = p.M;
+  } else {
+    int sum = 0, bad = 0;
+    if (tid < p.E) {
+      const int a = p.offsets[tid], b = p.offsets[tid + 1];
+      bad = a < 0 || b < a || b > p.M;
+      tab.start[tid] = a;
+      tab.end[tid] = b;
+      sum = (int)(((long long)b - a + BN - 1) / BN);
+    }
+    bad = __syncthreads_or(bad);
+    if (bad) sum = 0;
+    if (bad && blockIdx.x == 0 && tid == 0) fm_status(p, QMOE_ST_INDEX);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += up;
+    }
+    if (warp < 8 && lane == 31) s_sum[warp] = sum;
+    __syncthreads();
+    if (tid < p.E) {
+      for (int w = 0; w < warp; ++w) sum += s_sum[w];
+      tab.first[tid + 1] = sum;
+      if (tid == 0) tab.first[0] = 0;
+    }
+  }
+  __syncthreads();
+
+  // this CTA's tiles and its share [c0, c1) of their blocks along K
+  const int rank = p.split > 1 ? (int)cluster_ctarank() : 0;
+  const int half = CG == 2 ? (int)cluster_ctarank() : 0;  // of the pair's rows and tokens
+  const int tiles = tab.first[p.E] * p.row_tiles;
+  const int first = blockIdx.x / (CG * p.split), step = p.split > 1 ? max(tiles, (int)gridDim.x) : gridDim.x / CG;
+  const int nb = (p.K + 127) / 128;
+  auto stalled = [&](uint32_t role) { return (p.stall & role) && !fm_wait(never, 0, p, s_abort); };
+  const int c0 = (int)((long long)nb * rank / p.split), c1 = (int)((long long)nb * (rank + 1) / p.split);
+  f2 acc[P::kQ][P::kG][4];
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ codes
+    int it = 0, s = 0;
+    uint32_t ph = 0;
+    bool ok = !stalled(QMOE_DIAG_STALL_FP8_CODES);
+    const uint32_t el = elect_lane();
+    for (int t = first; t < tiles && ok; t += step) {
+      const FmTile f = fm_tile<BN>(p, tab, t);
+      const int row = f.e * p.N + (f.rt * CG + half) * 128;
+      // copies of kBox tokens, as many as the tile has (a pair: always all)
+      const int boxes = CG == 2 ? BN / CG / P::kBox : (f.m1 - f.m0 + P::kBox - 1) / P::kBox;
+      for (int c = c0; c < c1; ++c, ++it) {
+        if (it >= S) ok = fm_wait(&empty[s], ph ^ 1u, p, s_abort);
+        if (!ok) break;
+        if (el) {
+          uint8_t* st = ring + s * P::kStage;
+          if constexpr (CG == 2) {  // both CTAs report to the leader
+            const uint32_t bar = peer_u32(&full[s], 0);
+            if (half == 0) mbar_arrive_expect_tx(&full[s], 2 * (P::kA + P::kB));
+            tma_load_2d_pair(st, &tm_w, c * 128, row, bar);
+            for (int i = 0; i < boxes; ++i)
+              tma_load_2d_pair(st + P::kA + i * P::kBox * 128, &tm_x, c * 128, f.m0 + half * (BN / 2) + i * P::kBox, bar);
+          } else {
+            mbar_arrive_expect_tx(&full[s], P::kA + boxes * P::kBox * 128);
+            tma_load_2d(st, &tm_w, c * 128, row, &full[s]);
+            for (int i = 0; i < boxes; ++i)
+              tma_load_2d(st + P::kA + i * P::kBox * 128, &tm_x, c * 128, f.m0 + i * P::kBox, &full[s]);
+          }
+        }
+        __syncwarp();
+        if (++s == S) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+    }
+    // A pair's stages are counted in the leader alone, but both CTAs see the
+    // commits that give slots back (and stay until these have arrived).
+    if (lane == 0) fm_settle<S>(CG == 1 ? full : empty, it, p, s_abort);
+  } else if (warp == 1 && half == 0) {
+    // ------------------------------------------------------------- MMAs
+    int n = 0, s = 0;  // blocks so far
+    uint32_t ph = 0;
+    bool ok = !stalled(QMOE_DIAG_STALL_FP8_MMA), issued = false;
+    const uint32_t el = elect_lane();
+    for (int t = first; t < tiles && ok; t += step) {
+      const FmTile f = fm_tile<BN>(p, tab, t);
+      const int cols = CG == 2 ? BN : (f.m1 - f.m0 + 15) & ~15;
+      // D fp32, A and B e4m3, both K-major
+      const uint32_t idesc = 1u << 4 | (uint32_t)(cols >> 3) << 17 | (uint32_t)(128 * CG >> 4) << 24;
+      for (int c = c0; c < c1; ++c, ++n) {
+        const int b = n % NB;
+        if (n >= NB) ok = fm_wait<false>(&acc_free[b], (n / NB - 1) & 1, p, s_abort);
+        if (ok) ok = fm_wait<false>(&full[s], ph, p, s_abort);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t st = (smem_u32(ring + s * P::kStage) >> 4) & 0x3FFFu;  // a descriptor's address field
+        const uint32_t da = st | 1u << 16, db = (st + (P::kA >> 4)) | 1u << 16;
+        const int left = p.K - c * 128;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (32 * j >= left) break;
+          mma_f8<CG>(el, tmem + b * BN, da + 2 * j, db + 2 * j, idesc, j > 0);
+        }
+        mma_commit_mx<CG>(el, &empty[s]);
+        mma_commit_mx<CG>(el, &acc_full[b]);
+        issued = true;
+        if (++s == S) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+    }
+    if (issued) {  // all MMAs have finished before tensor memory is freed
+      if (CG == 1) mma_commit_mx<1>(el, fin);
+      else mma_commit_mx2_own(el, fin);  // a commit to the peer's barrier too could arrive there when it has left
+      if (el) mbar_wait(fin, 0, nullptr);
+    }
+  } else if (warp == 2 || warp == 3) {
+    // ----------------------------------------- scales, four blocks at a time
+    int it = 0;
+    const int rb = (p.N + 127) / 128;
+    bool ok = !stalled(QMOE_DIAG_STALL_FP8_SCALES);
+    for (int t = first; t < tiles && ok; t += step) {
+      const FmTile f = fm_tile<BN>(p, tab, t);
+      const int rt = f.rt * CG + half;
+      const float* ws = p.ws + ((size_t)f.e * rb + rt) * nb;
+      for (int c = c0; c < c1; c += 4, ++it) {
+        const int q = it % SQ;
+        float w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = rt < rb && c + j < c1 ? ws[c + j] : 0.f;
+        if (it >= SQ) ok = fm_wait(&sc_free[q], (it / SQ - 1) & 1, p, s_abort);
+        if (!ok) break;
+        float* out = scales + q * 4 * BN;
+#pragma unroll
+        for (int i = (warp - 2) * 32 + lane; i < BN; i += 64) {
+          float v[4] = {};
+          if (f.m0 + i < f.m1) {
+            const float* xs = p.xs + (size_t)(f.m0 + i) * nb + c;
+            if (p.wide_scales) {
+              const float4 u = *reinterpret_cast<const float4*>(xs);
+              v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) v[j] = c + j < c1 ? xs[j] : 0.f;
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) out[j * BN + i] = v[j] * w[j];
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sc_full[q]);
+      }
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------- the blocks' sums, scaled and added
+    const int qd = warp & 3, set = (warp - 4) >> 2;
+    uint8_t* buf = outbuf + (warp - 4) * (P::kW * 64);
+    int n = 0, it = 0;
+    bool ok = !stalled(QMOE_DIAG_STALL_FP8_OUTPUT);
+    for (int t = first; t < tiles && ok; t += step) {
+      const FmTile f = fm_tile<BN>(p, tab, t);
+      const int cols = f.m1 - f.m0;
+#pragma unroll
+      for (int q = 0; q < P::kQ; ++q)
+#pragma unroll
+        for (int i = 0; i < P::kG; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[q][i][j] = make_float2(0.f, 0.f);
+      for (int c = c0; c < c1; ++c, ++n) {
+        const int b = n % NB, sub = (c - c0) & 3, slot = it % SQ;
+        if (sub == 0) ok = fm_wait(&sc_full[slot], (it / SQ) & 1, p, s_abort);
+        if (ok) ok = fm_wait(&acc_full[b], (n / NB) & 1, p, s_abort);
+        if (!ok) break;
+        tc_fence_after();
+        const float* sc = scales + (slot * 4 + sub) * BN + 2 * (lane & 3);
+        const uint32_t d = tmem + ((uint32_t)(qd * 32) << 16) + b * BN;
+#pragma unroll
+        for (int q = 0; q < P::kQ; ++q) {
+          const int col = (2 * q + set) * P::kW;
+          if (col < cols) {
+            f2 v[P::kG][4];
+            fm_load<P::kG>(d + col, v);
+#pragma unroll
+            for (int i = 0; i < P::kG; ++i) {
+              const f2 s = *reinterpret_cast<const f2*>(sc + col + 8 * i);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) acc[q][i][j] = ffma2(v[i][j], s, acc[q][i][j]);
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (CG == 1) mbar_arrive(&acc_free[b]);
+          else mbar_arrive_cluster(peer_u32(&acc_free[b], 0));
+          if (sub == 3 || c + 1 == c1) mbar_arrive(&sc_free[slot]);
+        }
+        if (sub == 3 || c + 1 == c1) ++it;
+      }
+      if (!ok || p.split > 1) break;
+      const int n0 = (f.rt * CG + half) * 128 + qd * 32;
+#pragma unroll
+      for (int q = 0; q < P::kQ; ++q) {
+        const int col = (2 * q + set) * P::kW, m = f.m0 + col;
+        if (m >= f.m1 || n0 >= p.N) continue;
+        if (p.wide_out) {
+          // token 8 i + lane % 8 is a row of 64 bytes; its four 16-byte pieces
+          // (8 outputs each) are permuted against bank conflicts
+          const uint32_t a = smem_u32(buf) + (lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
+#pragma unroll
+          for (int i = 0; i < P::kG; ++i)
+            stmatrix_t4(a + i * 512, fm_pack(p, acc[q][i][0]), fm_pack(p, acc[q][i][1]), fm_pack(p, acc[q][i][2]),
+                        fm_pack(p, acc[q][i][3]));
+          __syncwarp();
+          const int tok = lane >> 2, piece = lane & 3;
+          uint16_t* y = static_cast<uint16_t*>(p.y) + (size_t)(m + tok) * p.N + n0 + piece * 8;
+#pragma unroll
+          for (int i = 0; i < P::kG; ++i, y += (size_t)8 * p.N)
+            if (m + 8 * i + tok < f.m1 && n0 + piece * 8 < p.N)
+              *reinterpret_cast<uint4*>(y) =
+                  *reinterpret_cast<const uint4*>(buf + i * 512 + tok * 64 + ((piece ^ ((tok >> 1) & 3)) << 4));
+          __syncwarp();
+        } else {
+#pragma unroll
+          for (int i = 0; i < P::kG; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int nn = n0 + (lane >> 2) + 8 * j, mm = m + 8 * i + 2 * (lane & 3);
+              if (nn < p.N) {
+                if (mm < f.m1) fm_store(p, (size_t)mm * p.N + nn, acc[q][i][j].x);
+                if (mm + 1 < f.m1) fm_store(p, (size_t)(mm + 1) * p.N + nn, acc[q][i][j].y);
+              }
+            }
+        }
+      }
+    }
+  }
+  __syncwarp();
+  if (p.split > 1) {
+    // Each CTA sends its partial sums of tokens j to CTA j / per, which adds
+    // them in rank order and writes y.  (A cluster without a tile only keeps
+    // the barriers.)
+    float* part = P::kPart ? part_own : reinterpret_cast<float*>(ring);
+    const bool some = first < tiles;
+    FmTile f = {0, 0, 0, 0};
+    if (some) f = fm_tile<BN>(p, tab, first);
+    const int rows = f.m1 - f.m0, per = max(2, BN / p.split), lper = 31 - __clz(per);
+    if (!P::kPart) cluster_arrive();
+    cluster_wait();
+    if (warp >= 4) {
+      const int qd = warp & 3, set = (warp - 4) >> 2;
+#pragma unroll
+      for (int q = 0; q < P::kQ; ++q)
+#pragma unroll
+        for (int i = 0; i < P::kG; ++i) {
+          const int tok = (2 * q + set) * P::kW + 8 * i + 2 * (lane & 3);
+          if (tok < rows) {
+            const uint32_t to = peer_u32(part + (((size_t)rank * per + (tok & (per - 1))) * 64 + qd * 32 + (lane >> 2)) * 2, tok >> lper);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to + 64 * j), "f"(acc[q][i][j].x), "f"(acc[q][i][j].y)
+                           : "memory");
+          }
+        }
+    }
+    __syncwarp();
+    cluster_sync_all();
+    const int mine = min(per, rows - rank * per);
+    const f2* p2 = reinterpret_cast<const f2*>(part);
+    for (int i = tid; i < (mine + 1) / 2 * 128; i += blockDim.x) {
+      const int nn = f.rt * 128 + (i & 127), j = rank * per + (i >> 7) * 2;
+      if (nn < p.N) {
+        f2 v = p2[i];
+        for (int r = 1; r < p.split; ++r) v = fadd2(v, p2[r * per * 64 + i]);
+        const size_t o = (size_t)(f.m0 + j) * p.N + nn;
+        fm_store(p, o, v.x);
+        if (j + 1 < rows) fm_store(p, o + p.N, v.y);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (CG == 2) cluster_sync_all();  // neither CTA leaves while the other may use its memory
+  if (warp == 1) {
+    tc_fence_after();
+    if (CG == 1) tmem_dealloc(tmem, 512);
+    else tmem_dealloc2(tmem, 512);
+  }
+}
+
+// Most token tiles that rows of E experts can make.
+static long long fm_token_tiles(const FmParams& p, int bn) {
+  if (!p.offsets) return (p.M + bn - 1) / bn;
+  const long long most = p.M / bn + (p.E < p.M ? p.E : p.M);
+  return most < p.M ? most : p.M;
+}
+
+template <int BN, int CG>
+static cudaError_t launch_fm(FmParams p, int split, const uint8_t* xc, const uint8_t* wc, cudaStream_t st) {
+  using P = FmPlan<BN, CG>;
+  static_assert(P::kStages >= 3 && P::kBufs * BN <= 512, "plan");
+  static_assert((2 * P::kStages + 2 * P::kBufs + 2 * P::kQuads + 2) * 8 + 40 <= kFmBars, "barriers");
+  p.split = split;
+  p.row_tiles = (p.N + 128 * CG - 1) / (128 * CG);
+  const long long tiles = fm_token_tiles(p, BN) * p.row_tiles;
+  if (tiles > (1LL << 27)) return cudaErrorInvalidValue;
+  CUtensorMap tw, tx;
+  if (!make_map(&tw, wc, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.K, (uint64_t)p.E * p.N, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B) ||
+      !make_map(&tx, xc, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.K, p.M, 128, P::kBox, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
+    return cudaErrorNotSupported;
+  p.wide_out = p.y_dtype != QMOE_F32 && p.N % 8 == 0 && !(reinterpret_cast<uintptr_t>(p.y) & 15);
+  p.wide_scales = split == 1 && p.K % 512 == 0 && !(reinterpret_cast<uintptr_t>(p.xs) & 15);
+  const int sms = device_sm_count();
+  auto kernel = fp8_matmul_kernel<BN, CG>;
+  // All of the SM's shared memory, used or not: the CTA takes all of its tensor
+  // memory, and a CTA of another kernel that waits for some (or has some) must
+  // not share the SM: two clusters could then wait for one another.
+  cudaError_t err = ensure_smem(kernel, kFmSmem);
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.split > 1 ? tiles * p.split : CG * (tiles < sms / CG ? tiles : sms / CG)));
+  cfg.blockDim = dim3(kFmThreads);
+  cfg.dynamicSmemBytes = kFmSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = p.split * CG;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, tw, tx, p);
+}
+
+// CTAs of clusters of `split` (2, 4, 8) that the device holds at once, one CTA
+// to an SM.  A query that fails fails the call: with a guess in its place, the
+// same call would sum in another order another time.
+static cudaError_t fm_capacity(int split, int* ctas) {
+  static int cached[64][4] = {};  // CTAs + 1
+  const int l = split == 8 ? 3 : split == 4 ? 2 : 1;
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!cached[dev][l]) {
+    auto kernel = fp8_matmul_kernel<16, 1>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(split);
+    cfg.blockDim = dim3(kFmThreads);
+    cfg.dynamicSmemBytes = kFmSmem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = split;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if ((err = ensure_smem(kernel, kFmSmem)) != cudaSuccess ||
+        (err = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg)) != cudaSuccess)
+      return err;
+    cached[dev][l] = n * split + 1;
+  }
+  *ctas = cached[dev][l] - 1;
+  return cudaSuccess;
+}
+
+struct FmChoice {
+  int bn, cg, split;
+};
+static cudaError_t fm_choose(const FmParams& p, FmChoice* choice) {
+  static const struct {
+    int bn, cg, start, stage, tile, epilogue, exchange;
+  } kinds[] = {{16, 1, 1900, 170, 300, 200, 1200},   {32, 1, 2000, 170, 350, 300, 1300},
+               {64, 1, 2900, 165, 500, 850, 1400},   {128, 1, 3600, 185, 1200, 1350, 2900},
+               {256, 1, 3900, 300, 800, 1900, 0},    {256, 2, 4600, 300, 1250, 2700, 0}};
+  int capacity[9] = {};
+  for (int split = 2; split <= 8; split *= 2) {
+    const cudaError_t err = fm_capacity(split, &capacity[split]);
+    if (err != cudaSuccess) return err;
+  }
+  const int nb = (p.K + 127) / 128;
+  const long long active = p.offsets ? (p.E < p.M ? p.E : p.M) : 1, each = (p.M + active - 1) / active;
+  long long least = -1;
+  for (const auto& k : kinds) {
+    if (k.bn < 64 && each > k.bn) continue;
+    const long long rows = (p.N + 128 * k.cg - 1) / (128 * k.cg);
+    const long long tiles = rows * active * ((each + k.bn - 1) / k.bn);
+    for (int split = 1; split <= 8; split *= 2) {
+      if (split > 1 && (!k.exchange || split > nb || rows * fm_token_tiles(p, k.bn) * split > capacity[split])) break;
+      const long long slots = split > 1 ? tiles : device_sm_count() / k.cg;
+      const long long rounds = (tiles + slots - 1) / slots;
+      const long long one = (long long)((nb + split - 1) / split) * k.stage, more = one + k.tile;
+      const long long t = k.start + one + (rounds - 1) * (more > k.epilogue ? more : k.epilogue) +
+                          (split > 1 ? k.exchange : 0);
+      if (least < 0 || t < least) {
+        least = t;
+        *choice = {k.bn, k.cg, split};
+      }
+    }
+  }
+  return cudaSuccess;
 }
 
 cudaError_t fp8_status_word(void** word) { return cudaGetSymbolAddress(word, g_fp8_status); }
 
+static FmParams fm_params(const float* xs, const float* ws, const int32_t* offsets, int E, int M, int N, int K) {
+  FmParams p = {};
+  p.xs = xs;
+  p.ws = ws;
+  p.offsets = offsets;
+  p.E = E;
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  return p;
+}
+
+cudaError_t fp8_matmul_variant(bool grouped, int E, int M, int N, int K, int* tokens, int* pair, int* split) {
+  static const int32_t some = 0;  // looked at for being given alone
+  const FmParams p = fm_params(nullptr, nullptr, grouped ? &some : nullptr, E, M, N, K);
+  FmChoice c = {};
+  const cudaError_t err = fm_choose(p, &c);
+  *tokens = c.bn;
+  *pair = c.cg == 2;
+  *split = c.split;
+  return err;
+}
+
 cudaError_t launch_fp8_matmul(const uint8_t* xc, const float* xs, const uint8_t* wc, const float* ws,
                               const int32_t* offsets, int E, int M, int N, int K, void* y, int y_dtype, uint32_t* status,
-                              cudaStream_t st) {
-  FmParams p = {xc, wc, xs, ws, offsets, y, status, E, M, N, K, y_dtype};
-  const int mt = (M + 63) / 64;
-  return launch_kernel(fp8_matmul_kernel, dim3((N + 63) / 64, mt < 128 ? mt : 128, E), dim3(256), 0, st, true, p);
+                              uint32_t wait_limit_kilocycles, uint32_t stall, cudaStream_t st) {
+  FmParams p = fm_params(xs, ws, offsets, E, M, N, K);
+  p.y = y;
+  p.y_dtype = y_dtype;
+  p.status = status;
+  p.stall = stall;
+  p.wait_limit = wait_limit_kilocycles ? (long long)wait_limit_kilocycles << 10 : kWaitLimitCycles;
+  FmChoice c = {};
+  const cudaError_t err = fm_choose(p, &c);
+  if (err != cudaSuccess) return err;
+  switch (c.bn) {
+    case 16: return launch_fm<16, 1>(p, c.split, xc, wc, st);
+    case 32: return launch_fm<32, 1>(p, c.split, xc, wc, st);
+    case 64: return launch_fm<64, 1>(p, c.split, xc, wc, st);
+    case 128: return launch_fm<128, 1>(p, c.split, xc, wc, st);
+  }
+  if (c.cg == 2) return launch_fm<256, 2>(p, 1, xc, wc, st);
+  return launch_fm<256, 1>(p, 1, xc, wc, st);
 }
 
 }  // namespace qmoe

@@ -344,14 +344,14 @@ def test_matmul_rows_before_the_first_expert_stay():
 
 
 @pytest.mark.parametrize("offsets", [[0, 5, 11], [-3, 5, 10], [0, 7, 2], [0, 2 ** 31 - 1, 10], [-2 ** 31, 2 ** 31 - 1, -2 ** 31]])
-def test_matmul_bad_offsets_are_cut_off_and_reported(offsets):
+def test_matmul_bad_offsets_are_reported(offsets):
     M, N, K = 10, 72, 128
     ops = [dev(a) for a in operands(M, N, K, 2, 3)]
     buf = torch.full((3, M, N), 7.0, device=DEV)
     st = torch.zeros(1, dtype=torch.int32, device=DEV)
     off = torch.tensor(offsets, dtype=torch.int32, device=DEV)
     B.qmoe_fp8_matmul(*ops, F32, offsets=off, out=buf[1], status=st)
-    assert int(st.item()) == 2 and (buf[::2] == 7).all()
+    assert int(st.item()) == 2 and (buf == 7).all()
     B.qmoe_fp8_matmul(*ops, F32, offsets=off, out=buf[1])
     assert B.qmoe_fp8_status() == (6, 2) and B.qmoe_fp8_status() == (0, 0)
     good = torch.tensor([0, 5, 10], dtype=torch.int32, device=DEV)
@@ -574,7 +574,8 @@ def test_large_offsets():
     wc, ws = B.qmoe_fp8_quantize_weights(make(64, H, 6, F16, 0.0).to(DEV))
     off = torch.tensor([T * k - 200, T * k], dtype=torch.int32, device=DEV)
     y = B.qmoe_fp8_matmul(codes, scales, wc[None], ws[None], F16, offsets=off)
-    assert torch.equal(y[-200:].view(50, 4, 64)[:, 0], B.qmoe_fp8_matmul(codes[-200::4].contiguous(), scales[-200::4].contiguous(), wc, ws, F16))
+    # (within the bound: how K is split, and so the order of the sums, goes by the number of rows)
+    check_product((codes[-200:].cpu().numpy(), scales[-200:].cpu().numpy(), wc.cpu().numpy()[None], ws.cpu().numpy()[None]), y[-200:], F16)
 
 
 # ---------------------------------------------------------------- the layer
