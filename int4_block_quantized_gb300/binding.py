@@ -789,8 +789,8 @@ def qmoe_fp8_matmul(x_codes, x_scales, w_codes, w_scales, dtype=torch.bfloat16, 
 
 
 def qmoe_fp8_matmul_variant(M, N, K, E=None):
-    """(tokens per tile, pairs of CTAs, CTAs along K) of the kernel that a product
-    of these sizes runs on the current device; E: grouped, over so many experts."""
+    """(tile, form, CTAs along K) of the kernel that a product of these sizes runs on
+    the current device, as qmoe.h has them; E: grouped, over so many experts."""
     v = (ctypes.c_int * 3)()
     _fp8_size(M, K, "qmoe_fp8_matmul_variant"), _fp8_size(N * (E or 1), K, "qmoe_fp8_matmul_variant")
     _check(lib().qmoe_fp8_matmul_variant(E is not None, 1 if E is None else E, M, N, K, v), "qmoe_fp8_matmul_variant")

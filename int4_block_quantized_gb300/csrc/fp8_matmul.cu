@@ -35,7 +35,7 @@ struct FmParams {
   void* y;
   uint32_t* status;
   int E, M, N, K, y_dtype;
-  int row_tiles;        // tiles of 128 CG weight rows of an expert
+  int row_tiles;        // tiles of an expert's weight rows
   int wide_out;         // y: 16 bits, rows on 16-byte boundaries
   int wide_scales;      // four of a row's scales on 16 bytes
   int split;            // CTAs of a cluster that share a tile's K
@@ -43,16 +43,16 @@ struct FmParams {
   long long wait_limit; // SM cycles
 };
 
-template <int BN, int CG>
+template <int BN>
 struct FmPlan {
-  static constexpr uint32_t kA = 128 * 128, kB = BN / CG * 128;  // one CTA's share of a block's codes
-  static constexpr int kBox = BN / CG < 64 ? BN / CG : 64;       // tokens of a copy
+  static constexpr uint32_t kA = 128 * 128, kB = BN * 128;  // a block's codes
+  static constexpr int kBox = BN < 64 ? BN : 64;                 // tokens of a copy
   // buffers of tensor memory for the blocks' sums
   static constexpr int kBufs = BN >= 64 ? 512 / BN : 8;
   // tokens that a warp reads at once, and how often: two warps per lane quadrant take turns
   static constexpr int kW = BN >= 64 ? 32 : BN / 2, kQ = BN / 2 / kW, kG = kW / 8;
   static constexpr uint32_t kOut = 8 * kW * 64;                  // 32 outputs of kW tokens a warp, turned round there
-  static constexpr int kQuads = BN == 256 ? 3 : 4;               // scales: slots of four blocks
+  static constexpr int kQuads = 4;                               // scales: slots of four blocks
   static constexpr uint32_t kScales = kQuads * 4 * BN * 4;
   // a split tile's partial sums [split][tokens of a CTA / 2][128][2]: a place of
   // their own where they are small, else the ring once the cluster is done with it
@@ -175,7 +175,7 @@ __device__ __forceinline__ void mma_f8(uint32_t e, uint32_t d, uint32_t a, uint3
 }
 #undef QMOE_MMA_F8
 
-// A tile: 128 CG weight rows of an expert from row rt, tokens m0 .. m1 - 1.
+// A tile: the expert, which of its tiles of weight rows, tokens m0 .. m1 - 1.
 struct FmTile {
   int e, rt, m0, m1;
 };
@@ -184,6 +184,41 @@ struct FmTable {
   int start[kMaxExperts], end[kMaxExperts];
 };
 static_assert(sizeof(FmTable) <= kFmTable, "table");
+
+// The experts' rows and token tiles of BN; no tiles where the offsets are no
+// offsets.  All threads of the CTA (at least as many as experts).
+template <int BN>
+__device__ __forceinline__ void fm_table(const FmParams& p, FmTable& tab, int* s_sum) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (!p.offsets) {
+    if (tid == 0) tab.first[0] = 0, tab.first[1] = (p.M + BN - 1) / BN, tab.start[0] = 0, tab.end[0] = p.M;
+  } else {
+    int sum = 0, bad = 0;
+    if (tid < p.E) {
+      const int a = p.offsets[tid], b = p.offsets[tid + 1];
+      bad = a < 0 || b < a || b > p.M;
+      tab.start[tid] = a;
+      tab.end[tid] = b;
+      sum = (int)(((long long)b - a + BN - 1) / BN);
+    }
+    bad = __syncthreads_or(bad);
+    if (bad) sum = 0;
+    if (bad && blockIdx.x == 0 && tid == 0) fm_status(p, QMOE_ST_INDEX);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += up;
+    }
+    if (warp < 8 && lane == 31) s_sum[warp] = sum;
+    __syncthreads();
+    if (tid < p.E) {
+      for (int w = 0; w < warp; ++w) sum += s_sum[w];
+      tab.first[tid + 1] = sum;
+      if (tid == 0) tab.first[0] = 0;
+    }
+  }
+  __syncthreads();
+}
 
 // Tile t: by expert, within it in groups of 8 row tiles, so that the tiles in
 // flight share weights and tokens in L2.
@@ -207,11 +242,11 @@ __device__ __forceinline__ FmTile fm_tile(const FmParams& p, const FmTable& tab,
   return f;
 }
 
-template <int BN, int CG>
+template <int BN>
 __global__ void __launch_bounds__(kFmThreads, 1)
     fp8_matmul_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                       const FmParams p) {
-  using P = FmPlan<BN, CG>;
+  using P = FmPlan<BN>;
   constexpr int S = P::kStages, NB = P::kBufs, SQ = P::kQuads;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -241,7 +276,7 @@ __global__ void __launch_bounds__(kFmThreads, 1)
     }
     for (int b = 0; b < NB; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_free[b], 8 * CG);
+      mbar_init(&acc_free[b], 8);
     }
     for (int b = 0; b < SQ; ++b) {
       mbar_init(&sc_full[b], 2);
@@ -253,17 +288,11 @@ __global__ void __launch_bounds__(kFmThreads, 1)
     fence_barrier_init();
   }
   if (warp == 1) {
-    if (CG == 1) {
-      tmem_alloc(s_tmem, 512);
-      tmem_relinquish();
-    } else {
-      tmem_alloc2(s_tmem, 512);
-      tmem_relinquish2();
-    }
+    tmem_alloc(s_tmem, 512);
+    tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
-  if (CG == 2) cluster_sync_all();  // the pair's barriers are set up
   tc_fence_after();
   // all 512 columns are this CTA's, so they start at 0
   constexpr uint32_t tmem = 0;
@@ -271,41 +300,12 @@ __global__ void __launch_bounds__(kFmThreads, 1)
   pdl_wait();
   pdl_trigger();
 
-  // the experts' rows and token tiles; none where the offsets are no offsets
-  if (!p.offsets) {
-    if (tid == 0) tab.first[0] = 0, tab.first[1] = (p.M + BN - 1) / BN, tab.start[0] = 0, tab.end[0] = p.M;
-  } else {
-    int sum = 0, bad = 0;
-    if (tid < p.E) {
-      const int a = p.offsets[tid], b = p.offsets[tid + 1];
-      bad = a < 0 || b < a || b > p.M;
-      tab.start[tid] = a;
-      tab.end[tid] = b;
-      sum = (int)(((long long)b - a + BN - 1) / BN);
-    }
-    bad = __syncthreads_or(bad);
-    if (bad) sum = 0;
-    if (bad && blockIdx.x == 0 && tid == 0) fm_status(p, QMOE_ST_INDEX);
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int up = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += up;
-    }
-    if (warp < 8 && lane == 31) s_sum[warp] = sum;
-    __syncthreads();
-    if (tid < p.E) {
-      for (int w = 0; w < warp; ++w) sum += s_sum[w];
-      tab.first[tid + 1] = sum;
-      if (tid == 0) tab.first[0] = 0;
-    }
-  }
-  __syncthreads();
+  fm_table<BN>(p, tab, s_sum);
 
   // this CTA's tiles and its share [c0, c1) of their blocks along K
   const int rank = p.split > 1 ? (int)cluster_ctarank() : 0;
-  const int half = CG == 2 ? (int)cluster_ctarank() : 0;  // of the pair's rows and tokens
   const int tiles = tab.first[p.E] * p.row_tiles;
-  const int first = blockIdx.x / (CG * p.split), step = p.split > 1 ? max(tiles, (int)gridDim.x) : gridDim.x / CG;
+  const int first = blockIdx.x / p.split, step = p.split > 1 ? max(tiles, (int)gridDim.x) : gridDim.x;
   const int nb = (p.K + 127) / 128;
   auto stalled = [&](uint32_t role) { return (p.stall & role) && !fm_wait(never, 0, p, s_abort); };
   const int c0 = (int)((long long)nb * rank / p.split), c1 = (int)((long long)nb * (rank + 1) / p.split);
@@ -319,26 +319,17 @@ __global__ void __launch_bounds__(kFmThreads, 1)
     const uint32_t el = elect_lane();
     for (int t = first; t < tiles && ok; t += step) {
       const FmTile f = fm_tile<BN>(p, tab, t);
-      const int row = f.e * p.N + (f.rt * CG + half) * 128;
-      // copies of kBox tokens, as many as the tile has (a pair: always all)
-      const int boxes = CG == 2 ? BN / CG / P::kBox : (f.m1 - f.m0 + P::kBox - 1) / P::kBox;
+      const int row = f.e * p.N + f.rt * 128;
+      const int boxes = (f.m1 - f.m0 + P::kBox - 1) / P::kBox;  // copies, as many as the tile has tokens
       for (int c = c0; c < c1; ++c, ++it) {
         if (it >= S) ok = fm_wait(&empty[s], ph ^ 1u, p, s_abort);
         if (!ok) break;
         if (el) {
           uint8_t* st = ring + s * P::kStage;
-          if constexpr (CG == 2) {  // both CTAs report to the leader
-            const uint32_t bar = peer_u32(&full[s], 0);
-            if (half == 0) mbar_arrive_expect_tx(&full[s], 2 * (P::kA + P::kB));
-            tma_load_2d_pair(st, &tm_w, c * 128, row, bar);
-            for (int i = 0; i < boxes; ++i)
-              tma_load_2d_pair(st + P::kA + i * P::kBox * 128, &tm_x, c * 128, f.m0 + half * (BN / 2) + i * P::kBox, bar);
-          } else {
-            mbar_arrive_expect_tx(&full[s], P::kA + boxes * P::kBox * 128);
-            tma_load_2d(st, &tm_w, c * 128, row, &full[s]);
-            for (int i = 0; i < boxes; ++i)
-              tma_load_2d(st + P::kA + i * P::kBox * 128, &tm_x, c * 128, f.m0 + i * P::kBox, &full[s]);
-          }
+          mbar_arrive_expect_tx(&full[s], P::kA + boxes * P::kBox * 128);
+          tma_load_2d(st, &tm_w, c * 128, row, &full[s]);
+          for (int i = 0; i < boxes; ++i)
+            tma_load_2d(st + P::kA + i * P::kBox * 128, &tm_x, c * 128, f.m0 + i * P::kBox, &full[s]);
         }
         __syncwarp();
         if (++s == S) {
@@ -347,10 +338,8 @@ __global__ void __launch_bounds__(kFmThreads, 1)
         }
       }
     }
-    // A pair's stages are counted in the leader alone, but both CTAs see the
-    // commits that give slots back (and stay until these have arrived).
-    if (lane == 0) fm_settle<S>(CG == 1 ? full : empty, it, p, s_abort);
-  } else if (warp == 1 && half == 0) {
+    if (lane == 0) fm_settle<S>(full, it, p, s_abort);
+  } else if (warp == 1) {
     // ------------------------------------------------------------- MMAs
     int n = 0, s = 0;  // blocks so far
     uint32_t ph = 0;
@@ -358,9 +347,9 @@ __global__ void __launch_bounds__(kFmThreads, 1)
     const uint32_t el = elect_lane();
     for (int t = first; t < tiles && ok; t += step) {
       const FmTile f = fm_tile<BN>(p, tab, t);
-      const int cols = CG == 2 ? BN : (f.m1 - f.m0 + 15) & ~15;
+      const int cols = (f.m1 - f.m0 + 15) & ~15;
       // D fp32, A and B e4m3, both K-major
-      const uint32_t idesc = 1u << 4 | (uint32_t)(cols >> 3) << 17 | (uint32_t)(128 * CG >> 4) << 24;
+      const uint32_t idesc = 1u << 4 | (uint32_t)(cols >> 3) << 17 | (uint32_t)(128 >> 4) << 24;
       for (int c = c0; c < c1; ++c, ++n) {
         const int b = n % NB;
         if (n >= NB) ok = fm_wait<false>(&acc_free[b], (n / NB - 1) & 1, p, s_abort);
@@ -373,10 +362,10 @@ __global__ void __launch_bounds__(kFmThreads, 1)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           if (32 * j >= left) break;
-          mma_f8<CG>(el, tmem + b * BN, da + 2 * j, db + 2 * j, idesc, j > 0);
+          mma_f8<1>(el, tmem + b * BN, da + 2 * j, db + 2 * j, idesc, j > 0);
         }
-        mma_commit_mx<CG>(el, &empty[s]);
-        mma_commit_mx<CG>(el, &acc_full[b]);
+        mma_commit_mx<1>(el, &empty[s]);
+        mma_commit_mx<1>(el, &acc_full[b]);
         issued = true;
         if (++s == S) {
           s = 0;
@@ -385,8 +374,7 @@ __global__ void __launch_bounds__(kFmThreads, 1)
       }
     }
     if (issued) {  // all MMAs have finished before tensor memory is freed
-      if (CG == 1) mma_commit_mx<1>(el, fin);
-      else mma_commit_mx2_own(el, fin);  // a commit to the peer's barrier too could arrive there when it has left
+      mma_commit_mx<1>(el, fin);
       if (el) mbar_wait(fin, 0, nullptr);
     }
   } else if (warp == 2 || warp == 3) {
@@ -396,7 +384,7 @@ __global__ void __launch_bounds__(kFmThreads, 1)
     bool ok = !stalled(QMOE_DIAG_STALL_FP8_SCALES);
     for (int t = first; t < tiles && ok; t += step) {
       const FmTile f = fm_tile<BN>(p, tab, t);
-      const int rt = f.rt * CG + half;
+      const int rt = f.rt;
       const float* ws = p.ws + ((size_t)f.e * rb + rt) * nb;
       for (int c = c0; c < c1; c += 4, ++it) {
         const int q = it % SQ;
@@ -466,14 +454,13 @@ __global__ void __launch_bounds__(kFmThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          if (CG == 1) mbar_arrive(&acc_free[b]);
-          else mbar_arrive_cluster(peer_u32(&acc_free[b], 0));
+          mbar_arrive(&acc_free[b]);
           if (sub == 3 || c + 1 == c1) mbar_arrive(&sc_free[slot]);
         }
         if (sub == 3 || c + 1 == c1) ++it;
       }
       if (!ok || p.split > 1) break;
-      const int n0 = (f.rt * CG + half) * 128 + qd * 32;
+      const int n0 = f.rt * 128 + qd * 32;
 #pragma unroll
       for (int q = 0; q < P::kQ; ++q) {
         const int col = (2 * q + set) * P::kW, m = f.m0 + col;
@@ -555,6 +542,373 @@ __global__ void __launch_bounds__(kFmThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+
+// ------------------------------------------------------------- many tokens
+// Here 128 tokens are the MMA's M operand and BN weight rows its N: a thread of
+// the warps that add has a token to itself, so that a block's scale is one number
+// to it, and reads tensor memory in whole rows (32x32b, measured at 18 cycles for
+// 32 columns of a warp; fragments take 32).  Two warps to each lane quadrant, a
+// half of the columns each.  Warp 0 copies codes, 1 issues MMAs, 2 prepares
+// scales, 3 to 10 add and write y.
+constexpr int kFwThreads = 384;
+// 256 outputs: the adding warps hold 128 sums a thread and take registers of the
+// others: 256 x 208 + 128 x 88 = 384 x 168, which the launch has (checked there).
+constexpr int kFwRegs = 168, kFwManyRegs = 208, kFwFewRegs = 88;
+static_assert(256 * kFwManyRegs + 128 * kFwFewRegs <= kFwThreads * kFwRegs, "registers");
+
+template <int BN, int CG>
+struct FwPlan {
+  static constexpr uint32_t kA = 128 * 128, kB = BN / CG * 128, kStage = kA + kB;  // one CTA's share of a block's codes
+  static constexpr int kBufs = 512 / BN;
+  static constexpr int kHalves = BN / 128;                        // scale blocks of a tile's weight rows
+  static constexpr int kC = BN / 2 / 16;                          // a warp's columns, 16 at a time
+  static constexpr int kQuads = 2;                                // scales: slots of four blocks
+  static constexpr uint32_t kScales = kQuads * 4 * kHalves * 512;
+  static constexpr uint32_t kOut = 8 * 32 * 17 * 4;               // rows of y that are not written in wide words
+  static constexpr uint32_t kAt = (kFmBars + kFmTable + kScales + kOut + 1023) & ~1023u;
+  static constexpr int kStages = (int)((kFmSmem - 1024 - kAt) / kStage);
+};
+
+__device__ __forceinline__ void fw_load(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+// waits for the loads so far; the registers pass through, so that no use of
+// theirs is scheduled before
+__device__ __forceinline__ void fw_wait(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+
+// Arrives on a barrier of the other CTA (its shared::cluster address).  Relaxed:
+// what it tells is that loads into registers are done, no memory is handed over
+// (a release there waits for this thread's writes of y, too).
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+template <int BN, int CG>
+__global__ void __launch_bounds__(kFwThreads, 1)
+    fp8_wide_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x, const FmParams p) {
+  using P = FwPlan<BN, CG>;
+  constexpr int BT = 128 * CG;  // tokens of a tile
+  constexpr int S = P::kStages, NB = P::kBufs, SQ = P::kQuads;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem);
+  uint64_t* empty = full + S;
+  uint64_t* acc_full = empty + S;      // [NB]
+  uint64_t* acc_free = acc_full + NB;  // [NB]
+  uint64_t* sc_full = acc_free + NB;   // [SQ]
+  uint64_t* sc_free = sc_full + SQ;    // [SQ]
+  uint64_t* fin = sc_free + SQ;
+  uint64_t* never = fin + 1;  // nothing arrives here (p.stall)
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(never + 1);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+  int* s_sum = reinterpret_cast<int*>(s_tmem + 2);  // [8]
+  FmTable& tab = *reinterpret_cast<FmTable*>(smem + kFmBars);
+  float* scales = reinterpret_cast<float*>(smem + kFmBars + kFmTable);
+  uint8_t* outbuf = smem + kFmBars + kFmTable + P::kScales;
+  uint8_t* ring = smem + P::kAt;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be the same in all lanes
+
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < NB; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_free[b], 8 * CG);
+    }
+    for (int b = 0; b < SQ; ++b) {
+      mbar_init(&sc_full[b], 1);
+      mbar_init(&sc_free[b], 8);
+    }
+    mbar_init(fin, 1);
+    mbar_init(never, 1);
+    *s_abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    if (CG == 1) {
+      tmem_alloc(s_tmem, 512);
+      tmem_relinquish();
+    } else {
+      tmem_alloc2(s_tmem, 512);
+      tmem_relinquish2();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (CG == 2) cluster_sync_all();  // the pair's barriers are set up
+  tc_fence_after();
+  constexpr uint32_t tmem = 0;  // all 512 columns are this CTA's
+  pdl_wait();
+  pdl_trigger();
+  fm_table<BT>(p, tab, s_sum);
+
+  const int tiles = tab.first[p.E] * p.row_tiles, nb = (p.K + 127) / 128;
+  const int half = CG == 2 ? (int)cluster_ctarank() : 0;  // of the pair's tokens
+  const int first = blockIdx.x / CG, step = gridDim.x / CG;
+  auto stalled = [&](uint32_t role) { return (p.stall & role) && !fm_wait(never, 0, p, s_abort); };
+  if (warp >= 4) {
+    if (BN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFwManyRegs));
+    // ------------------------------------- the blocks' sums, scaled and added
+    const int qd = warp & 3, set = warp >= 8;
+    float* buf = reinterpret_cast<float*>(outbuf) + (warp - 4) * 32 * 17;
+    int n = 0, it = 0;
+    bool ok = !stalled(QMOE_DIAG_STALL_FP8_OUTPUT);
+    for (int t = first; t < tiles && ok; t += step) {
+      const FmTile f = fm_tile<BT>(p, tab, t);
+      const int n0 = f.rt * BN + set * (BN / 2), cols = p.N - n0;  // this warp's columns
+      const int m0 = f.m0 + half * 128 + qd * 32;                  // and tokens
+      const bool live = cols > 0 && m0 < f.m1;
+      float acc[P::kC][16];
+#pragma unroll
+      for (int q = 0; q < P::kC; ++q)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) acc[q][j] = 0.f;
+      // `ready`: what is waited for next had come when this was last looked at,
+      // which is under the last sums of the block before, so that the answer's
+      // latency costs nothing
+      bool ready = false;
+      for (int c = 0; c < nb; ++c, ++n) {
+        const int b = n % NB, sub = c & 3, slot = it % SQ;
+        if (!__all_sync(0xffffffffu, ready)) {
+          if (sub == 0) ok = fm_wait(&sc_full[slot], (it / SQ) & 1, p, s_abort);
+          if (ok) ok = fm_wait(&acc_full[b], (n / NB) & 1, p, s_abort);
+          if (!ok) break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + ((uint32_t)(qd * 32) << 16) + b * BN + set * (BN / 2);
+        uint32_t v[2][16];
+        if (live) fw_load(d, v[0]);
+        const float s = scales[((slot * 4 + sub) * P::kHalves + (P::kHalves > 1 ? set : 0)) * 128 + qd * 32 + lane];
+        auto freed = [&]() {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (half == 0) mbar_arrive(&acc_free[b]);
+            else mbar_arrive_remote(peer_u32(&acc_free[b], 0));
+          }
+          if (sub == 3) ++it;
+          ready = c + 1 < nb && mbar_try_wait(&acc_full[(n + 1) % NB], ((n + 1) / NB) & 1) &&
+                  (sub != 3 || mbar_try_wait(&sc_full[it % SQ], (it / SQ) & 1));
+        };
+        if (live) {
+#pragma unroll
+          for (int q = 0; q < P::kC; ++q) {
+            fw_wait(v[q & 1]);
+            if (q + 1 < P::kC) fw_load(d + 16 * (q + 1), v[(q + 1) & 1]);
+            else freed();  // the last sums are still to come, but the buffer has been read
+#pragma unroll
+            for (int j = 0; j < 16; ++j) acc[q][j] = fmaf(__uint_as_float(v[q & 1][j]), s, acc[q][j]);
+          }
+        } else {
+          freed();
+        }
+        if ((sub == 3 || c + 1 == nb) && lane == 0) mbar_arrive(&sc_free[slot]);
+      }
+      if (nb & 3) ++it;
+      if (!ok) break;
+      if (!live) continue;
+      if (p.wide_out) {
+        // 32 tokens x 64 bytes at a time through shared memory (the four 16-byte
+        // pieces of a row permuted against bank conflicts), so that four lanes
+        // write 64 bytes of a row: a row to each lane takes 32 cycles a store
+        uint8_t* row = reinterpret_cast<uint8_t*>(buf) + lane * 64;
+        const int w32 = p.y_dtype == QMOE_F32, x = lane >> 1 & 3;
+        auto out = [&](int col, int per) {  // columns col .. + 64 bytes, `per` of them to 16 bytes
+          __syncwarp();
+          const int piece = lane & 3;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = 8 * i + (lane >> 2);
+            const uint4 v = *reinterpret_cast<const uint4*>(reinterpret_cast<uint8_t*>(buf) + r * 64 + ((piece ^ (r >> 1 & 3)) << 4));
+            if (m0 + r < f.m1 && col + piece * per < cols)
+              *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.y) + ((size_t)(m0 + r) * p.N + n0 + col + piece * per) * (w32 ? 4 : 2)) = v;
+          }
+          __syncwarp();
+        };
+        if (w32) {
+#pragma unroll
+          for (int q = 0; q < P::kC; ++q)
+            if (16 * q < cols) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<float4*>(row + ((j ^ x) << 4)) = make_float4(acc[q][4 * j], acc[q][4 * j + 1], acc[q][4 * j + 2], acc[q][4 * j + 3]);
+              out(16 * q, 4);
+            }
+        } else {
+#pragma unroll
+          for (int q = 0; q < P::kC; q += 2)
+            if (16 * q < cols) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float* a = acc[q + j / 2] + 8 * (j & 1);
+                *reinterpret_cast<uint4*>(row + ((j ^ x) << 4)) =
+                    make_uint4(fm_pack(p, make_float2(a[0], a[1])), fm_pack(p, make_float2(a[2], a[3])),
+                               fm_pack(p, make_float2(a[4], a[5])), fm_pack(p, make_float2(a[6], a[7])));
+              }
+              out(16 * q, 8);
+            }
+        }
+      } else {
+        // 32 tokens x 16 columns at a time through shared memory, so that
+        // neighbouring lanes write neighbouring columns
+#pragma unroll
+        for (int q = 0; q < P::kC; ++q) {
+          if (16 * q < cols) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) buf[lane * 17 + j] = acc[q][j];
+            __syncwarp();
+            const int col = lane & 15;
+            for (int r = lane >> 4; r < 32; r += 2)
+              if (m0 + r < f.m1 && 16 * q + col < cols)
+                fm_store(p, (size_t)(m0 + r) * p.N + n0 + 16 * q + col, buf[r * 17 + col]);
+            __syncwarp();
+          }
+        }
+      }
+    }
+  } else {
+    if (BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFwFewRegs));
+    if (warp == 0) {
+      // ------------------------------------------------------------ codes
+      int it = 0, s = 0;
+      uint32_t ph = 0;
+      bool ok = !stalled(QMOE_DIAG_STALL_FP8_CODES);
+      const uint32_t el = elect_lane();
+      for (int t = first; t < tiles && ok; t += step) {
+        const FmTile f = fm_tile<BT>(p, tab, t);
+        // copies of 64 rows: of this CTA's tokens, of all of them, of weights
+        const int n = f.m1 - f.m0, xb = min(max((n - half * 128 + 63) / 64, 0), 2), all = (n + 63) / 64;
+        const int wb = CG == 2 ? BN / 2 / 64 : (min(BN, p.N - f.rt * BN) + 63) / 64;
+        const int m0 = f.m0 + half * 128, row = f.e * p.N + f.rt * BN + half * (BN / 2);
+        for (int c = 0; c < nb; ++c, ++it) {
+          if (it >= S) ok = fm_wait(&empty[s], ph ^ 1u, p, s_abort);
+          if (!ok) break;
+          if (el) {
+            uint8_t* st = ring + s * P::kStage;
+            if constexpr (CG == 2) {  // both CTAs report to the leader
+              const uint32_t bar = peer_u32(&full[s], 0);
+              if (half == 0) mbar_arrive_expect_tx(&full[s], (all + 2 * wb) * 64 * 128);
+              for (int i = 0; i < xb; ++i) tma_load_2d_pair(st + i * 8192, &tm_x, c * 128, m0 + 64 * i, bar);
+              for (int i = 0; i < wb; ++i) tma_load_2d_pair(st + P::kA + i * 8192, &tm_w, c * 128, row + 64 * i, bar);
+            } else {
+              mbar_arrive_expect_tx(&full[s], (xb + wb) * 64 * 128);
+              for (int i = 0; i < xb; ++i) tma_load_2d(st + i * 8192, &tm_x, c * 128, m0 + 64 * i, &full[s]);
+              for (int i = 0; i < wb; ++i) tma_load_2d(st + P::kA + i * 8192, &tm_w, c * 128, row + 64 * i, &full[s]);
+            }
+          }
+          __syncwarp();
+          if (++s == S) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      // A pair's stages are counted in the leader alone, but both CTAs see the
+      // commits that give slots back (and stay until these have arrived).
+      if (lane == 0) fm_settle<S>(CG == 1 ? full : empty, it, p, s_abort);
+    } else if (warp == 1 && half == 0) {  // a pair: the leader issues for both
+      // ------------------------------------------------------------- MMAs
+      int n = 0, s = 0;  // blocks so far
+      uint32_t ph = 0;
+      bool ok = !stalled(QMOE_DIAG_STALL_FP8_MMA), issued = false;
+      const uint32_t el = elect_lane();
+      for (int t = first; t < tiles && ok; t += step) {
+        const FmTile f = fm_tile<BT>(p, tab, t);
+        const int cols = CG == 2 ? BN : (min(BN, p.N - f.rt * BN) + 15) & ~15;
+        const uint32_t idesc = 1u << 4 | (uint32_t)(cols >> 3) << 17 | (uint32_t)(BT >> 4) << 24;
+        for (int c = 0; c < nb; ++c, ++n) {
+          const int b = n % NB;
+          ok = fm_wait<false>(&full[s], ph, p, s_abort);
+          if (ok && n >= NB) ok = fm_wait<false>(&acc_free[b], (n / NB - 1) & 1, p, s_abort);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t st = (smem_u32(ring + s * P::kStage) >> 4) & 0x3FFFu;  // a descriptor's address field
+          const uint32_t da = st | 1u << 16, db = (st + (P::kA >> 4)) | 1u << 16;
+          const int left = p.K - c * 128;
+  #pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (32 * j >= left) break;
+            mma_f8<CG>(el, tmem + b * BN, da + 2 * j, db + 2 * j, idesc, j > 0);
+          }
+          mma_commit_mx<CG>(el, &empty[s]);
+          mma_commit_mx<CG>(el, &acc_full[b]);
+          issued = true;
+          if (++s == S) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      if (issued) {  // all MMAs have finished before tensor memory is freed
+        if (CG == 1) mma_commit_mx<1>(el, fin);
+        else mma_commit_mx2_own(el, fin);  // a commit to the peer's barrier too could arrive there when it has left
+        if (el) mbar_wait(fin, 0, nullptr);
+      }
+    } else if (warp == 2) {
+      // ------------ scales of 128 tokens by kHalves weight blocks, four k blocks at a time
+      int it = 0;
+      const int rb = (p.N + 127) / 128;
+      bool ok = !stalled(QMOE_DIAG_STALL_FP8_SCALES);
+      for (int t = first; t < tiles && ok; t += step) {
+        const FmTile f = fm_tile<BT>(p, tab, t);
+        const float* ws = p.ws + ((size_t)f.e * rb + f.rt * P::kHalves) * nb;
+        for (int c = 0; c < nb; c += 4, ++it) {
+          const int q = it % SQ;
+          float v[4][4] = {}, w[P::kHalves][4];
+  #pragma unroll
+          for (int h = 0; h < P::kHalves; ++h)
+  #pragma unroll
+            for (int j = 0; j < 4; ++j) w[h][j] = f.rt * P::kHalves + h < rb && c + j < nb ? ws[h * nb + c + j] : 0.f;
+  #pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (f.m0 + half * 128 + 32 * i + lane < f.m1) {
+              const float* xs = p.xs + (size_t)(f.m0 + half * 128 + 32 * i + lane) * nb + c;
+              if (p.wide_scales) {
+                const float4 u = *reinterpret_cast<const float4*>(xs);
+                v[i][0] = u.x, v[i][1] = u.y, v[i][2] = u.z, v[i][3] = u.w;
+              } else {
+  #pragma unroll
+                for (int j = 0; j < 4; ++j) v[i][j] = c + j < nb ? xs[j] : 0.f;
+              }
+            }
+          if (it >= SQ) ok = fm_wait(&sc_free[q], (it / SQ - 1) & 1, p, s_abort);
+          if (!ok) break;
+          float* out = scales + q * 4 * P::kHalves * 128;
+  #pragma unroll
+          for (int j = 0; j < 4; ++j)
+  #pragma unroll
+            for (int h = 0; h < P::kHalves; ++h)
+  #pragma unroll
+              for (int i = 0; i < 4; ++i) out[(j * P::kHalves + h) * 128 + 32 * i + lane] = v[i][j] * w[h][j];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sc_full[q]);
+        }
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
   if (CG == 2) cluster_sync_all();  // neither CTA leaves while the other may use its memory
   if (warp == 1) {
     tc_fence_after();
@@ -570,13 +924,13 @@ static long long fm_token_tiles(const FmParams& p, int bn) {
   return most < p.M ? most : p.M;
 }
 
-template <int BN, int CG>
+template <int BN>
 static cudaError_t launch_fm(FmParams p, int split, const uint8_t* xc, const uint8_t* wc, cudaStream_t st) {
-  using P = FmPlan<BN, CG>;
+  using P = FmPlan<BN>;
   static_assert(P::kStages >= 3 && P::kBufs * BN <= 512, "plan");
   static_assert((2 * P::kStages + 2 * P::kBufs + 2 * P::kQuads + 2) * 8 + 40 <= kFmBars, "barriers");
   p.split = split;
-  p.row_tiles = (p.N + 128 * CG - 1) / (128 * CG);
+  p.row_tiles = (p.N + 127) / 128;
   const long long tiles = fm_token_tiles(p, BN) * p.row_tiles;
   if (tiles > (1LL << 27)) return cudaErrorInvalidValue;
   CUtensorMap tw, tx;
@@ -588,14 +942,14 @@ static cudaError_t launch_fm(FmParams p, int split, const uint8_t* xc, const uin
   p.wide_out = p.y_dtype != QMOE_F32 && p.N % 8 == 0 && !(reinterpret_cast<uintptr_t>(p.y) & 15);
   p.wide_scales = split == 1 && p.K % 512 == 0 && !(reinterpret_cast<uintptr_t>(p.xs) & 15);
   const int sms = device_sm_count();
-  auto kernel = fp8_matmul_kernel<BN, CG>;
+  auto kernel = fp8_matmul_kernel<BN>;
   // All of the SM's shared memory, used or not: the CTA takes all of its tensor
   // memory, and a CTA of another kernel that waits for some (or has some) must
   // not share the SM: two clusters could then wait for one another.
   cudaError_t err = ensure_smem(kernel, kFmSmem);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.split > 1 ? tiles * p.split : CG * (tiles < sms / CG ? tiles : sms / CG)));
+  cfg.gridDim = dim3((unsigned)(p.split > 1 ? tiles * p.split : tiles < sms ? tiles : sms));
   cfg.blockDim = dim3(kFmThreads);
   cfg.dynamicSmemBytes = kFmSmem;
   cfg.stream = st;
@@ -603,7 +957,54 @@ static cudaError_t launch_fm(FmParams p, int split, const uint8_t* xc, const uin
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = p.split * CG;
+  attr[1].val.clusterDim.x = p.split;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, tw, tx, p);
+}
+
+template <int BN, int CG>
+static cudaError_t launch_fw(FmParams p, const uint8_t* xc, const uint8_t* wc, cudaStream_t st) {
+  using P = FwPlan<BN, CG>;
+  static_assert(P::kStages >= 3, "plan");
+  static_assert((2 * P::kStages + 2 * P::kBufs + 2 * P::kQuads + 2) * 8 + 40 <= kFmBars, "barriers");
+  p.split = 1;
+  p.row_tiles = (p.N + BN - 1) / BN;
+  const long long tiles = fm_token_tiles(p, 128 * CG) * p.row_tiles;
+  if (tiles > (1LL << 27)) return cudaErrorInvalidValue;
+  CUtensorMap tw, tx;
+  if (!make_map(&tw, wc, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.K, (uint64_t)p.E * p.N, 128, 64, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B) ||
+      !make_map(&tx, xc, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.K, p.M, 128, 64, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
+    return cudaErrorNotSupported;
+  p.wide_out = p.N % (p.y_dtype == QMOE_F32 ? 4 : 8) == 0 && !(reinterpret_cast<uintptr_t>(p.y) & 15);
+  p.wide_scales = p.K % 512 == 0 && !(reinterpret_cast<uintptr_t>(p.xs) & 15);
+  const int sms = device_sm_count();
+  auto kernel = fp8_wide_kernel<BN, CG>;
+  const cudaError_t err = ensure_smem(kernel, kFmSmem);  // all of it, as above
+  if (err != cudaSuccess) return err;
+  if (BN == 256) {  // the warps' shares of the registers wait for what the launch does not have
+    static int regs = 0;
+    if (!regs) {
+      cudaFuncAttributes a;
+      const cudaError_t e = cudaFuncGetAttributes(&a, kernel);
+      if (e != cudaSuccess) return e;
+      regs = a.numRegs;
+    }
+    if (regs < kFwRegs) return cudaErrorInvalidDeviceFunction;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(CG * (tiles < sms / CG ? tiles : sms / CG)));
+  cfg.blockDim = dim3(kFwThreads);
+  cfg.dynamicSmemBytes = kFmSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CG;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
@@ -621,7 +1022,7 @@ static cudaError_t fm_capacity(int split, int* ctas) {
   if (err != cudaSuccess) return err;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!cached[dev][l]) {
-    auto kernel = fp8_matmul_kernel<16, 1>;
+    auto kernel = fp8_matmul_kernel<16>;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(split);
     cfg.blockDim = dim3(kFmThreads);
@@ -642,15 +1043,18 @@ static cudaError_t fm_capacity(int split, int* ctas) {
   return cudaSuccess;
 }
 
+// wide 0: bn tokens a tile, 128 weight rows; 1: 128 tokens, bn weight rows; 2: the
+// same by pairs of CTAs.
 struct FmChoice {
-  int bn, cg, split;
+  int bn, wide, split;
 };
 static cudaError_t fm_choose(const FmParams& p, FmChoice* choice) {
   static const struct {
-    int bn, cg, start, stage, tile, epilogue, exchange;
-  } kinds[] = {{16, 1, 1900, 170, 300, 200, 1200},   {32, 1, 2000, 170, 350, 300, 1300},
-               {64, 1, 2900, 165, 500, 850, 1400},   {128, 1, 3600, 185, 1200, 1350, 2900},
-               {256, 1, 3900, 300, 800, 1900, 0},    {256, 2, 4600, 300, 1250, 2700, 0}};
+    int bn, wide, start, stage, tile, epilogue, exchange;
+  } kinds[] = {{16, 0, 3300, 150, 300, 200, 400},  {32, 0, 4000, 150, 350, 300, 1000},
+               {64, 0, 4700, 200, 500, 850, 1300}, {128, 0, 5200, 300, 1200, 1350, 2000},
+               {128, 1, 4000, 285, 1000, 0, 0},    {256, 1, 4300, 460, 1500, 0, 0},
+               {256, 2, 4800, 460, 1300, 0, 0}};
   int capacity[9] = {};
   for (int split = 2; split <= 8; split *= 2) {
     const cudaError_t err = fm_capacity(split, &capacity[split]);
@@ -660,19 +1064,22 @@ static cudaError_t fm_choose(const FmParams& p, FmChoice* choice) {
   const long long active = p.offsets ? (p.E < p.M ? p.E : p.M) : 1, each = (p.M + active - 1) / active;
   long long least = -1;
   for (const auto& k : kinds) {
-    if (k.bn < 64 && each > k.bn) continue;
-    const long long rows = (p.N + 128 * k.cg - 1) / (128 * k.cg);
-    const long long tiles = rows * active * ((each + k.bn - 1) / k.bn);
+    if (!k.wide && k.bn < 64 && each > k.bn) continue;
+    const int bt = k.wide ? 128 * k.wide : k.bn, br = k.wide ? k.bn : 128;
+    const long long rows = (p.N + br - 1) / br;
+    // an expert's last tile is half full on average
+    const long long some = p.offsets ? p.M / bt + active / 2 : (p.M + bt - 1) / bt;
+    const long long tiles = rows * (some > active ? some : active);
     for (int split = 1; split <= 8; split *= 2) {
       if (split > 1 && (!k.exchange || split > nb || rows * fm_token_tiles(p, k.bn) * split > capacity[split])) break;
-      const long long slots = split > 1 ? tiles : device_sm_count() / k.cg;
+      const long long slots = split > 1 ? tiles : k.wide == 2 ? device_sm_count() / 2 : device_sm_count();
       const long long rounds = (tiles + slots - 1) / slots;
       const long long one = (long long)((nb + split - 1) / split) * k.stage, more = one + k.tile;
       const long long t = k.start + one + (rounds - 1) * (more > k.epilogue ? more : k.epilogue) +
                           (split > 1 ? k.exchange : 0);
       if (least < 0 || t < least) {
         least = t;
-        *choice = {k.bn, k.cg, split};
+        *choice = {k.bn, k.wide, split};
       }
     }
   }
@@ -693,13 +1100,13 @@ static FmParams fm_params(const float* xs, const float* ws, const int32_t* offse
   return p;
 }
 
-cudaError_t fp8_matmul_variant(bool grouped, int E, int M, int N, int K, int* tokens, int* pair, int* split) {
+cudaError_t fp8_matmul_variant(bool grouped, int E, int M, int N, int K, int* tile, int* wide, int* split) {
   static const int32_t some = 0;  // looked at for being given alone
   const FmParams p = fm_params(nullptr, nullptr, grouped ? &some : nullptr, E, M, N, K);
   FmChoice c = {};
   const cudaError_t err = fm_choose(p, &c);
-  *tokens = c.bn;
-  *pair = c.cg == 2;
+  *tile = c.bn;
+  *wide = c.wide;
   *split = c.split;
   return err;
 }
@@ -716,14 +1123,12 @@ cudaError_t launch_fp8_matmul(const uint8_t* xc, const float* xs, const uint8_t*
   FmChoice c = {};
   const cudaError_t err = fm_choose(p, &c);
   if (err != cudaSuccess) return err;
-  switch (c.bn) {
-    case 16: return launch_fm<16, 1>(p, c.split, xc, wc, st);
-    case 32: return launch_fm<32, 1>(p, c.split, xc, wc, st);
-    case 64: return launch_fm<64, 1>(p, c.split, xc, wc, st);
-    case 128: return launch_fm<128, 1>(p, c.split, xc, wc, st);
-  }
-  if (c.cg == 2) return launch_fm<256, 2>(p, 1, xc, wc, st);
-  return launch_fm<256, 1>(p, 1, xc, wc, st);
+  if (c.wide == 2) return launch_fw<256, 2>(p, xc, wc, st);
+  if (c.wide) return c.bn == 256 ? launch_fw<256, 1>(p, xc, wc, st) : launch_fw<128, 1>(p, xc, wc, st);
+  if (c.bn == 16) return launch_fm<16>(p, c.split, xc, wc, st);
+  if (c.bn == 32) return launch_fm<32>(p, c.split, xc, wc, st);
+  if (c.bn == 64) return launch_fm<64>(p, c.split, xc, wc, st);
+  return launch_fm<128>(p, c.split, xc, wc, st);
 }
 
 }  // namespace qmoe

@@ -102,7 +102,7 @@ cudaError_t launch_fp8_dequant(const uint8_t* codes, const float* scales, int E,
 cudaError_t launch_fp8_matmul(const uint8_t* xc, const float* xs, const uint8_t* wc, const float* ws,
                               const int32_t* offsets, int E, int M, int N, int K, void* y, int y_dtype, uint32_t* status,
                               uint32_t wait_limit_kilocycles, uint32_t stall, cudaStream_t st);
-cudaError_t fp8_matmul_variant(bool grouped, int E, int M, int N, int K, int* tokens, int* pair, int* split);
+cudaError_t fp8_matmul_variant(bool grouped, int E, int M, int N, int K, int* tile, int* wide, int* split);
 cudaError_t fp8_status_word(void** word);  // the current device's, for calls without one
 cudaError_t launch_sort_experts(const int32_t* ids, int A, int E, int32_t* offsets, int32_t* perm, int32_t* pos,
                                 cudaStream_t st);
