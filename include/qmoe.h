@@ -524,7 +524,8 @@ int qmoe_mx_untile_scales(const uint8_t* scales, int R, int K, uint8_t* scales_r
  * (the product rounded once, as if it were exact before).  A block with a NaN
  * or an infinity gets a NaN scale and zero codes.
  * K is at most 2^30 and so are M and E * N (QMOE_ERR_UNSUPPORTED).  Inputs and
- * outputs of one call must not overlap (qmoe_combine's out is the exception).
+ * outputs of one call must not overlap (but for qmoe_combine's out, which may be
+ * its residual, and qmoe_combine_backward's dys, which may be its ys).
  *
  * pos int32 [T, k] gives the place of each assignment t * k + j among the rows
  * of the experts' order, T * k of them: row pos[t, j] belongs to token t.  An
@@ -636,7 +637,7 @@ int qmoe_combine(const void* ys, int ys_dtype, const int32_t* pos, const float* 
  *   dys[pos[t, j]] = w[t, j] dout[t]                 [T * k, H], ys_dtype; NULL: not wanted
  *   dw[t, j] = sum_h dout[t, h] ys[pos[t, j], h]     fp32 [T, k]; 0 where j goes nowhere; NULL: not wanted
  * (the residual's gradient is dout).  ys may be NULL where dw is.  Sums are
- * fp32, in a fixed order.  H a multiple of 8.  Bound by HBM. */
+ * fp32, in a fixed order.  dys may be ys.  H a multiple of 8.  Bound by HBM. */
 int qmoe_combine_backward(const void* dout, int dout_dtype, const void* ys, int ys_dtype, const int32_t* pos,
                           const float* w, int T, int H, int k, void* dys, float* dw, void* stream);
 

@@ -15,31 +15,50 @@ namespace qmoe {
 // over warps, CTAs (through distributed shared memory) and experts; then every
 // warp walks its run again, 32 assignments at a time, and gives each its place:
 // where its expert starts, plus the expert's assignments in earlier warps and
-// rounds, plus those in lower lanes (match_any).  Bin E: no expert.
-// Bound by latency: the chain of both walks and three barriers.
-constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
+// rounds, plus those in lower lanes.  Lanes of one expert find each other by a
+// vote on each bit of its number (match_any goes through the experts one by one).
+// Bin E: no expert.  Bound by latency: the chain of both walks and the barriers.
 constexpr int kSortCluster = 8;
+constexpr int kSortAhead = 8;  // loads in flight a thread
 
-__global__ void __launch_bounds__(kSortThreads) sort_experts_kernel(const int32_t* __restrict__ ids, int A, int E,
-                                                                    int32_t* __restrict__ offsets,
-                                                                    int32_t* __restrict__ perm,
-                                                                    int32_t* __restrict__ pos) {
-  extern __shared__ uint32_t s_hist[];  // [kSortWarps][E + 1]
-  __shared__ uint32_t s_total[kMaxExperts + 1], s_start[kMaxExperts + 1], s_sum[kSortWarps];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, bins = E + 1;
+__global__ void __launch_bounds__(1024) sort_experts_kernel(const int32_t* __restrict__ ids, int A, int E,
+                                                            int32_t* __restrict__ offsets, int32_t* __restrict__ perm,
+                                                            int32_t* __restrict__ pos) {
+  extern __shared__ uint32_t s_hist[];  // [warps][E + 1]
+  __shared__ uint32_t s_total[kMaxExperts + 1], s_start[kMaxExperts + 1], s_sum[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5, bins = E + 1;
   const int C = (int)cluster_nctarank(), rank = (int)cluster_ctarank();
-  const int per = (int)((((long long)A + C * kSortWarps - 1) / (C * kSortWarps) + 31) & ~31LL);
-  const long long a0 = (long long)(rank * kSortWarps + warp) * per;
+  const int per = (int)((((long long)A + C * warps - 1) / (C * warps) + 31) & ~31LL);
+  const long long a0 = (long long)(rank * warps + warp) * per;
   const int n = (int)(a0 >= A ? 0 : min((long long)per, A - a0));
+  const long long cta = A - (long long)rank * warps * per;  // assignments from this CTA's first on
+  const int used = cta <= 0 ? 0 : (int)min((long long)warps, (cta + per - 1) / per);  // its warps with assignments
   uint32_t* hist = s_hist + warp * bins;
-  for (int e = lane; e < bins; e += 32) hist[e] = 0;
+  if (n > 0)
+    for (int e = lane; e < bins; e += 32) hist[e] = 0;
   __syncwarp();
   pdl_wait();
-  for (int i = lane; i < n; i += 32) atomicAdd(&hist[min((uint32_t)ids[a0 + i], (uint32_t)E)], 1u);
+  // f(offset, bin) for 32 assignments of the run at a time, ~0 for the lanes behind its end
+  auto walk = [&](auto f) {
+    for (int i = 0; i < n; i += 32 * kSortAhead) {
+      uint32_t e[kSortAhead];
+#pragma unroll
+      for (int j = 0; j < kSortAhead; ++j)
+        e[j] = i + 32 * j + lane < n ? min((uint32_t)ids[a0 + i + 32 * j + lane], (uint32_t)E) : ~0u;
+#pragma unroll
+      for (int j = 0; j < kSortAhead; ++j) {
+        if (i + 32 * j >= n) break;
+        f(i + 32 * j + lane, e[j]);
+      }
+    }
+  };
+  walk([&](int, uint32_t e) {
+    if (e != ~0u) atomicAdd(&hist[e], 1u);
+  });
   __syncthreads();
   if (tid < bins) {
     uint32_t sum = 0;
-    for (int w = 0; w < kSortWarps; ++w) {
+    for (int w = 0; w < used; ++w) {
       const uint32_t c = s_hist[w * bins + tid];
       s_hist[w * bins + tid] = sum;
       sum += c;
@@ -50,10 +69,14 @@ __global__ void __launch_bounds__(kSortThreads) sort_experts_kernel(const int32_
   else __syncthreads();
   uint32_t all = 0, before = 0;
   if (tid < bins) {
-    for (int r = 0; r < C; ++r) {
-      const uint32_t c = C > 1 ? __float_as_uint(ld_dsmem_f32(reinterpret_cast<const float*>(&s_total[tid]), r)) : s_total[tid];
-      before += r < rank ? c : 0;
-      all += c;
+    if (C == 1) {
+      all = s_total[tid];
+    } else {
+      for (int r = 0; r < C; ++r) {
+        const uint32_t c = __float_as_uint(ld_dsmem_f32(reinterpret_cast<const float*>(&s_total[tid]), r));
+        before += r < rank ? c : 0;
+        all += c;
+      }
     }
   }
   // exclusive sum over the bins (at most 257, threads of the first nine warps)
@@ -72,10 +95,14 @@ __global__ void __launch_bounds__(kSortThreads) sort_experts_kernel(const int32_
     s_start[tid] = start + before;
   }
   __syncthreads();
-  for (int i = lane; i < ((n + 31) & ~31); i += 32) {
-    const bool in = i < n;
-    const uint32_t e = in ? min((uint32_t)ids[a0 + i], (uint32_t)E) : 0xffffffffu;
-    const uint32_t peers = __match_any_sync(0xffffffffu, e);
+  const int bits = 32 - __clz(E);
+  walk([&](int i, uint32_t e) {
+    const bool in = e != ~0u;
+    uint32_t peers = __ballot_sync(0xffffffffu, in);
+    for (int b = 0; b < bits; ++b) {
+      const uint32_t one = __ballot_sync(0xffffffffu, e >> b & 1);
+      peers &= e >> b & 1 ? one : ~one;
+    }
     if (in) {
       const uint32_t p = s_start[e] + hist[e] + __popc(peers & ((1u << lane) - 1));
       const bool some = e < (uint32_t)E;
@@ -85,18 +112,17 @@ __global__ void __launch_bounds__(kSortThreads) sort_experts_kernel(const int32_
     __syncwarp();
     if (in && (peers >> lane) == 1u) hist[e] += __popc(peers);  // the highest lane of its expert
     __syncwarp();
-  }
+  });
   if (C > 1) cluster_sync_all();  // no CTA leaves while another may read its totals
 }
 
 cudaError_t launch_sort_experts(const int32_t* ids, int A, int E, int32_t* offsets, int32_t* perm, int32_t* pos,
                                 cudaStream_t st) {
-  const size_t smem = (size_t)kSortWarps * (E + 1) * 4;
+  const int C = A > 4096 ? kSortCluster : 1, threads = A > 1024 ? 1024 : 320;  // at least E + 1
   cudaLaunchConfig_t cfg = {};
-  const int C = A > 4096 ? kSortCluster : 1;
   cfg.gridDim = dim3(C);
-  cfg.blockDim = dim3(kSortThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = (size_t)(threads / 32) * (E + 1) * 4;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -124,9 +150,13 @@ __global__ void __launch_bounds__(256) dispatch_kernel(const uint4* __restrict__
   const uint32_t rows = (uint32_t)T * k;
   for (RowWalk w(blockIdx.x * 256 + threadIdx.x, gridDim.x * 256, (uint32_t)units); w.r < (uint32_t)T; w.next()) {
     const uint4 v = x[(size_t)w.r * units + w.u];
-    for (int j = 0; j < k; ++j) {
-      const uint32_t p = (uint32_t)pos[(size_t)w.r * k + j];
-      if (p < rows) xs[(size_t)p * units + w.u] = v;
+    for (int j0 = 0; j0 < k; j0 += 4) {
+      uint32_t p[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) p[j] = j0 + j < k ? (uint32_t)pos[(size_t)w.r * k + j0 + j] : ~0u;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (p[j] < rows) xs[(size_t)p[j] * units + w.u] = v;
     }
   }
 }
@@ -138,24 +168,32 @@ cudaError_t launch_dispatch(const void* x, int row_bytes, int T, int k, const in
 }
 
 // ------------------------------------------------------------------ combine
-// eight elements of T at element i (a multiple of 8), 16-byte aligned
+// eight elements of T, 16-byte aligned: loaded, and converted
 template <typename T>
-__device__ __forceinline__ void load8(const void* base, size_t i, float (&v)[8]) {
-  const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + i * sizeof(T));
-  if constexpr (sizeof(T) == 4) {
-    const uint4 a = p[0], b = p[1];
-    v[0] = __uint_as_float(a.x), v[1] = __uint_as_float(a.y), v[2] = __uint_as_float(a.z), v[3] = __uint_as_float(a.w);
-    v[4] = __uint_as_float(b.x), v[5] = __uint_as_float(b.y), v[6] = __uint_as_float(b.z), v[7] = __uint_as_float(b.w);
-  } else {
-    const uint4 a = p[0];
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+struct Eight {
+  uint4 w[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const void* base, size_t i) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + i * sizeof(T));
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[2 * j] = Half<T>::to_float((uint16_t)(w[j] & 0xffffu));
-      v[2 * j + 1] = Half<T>::to_float((uint16_t)(w[j] >> 16));
+    for (uint32_t q = 0; q < sizeof(T) / 2; ++q) w[q] = p[q];
+  }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        v[4 * q] = __uint_as_float(w[q].x), v[4 * q + 1] = __uint_as_float(w[q].y);
+        v[4 * q + 2] = __uint_as_float(w[q].z), v[4 * q + 3] = __uint_as_float(w[q].w);
+      }
+    } else {
+      const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[2 * j] = Half<T>::to_float((uint16_t)(u[j] & 0xffffu));
+        v[2 * j + 1] = Half<T>::to_float((uint16_t)(u[j] >> 16));
+      }
     }
   }
-}
+};
 template <typename T>
 __device__ __forceinline__ void store8(void* base, size_t i, const float (&v)[8]) {
   uint4* p = reinterpret_cast<uint4*>(static_cast<uint8_t*>(base) + i * sizeof(T));
@@ -172,7 +210,8 @@ __device__ __forceinline__ void store8(void* base, size_t i, const float (&v)[8]
 }
 
 // out[t] = residual[t] + sum_j w[t, j] ys[pos[t, j]], fp32 in this order, rounded
-// once.  A thread takes 8 columns of a token.  Bound by HBM.
+// once.  A thread takes 8 columns of a token, four assignments' loads in flight.
+// Bound by HBM.
 template <typename Y, typename O>
 __global__ void __launch_bounds__(256) combine_kernel(const void* __restrict__ ys, const int32_t* __restrict__ pos,
                                                       const float* __restrict__ wt, const void* residual, int T, int H,
@@ -180,30 +219,47 @@ __global__ void __launch_bounds__(256) combine_kernel(const void* __restrict__ y
   pdl_wait();
   const uint32_t rows = (uint32_t)T * k;
   for (RowWalk w(blockIdx.x * 256 + threadIdx.x, gridDim.x * 256, (uint32_t)H / 8); w.r < (uint32_t)T; w.next()) {
-    const size_t i = (size_t)w.r * H + 8 * w.u;
+    const size_t i = (size_t)w.r * H + 8 * w.u, a = (size_t)w.r * k;
     float s[8] = {};
-    if (residual) load8<O>(residual, i, s);
-    for (int j = 0; j < k; ++j) {
-      const uint32_t p = (uint32_t)pos[(size_t)w.r * k + j];
-      if (p >= rows) continue;
-      const float f = wt ? wt[(size_t)w.r * k + j] : 1.f;
-      float v[8];
-      load8<Y>(ys, (size_t)p * H + 8 * w.u, v);
+    if (residual) {
+      Eight<O> r;
+      r.load(residual, i);
+      r.values(s);
+    }
+    for (int j0 = 0; j0 < k; j0 += 4) {
+      uint32_t p[4];
+      float f[4];
+      Eight<Y> y[4];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) s[q] = fmaf(f, v[q], s[q]);
+      for (int j = 0; j < 4; ++j) {
+        p[j] = j0 + j < k ? (uint32_t)pos[a + j0 + j] : ~0u;
+        f[j] = wt && j0 + j < k ? wt[a + j0 + j] : 1.f;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (p[j] < rows) y[j].load(ys, (size_t)p[j] * H + 8 * w.u);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (p[j] < rows) {
+          float v[8];
+          y[j].values(v);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) s[q] = fmaf(f[j], v[q], s[q]);
+        }
     }
     store8<O>(out, i, s);
   }
 }
 
 // dys[pos[t, j]] = w[t, j] dout[t], dw[t, j] = sum_h dout[t, h] ys[pos[t, j], h] (fp32).
-// One warp per assignment; a token's warps are neighbours, so dout comes from
-// L1 or L2 but once.  Bound by HBM.
+// One warp per assignment, four steps of 256 columns in flight; a token's warps
+// are neighbours, so dout comes from L1 or L2 but once.  dys may be ys: a thread
+// has read what it writes.  Bound by HBM.
 template <typename Y, typename O>
-__global__ void __launch_bounds__(256) combine_backward_kernel(const void* __restrict__ dout, const void* __restrict__ ys,
+__global__ void __launch_bounds__(256) combine_backward_kernel(const void* __restrict__ dout, const void* ys,
                                                                const int32_t* __restrict__ pos,
                                                                const float* __restrict__ wt, int T, int H, int k,
-                                                               void* __restrict__ dys, float* __restrict__ dw) {
+                                                               void* dys, float* __restrict__ dw) {
   pdl_wait();
   const uint32_t rows = (uint32_t)T * k, lane = threadIdx.x & 31;
   for (uint32_t a = blockIdx.x * 8 + threadIdx.x / 32; a < rows; a += gridDim.x * 8) {
@@ -212,19 +268,31 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(const void* __res
     if (p < rows) {
       const float f = wt ? wt[a] : 1.f;
       const size_t from = (size_t)(a / k) * H, to = (size_t)p * H;
-      for (int h = lane * 8; h < H; h += 256) {
-        float d[8], y[8];
-        load8<O>(dout, from + h, d);
-        if (dw) {
-          load8<Y>(ys, to + h, y);
+      for (int h0 = lane * 8; h0 < H; h0 += 1024) {
+        Eight<O> d[4];
+        Eight<Y> y[4];
 #pragma unroll
-          for (int q = 0; q < 8; ++q) dot = fmaf(d[q], y[q], dot);
-        }
-        if (dys) {
+        for (int j = 0; j < 4; ++j)
+          if (h0 + 256 * j < H) {
+            d[j].load(dout, from + h0 + 256 * j);
+            if (dw) y[j].load(ys, to + h0 + 256 * j);
+          }
 #pragma unroll
-          for (int q = 0; q < 8; ++q) y[q] = f * d[q];
-          store8<Y>(dys, to + h, y);
-        }
+        for (int j = 0; j < 4; ++j)
+          if (h0 + 256 * j < H) {
+            float u[8], v[8];
+            d[j].values(u);
+            if (dw) {
+              y[j].values(v);
+#pragma unroll
+              for (int q = 0; q < 8; ++q) dot = fmaf(u[q], v[q], dot);
+            }
+            if (dys) {
+#pragma unroll
+              for (int q = 0; q < 8; ++q) v[q] = f * u[q];
+              store8<Y>(dys, to + h0 + 256 * j, v);
+            }
+          }
       }
     }
     if (dw) {

@@ -34,19 +34,27 @@ __global__ void __launch_bounds__(256) fp8_rows_kernel(const void* __restrict__ 
   const uint32_t nb = (uint32_t)(K + 127) / 128, rows = PLACES ? (uint32_t)M * k : (uint32_t)M;
   for (RowWalk w(blockIdx.x * 256 + threadIdx.x, gridDim.x * 256, nb * 8); w.r < (uint32_t)M; w.next()) {
     const bool in = 16 * w.u < (uint32_t)K;
-    float v[16] = {};
-    if (in) load16<T>(x, (size_t)w.r * K + 16 * w.u, v);
-    const Fp8Block b(fp8_group_max(fp8_max16(v)));
+    Sixteen<T> raw;
+    if (in) raw.load(x, (size_t)w.r * K + 16 * w.u);
+    else raw.clear();
+    const Fp8Block b(fp8_group_max(Sixteen<T>::max_bits(raw.max_raw())));
+    float v[16];
+    raw.values(v);
     const uint4 c = b.codes16(v);
     if (!PLACES) {
       if (in) *reinterpret_cast<uint4*>(codes + (size_t)w.r * K + 16 * w.u) = c;
       if (!(w.u & 7)) scales[(size_t)w.r * nb + w.u / 8] = b.scale;
     } else {
-      for (int j = 0; j < k; ++j) {
-        const uint32_t p = (uint32_t)pos[(size_t)w.r * k + j];
-        if (p >= rows) continue;  // this assignment goes nowhere
-        if (in) *reinterpret_cast<uint4*>(codes + (size_t)p * K + 16 * w.u) = c;
-        if (!(w.u & 7)) scales[(size_t)p * nb + w.u / 8] = b.scale;
+      for (int j0 = 0; j0 < k; j0 += 4) {
+        uint32_t p[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) p[j] = j0 + j < k ? (uint32_t)pos[(size_t)w.r * k + j0 + j] : ~0u;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (p[j] >= rows) continue;  // this assignment goes nowhere
+          if (in) *reinterpret_cast<uint4*>(codes + (size_t)p[j] * K + 16 * w.u) = c;
+          if (!(w.u & 7)) scales[(size_t)p[j] * nb + w.u / 8] = b.scale;
+        }
       }
     }
   }
@@ -66,7 +74,11 @@ __global__ void __launch_bounds__(256) fp8_swiglu_kernel(const void* __restrict_
       load16<T>(h, (size_t)w.r * 2 * I + 16 * w.u, g);
       load16<T>(h, (size_t)w.r * 2 * I + I + 16 * w.u, v);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) v[j] *= g[j] / (1.f + expf(-g[j]));
+      for (int j = 0; j < 16; ++j) {
+        float r;  // (a rounded quotient takes eight instructions more)
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + expf(-g[j])));
+        v[j] *= g[j] * r;
+      }
     }
     const Fp8Block b(fp8_group_max(fp8_max16(v)));
     const uint4 c = b.codes16(v);
@@ -79,34 +91,22 @@ __global__ void __launch_bounds__(256) fp8_swiglu_kernel(const void* __restrict_
 // One CTA per 128 x 128 block: a thread takes 16 columns of four rows, which it
 // keeps as they came until the block's maximum is known.  Bound by HBM.
 template <typename T>
-__global__ void __launch_bounds__(256) fp8_weights_kernel(const void* __restrict__ w, int N, int K,
+__global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 4) fp8_weights_kernel(const void* __restrict__ w, int N, int K,
                                                           uint8_t* __restrict__ codes, float* __restrict__ scales) {
   pdl_wait();
-  constexpr int W = sizeof(T) / 2;  // 32-byte pieces of 16 elements
   const uint32_t nb = (uint32_t)(K + 127) / 128, rb = (uint32_t)(N + 127) / 128;
   const uint32_t b = blockIdx.x % nb, q = blockIdx.x / nb, r = q % rb, e = q / rb;
   const uint32_t col = b * 128 + (threadIdx.x & 7) * 16, row = r * 128 + threadIdx.x / 8;
   const size_t at = ((size_t)e * N + row) * K + col;
-  uint32_t raw[4][W][8] = {};
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (col < (uint32_t)K && row + 32 * i < (uint32_t)N)
-#pragma unroll
-      for (int p = 0; p < W; ++p) load32(static_cast<const uint8_t*>(w) + (at + (size_t)32 * i * K) * sizeof(T) + 32 * p, raw[i][p]);
-  auto values = [&](int i, float(&v)[16]) {
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      if constexpr (sizeof(T) == 4) v[j] = __uint_as_float(raw[i][j / 8][j % 8]);
-      else v[j] = Half<T>::to_float((uint16_t)(raw[i][0][j / 2] >> (16 * (j & 1))));
-    }
-  };
-  uint32_t m = 0;
+  Sixteen<T> raw[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float v[16];
-    values(i, v);
-    m = max(m, fp8_max16(v));
+    if (col < (uint32_t)K && row + 32 * i < (uint32_t)N) raw[i].load(w, at + (size_t)32 * i * K);
+    else raw[i].clear();
   }
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = max(m, Sixteen<T>::max_bits(raw[i].max_raw()));
   m = __reduce_max_sync(0xffffffffu, m);
   __shared__ uint32_t part[8];
   if ((threadIdx.x & 31) == 0) part[threadIdx.x / 32] = m;
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(256) fp8_weights_kernel(const void* __restrict
   for (int i = 0; i < 4; ++i)
     if (col < (uint32_t)K && row + 32 * i < (uint32_t)N) {
       float v[16];
-      values(i, v);
+      raw[i].values(v);
       *reinterpret_cast<uint4*>(codes + at + (size_t)32 * i * K) = blk.codes16(v);
     }
   if (threadIdx.x == 0) scales[blockIdx.x] = blk.scale;
