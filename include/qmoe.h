@@ -582,8 +582,8 @@ int qmoe_fp8_matmul(const uint8_t* x_codes, const float* x_scales, const uint8_t
 
 /* The form of the kernel that qmoe_fp8_matmul runs for such a call on the
  * current device (no launch): variant_out[1] 0: tiles of variant_out[0] tokens
- * by 128 outputs, 1: of 128 tokens by variant_out[0] outputs, 2: of 256 by
- * variant_out[0] for pairs of CTAs; [2] CTAs that share a tile's K. */
+ * by 128 outputs, 1: of 128 tokens by variant_out[0] outputs; [2] CTAs that share
+ * a tile's K. */
 int qmoe_fp8_matmul_variant(int grouped, int E, int M, int N, int K, int variant_out[3]);
 
 /* qmoe_fp8_matmul with diagnostics of its failure path, as

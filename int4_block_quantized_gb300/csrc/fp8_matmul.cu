@@ -160,20 +160,19 @@ __device__ __forceinline__ void fm_load(uint32_t taddr, f2 (&r)[G][4]) {
 
 // D[tmem] (+)= A x B^T of e4m3 codes (shared-memory descriptors as sw128_desc,
 // low words), 32 k, by the lane of a converged warp whose e is 1.
-#define QMOE_MMA_F8(CGS)                                                                                 \
-  asm volatile(                                                                                          \
-      "{\n .reg .pred p, e;\n .reg .b64 a, b;\n mov.b64 a, {%1, %6};\n mov.b64 b, {%2, %6};\n"            \
-      " setp.ne.b32 e, %5, 0;\n setp.ne.b32 p, %4, 0;\n"                                                 \
-      " @e tcgen05.mma.cta_group::" CGS ".kind::f8f6f4 [%0], a, b, %3, p;\n}" ::"r"(d),                  \
-      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(e), "n"((1024u >> 4) | 1u << 14 | 2u << 29)       \
-      : "memory")
-template <int CG>
 __device__ __forceinline__ void mma_f8(uint32_t e, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
                                        uint32_t accumulate) {
-  if constexpr (CG == 1) QMOE_MMA_F8("1");
-  else QMOE_MMA_F8("2");
+  asm volatile(
+      "{\n .reg .pred p, e;\n .reg .b64 a, b;\n mov.b64 a, {%1, %6};\n mov.b64 b, {%2, %6};\n"
+      " setp.ne.b32 e, %5, 0;\n setp.ne.b32 p, %4, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, p;\n}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(e), "n"((1024u >> 4) | 1u << 14 | 2u << 29)
+      : "memory");
 }
-#undef QMOE_MMA_F8
+
+__device__ __forceinline__ void fm_prefetch_map(const void* tmap) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tmap)) : "memory");
+}
 
 // A tile: the expert, which of its tiles of weight rows, tokens m0 .. m1 - 1.
 struct FmTile {
@@ -291,6 +290,7 @@ __global__ void __launch_bounds__(kFmThreads, 1)
     tmem_alloc(s_tmem, 512);
     tmem_relinquish();
   }
+  if (warp == 0) fm_prefetch_map(&tm_w), fm_prefetch_map(&tm_x);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(kFmThreads, 1)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           if (32 * j >= left) break;
-          mma_f8<1>(el, tmem + b * BN, da + 2 * j, db + 2 * j, idesc, j > 0);
+          mma_f8(el, tmem + b * BN, da + 2 * j, db + 2 * j, idesc, j > 0);
         }
         mma_commit_mx<1>(el, &empty[s]);
         mma_commit_mx<1>(el, &acc_full[b]);
@@ -562,9 +562,9 @@ constexpr int kFwThreads = 384;
 constexpr int kFwRegs = 168, kFwManyRegs = 208, kFwFewRegs = 88;
 static_assert(256 * kFwManyRegs + 128 * kFwFewRegs <= kFwThreads * kFwRegs, "registers");
 
-template <int BN, int CG>
+template <int BN>
 struct FwPlan {
-  static constexpr uint32_t kA = 128 * 128, kB = BN / CG * 128, kStage = kA + kB;  // one CTA's share of a block's codes
+  static constexpr uint32_t kA = 128 * 128, kB = BN * 128, kStage = kA + kB;  // a block's codes
   static constexpr int kBufs = 512 / BN;
   static constexpr int kHalves = BN / 128;                        // scale blocks of a tile's weight rows
   static constexpr int kC = BN / 2 / 16;                          // a warp's columns, 16 at a time
@@ -593,18 +593,11 @@ __device__ __forceinline__ void fw_wait(uint32_t (&r)[16]) {
                : "memory");
 }
 
-// Arrives on a barrier of the other CTA (its shared::cluster address).  Relaxed:
-// what it tells is that loads into registers are done, no memory is handed over
-// (a release there waits for this thread's writes of y, too).
-__device__ __forceinline__ void mbar_arrive_remote(uint32_t bar) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-template <int BN, int CG>
+template <int BN>
 __global__ void __launch_bounds__(kFwThreads, 1)
     fp8_wide_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x, const FmParams p) {
-  using P = FwPlan<BN, CG>;
-  constexpr int BT = 128 * CG;  // tokens of a tile
+  using P = FwPlan<BN>;
+  constexpr int BT = 128;  // tokens of a tile
   constexpr int S = P::kStages, NB = P::kBufs, SQ = P::kQuads;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -633,7 +626,7 @@ __global__ void __launch_bounds__(kFwThreads, 1)
     }
     for (int b = 0; b < NB; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_free[b], 8 * CG);
+      mbar_init(&acc_free[b], 8);
     }
     for (int b = 0; b < SQ; ++b) {
       mbar_init(&sc_full[b], 1);
@@ -645,17 +638,12 @@ __global__ void __launch_bounds__(kFwThreads, 1)
     fence_barrier_init();
   }
   if (warp == 1) {
-    if (CG == 1) {
-      tmem_alloc(s_tmem, 512);
-      tmem_relinquish();
-    } else {
-      tmem_alloc2(s_tmem, 512);
-      tmem_relinquish2();
-    }
+    tmem_alloc(s_tmem, 512);
+    tmem_relinquish();
   }
+  if (warp == 0) fm_prefetch_map(&tm_w), fm_prefetch_map(&tm_x);
   tc_fence_before();
   __syncthreads();
-  if (CG == 2) cluster_sync_all();  // the pair's barriers are set up
   tc_fence_after();
   constexpr uint32_t tmem = 0;  // all 512 columns are this CTA's
   pdl_wait();
@@ -663,8 +651,6 @@ __global__ void __launch_bounds__(kFwThreads, 1)
   fm_table<BT>(p, tab, s_sum);
 
   const int tiles = tab.first[p.E] * p.row_tiles, nb = (p.K + 127) / 128;
-  const int half = CG == 2 ? (int)cluster_ctarank() : 0;  // of the pair's tokens
-  const int first = blockIdx.x / CG, step = gridDim.x / CG;
   auto stalled = [&](uint32_t role) { return (p.stall & role) && !fm_wait(never, 0, p, s_abort); };
   if (warp >= 4) {
     if (BN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFwManyRegs));
@@ -673,10 +659,10 @@ __global__ void __launch_bounds__(kFwThreads, 1)
     float* buf = reinterpret_cast<float*>(outbuf) + (warp - 4) * 32 * 17;
     int n = 0, it = 0;
     bool ok = !stalled(QMOE_DIAG_STALL_FP8_OUTPUT);
-    for (int t = first; t < tiles && ok; t += step) {
+    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
       const FmTile f = fm_tile<BT>(p, tab, t);
       const int n0 = f.rt * BN + set * (BN / 2), cols = p.N - n0;  // this warp's columns
-      const int m0 = f.m0 + half * 128 + qd * 32;                  // and tokens
+      const int m0 = f.m0 + qd * 32;                               // and tokens
       const bool live = cols > 0 && m0 < f.m1;
       float acc[P::kC][16];
 #pragma unroll
@@ -702,10 +688,7 @@ __global__ void __launch_bounds__(kFwThreads, 1)
         auto freed = [&]() {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) {
-            if (half == 0) mbar_arrive(&acc_free[b]);
-            else mbar_arrive_remote(peer_u32(&acc_free[b], 0));
-          }
+          if (lane == 0) mbar_arrive(&acc_free[b]);
           if (sub == 3) ++it;
           ready = c + 1 < nb && mbar_try_wait(&acc_full[(n + 1) % NB], ((n + 1) / NB) & 1) &&
                   (sub != 3 || mbar_try_wait(&sc_full[it % SQ], (it / SQ) & 1));
@@ -794,27 +777,18 @@ __global__ void __launch_bounds__(kFwThreads, 1)
       uint32_t ph = 0;
       bool ok = !stalled(QMOE_DIAG_STALL_FP8_CODES);
       const uint32_t el = elect_lane();
-      for (int t = first; t < tiles && ok; t += step) {
+      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
         const FmTile f = fm_tile<BT>(p, tab, t);
-        // copies of 64 rows: of this CTA's tokens, of all of them, of weights
-        const int n = f.m1 - f.m0, xb = min(max((n - half * 128 + 63) / 64, 0), 2), all = (n + 63) / 64;
-        const int wb = CG == 2 ? BN / 2 / 64 : (min(BN, p.N - f.rt * BN) + 63) / 64;
-        const int m0 = f.m0 + half * 128, row = f.e * p.N + f.rt * BN + half * (BN / 2);
+        const int xb = (f.m1 - f.m0 + 63) / 64, wb = (min(BN, p.N - f.rt * BN) + 63) / 64;  // copies of 64 rows
         for (int c = 0; c < nb; ++c, ++it) {
           if (it >= S) ok = fm_wait(&empty[s], ph ^ 1u, p, s_abort);
           if (!ok) break;
           if (el) {
             uint8_t* st = ring + s * P::kStage;
-            if constexpr (CG == 2) {  // both CTAs report to the leader
-              const uint32_t bar = peer_u32(&full[s], 0);
-              if (half == 0) mbar_arrive_expect_tx(&full[s], (all + 2 * wb) * 64 * 128);
-              for (int i = 0; i < xb; ++i) tma_load_2d_pair(st + i * 8192, &tm_x, c * 128, m0 + 64 * i, bar);
-              for (int i = 0; i < wb; ++i) tma_load_2d_pair(st + P::kA + i * 8192, &tm_w, c * 128, row + 64 * i, bar);
-            } else {
-              mbar_arrive_expect_tx(&full[s], (xb + wb) * 64 * 128);
-              for (int i = 0; i < xb; ++i) tma_load_2d(st + i * 8192, &tm_x, c * 128, m0 + 64 * i, &full[s]);
-              for (int i = 0; i < wb; ++i) tma_load_2d(st + P::kA + i * 8192, &tm_w, c * 128, row + 64 * i, &full[s]);
-            }
+            mbar_arrive_expect_tx(&full[s], (xb + wb) * 64 * 128);
+            for (int i = 0; i < xb; ++i) tma_load_2d(st + i * 8192, &tm_x, c * 128, f.m0 + 64 * i, &full[s]);
+            for (int i = 0; i < wb; ++i)
+              tma_load_2d(st + P::kA + i * 8192, &tm_w, c * 128, f.e * p.N + f.rt * BN + 64 * i, &full[s]);
           }
           __syncwarp();
           if (++s == S) {
@@ -823,18 +797,16 @@ __global__ void __launch_bounds__(kFwThreads, 1)
           }
         }
       }
-      // A pair's stages are counted in the leader alone, but both CTAs see the
-      // commits that give slots back (and stay until these have arrived).
-      if (lane == 0) fm_settle<S>(CG == 1 ? full : empty, it, p, s_abort);
-    } else if (warp == 1 && half == 0) {  // a pair: the leader issues for both
+      if (lane == 0) fm_settle<S>(full, it, p, s_abort);
+    } else if (warp == 1) {
       // ------------------------------------------------------------- MMAs
       int n = 0, s = 0;  // blocks so far
       uint32_t ph = 0;
       bool ok = !stalled(QMOE_DIAG_STALL_FP8_MMA), issued = false;
       const uint32_t el = elect_lane();
-      for (int t = first; t < tiles && ok; t += step) {
+      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
         const FmTile f = fm_tile<BT>(p, tab, t);
-        const int cols = CG == 2 ? BN : (min(BN, p.N - f.rt * BN) + 15) & ~15;
+        const int cols = (min(BN, p.N - f.rt * BN) + 15) & ~15;
         const uint32_t idesc = 1u << 4 | (uint32_t)(cols >> 3) << 17 | (uint32_t)(BT >> 4) << 24;
         for (int c = 0; c < nb; ++c, ++n) {
           const int b = n % NB;
@@ -848,10 +820,10 @@ __global__ void __launch_bounds__(kFwThreads, 1)
   #pragma unroll
           for (int j = 0; j < 4; ++j) {
             if (32 * j >= left) break;
-            mma_f8<CG>(el, tmem + b * BN, da + 2 * j, db + 2 * j, idesc, j > 0);
+            mma_f8(el, tmem + b * BN, da + 2 * j, db + 2 * j, idesc, j > 0);
           }
-          mma_commit_mx<CG>(el, &empty[s]);
-          mma_commit_mx<CG>(el, &acc_full[b]);
+          mma_commit_mx<1>(el, &empty[s]);
+          mma_commit_mx<1>(el, &acc_full[b]);
           issued = true;
           if (++s == S) {
             s = 0;
@@ -860,8 +832,7 @@ __global__ void __launch_bounds__(kFwThreads, 1)
         }
       }
       if (issued) {  // all MMAs have finished before tensor memory is freed
-        if (CG == 1) mma_commit_mx<1>(el, fin);
-        else mma_commit_mx2_own(el, fin);  // a commit to the peer's barrier too could arrive there when it has left
+        mma_commit_mx<1>(el, fin);
         if (el) mbar_wait(fin, 0, nullptr);
       }
     } else if (warp == 2) {
@@ -869,7 +840,7 @@ __global__ void __launch_bounds__(kFwThreads, 1)
       int it = 0;
       const int rb = (p.N + 127) / 128;
       bool ok = !stalled(QMOE_DIAG_STALL_FP8_SCALES);
-      for (int t = first; t < tiles && ok; t += step) {
+      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
         const FmTile f = fm_tile<BT>(p, tab, t);
         const float* ws = p.ws + ((size_t)f.e * rb + f.rt * P::kHalves) * nb;
         for (int c = 0; c < nb; c += 4, ++it) {
@@ -881,8 +852,8 @@ __global__ void __launch_bounds__(kFwThreads, 1)
             for (int j = 0; j < 4; ++j) w[h][j] = f.rt * P::kHalves + h < rb && c + j < nb ? ws[h * nb + c + j] : 0.f;
   #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (f.m0 + half * 128 + 32 * i + lane < f.m1) {
-              const float* xs = p.xs + (size_t)(f.m0 + half * 128 + 32 * i + lane) * nb + c;
+            if (f.m0 + 32 * i + lane < f.m1) {
+              const float* xs = p.xs + (size_t)(f.m0 + 32 * i + lane) * nb + c;
               if (p.wide_scales) {
                 const float4 u = *reinterpret_cast<const float4*>(xs);
                 v[i][0] = u.x, v[i][1] = u.y, v[i][2] = u.z, v[i][3] = u.w;
@@ -909,11 +880,9 @@ __global__ void __launch_bounds__(kFwThreads, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (CG == 2) cluster_sync_all();  // neither CTA leaves while the other may use its memory
   if (warp == 1) {
     tc_fence_after();
-    if (CG == 1) tmem_dealloc(tmem, 512);
-    else tmem_dealloc2(tmem, 512);
+    tmem_dealloc(tmem, 512);
   }
 }
 
@@ -964,14 +933,14 @@ static cudaError_t launch_fm(FmParams p, int split, const uint8_t* xc, const uin
   return cudaLaunchKernelEx(&cfg, kernel, tw, tx, p);
 }
 
-template <int BN, int CG>
+template <int BN>
 static cudaError_t launch_fw(FmParams p, const uint8_t* xc, const uint8_t* wc, cudaStream_t st) {
-  using P = FwPlan<BN, CG>;
+  using P = FwPlan<BN>;
   static_assert(P::kStages >= 3, "plan");
   static_assert((2 * P::kStages + 2 * P::kBufs + 2 * P::kQuads + 2) * 8 + 40 <= kFmBars, "barriers");
   p.split = 1;
   p.row_tiles = (p.N + BN - 1) / BN;
-  const long long tiles = fm_token_tiles(p, 128 * CG) * p.row_tiles;
+  const long long tiles = fm_token_tiles(p, 128) * p.row_tiles;
   if (tiles > (1LL << 27)) return cudaErrorInvalidValue;
   CUtensorMap tw, tx;
   if (!make_map(&tw, wc, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.K, (uint64_t)p.E * p.N, 128, 64, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -982,7 +951,7 @@ static cudaError_t launch_fw(FmParams p, const uint8_t* xc, const uint8_t* wc, c
   p.wide_out = p.N % (p.y_dtype == QMOE_F32 ? 4 : 8) == 0 && !(reinterpret_cast<uintptr_t>(p.y) & 15);
   p.wide_scales = p.K % 512 == 0 && !(reinterpret_cast<uintptr_t>(p.xs) & 15);
   const int sms = device_sm_count();
-  auto kernel = fp8_wide_kernel<BN, CG>;
+  auto kernel = fp8_wide_kernel<BN>;
   const cudaError_t err = ensure_smem(kernel, kFmSmem);  // all of it, as above
   if (err != cudaSuccess) return err;
   if (BN == 256) {  // the warps' shares of the registers wait for what the launch does not have
@@ -995,20 +964,7 @@ static cudaError_t launch_fw(FmParams p, const uint8_t* xc, const uint8_t* wc, c
     }
     if (regs < kFwRegs) return cudaErrorInvalidDeviceFunction;
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(CG * (tiles < sms / CG ? tiles : sms / CG)));
-  cfg.blockDim = dim3(kFwThreads);
-  cfg.dynamicSmemBytes = kFmSmem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = CG;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, tw, tx, p);
+  return launch_kernel(kernel, dim3((unsigned)(tiles < sms ? tiles : sms)), dim3(kFwThreads), kFmSmem, st, true, tw, tx, p);
 }
 
 // CTAs of clusters of `split` (2, 4, 8) that the device holds at once, one CTA
@@ -1043,8 +999,7 @@ static cudaError_t fm_capacity(int split, int* ctas) {
   return cudaSuccess;
 }
 
-// wide 0: bn tokens a tile, 128 weight rows; 1: 128 tokens, bn weight rows; 2: the
-// same by pairs of CTAs.
+// wide 0: bn tokens a tile, 128 weight rows; 1: 128 tokens, bn weight rows.
 struct FmChoice {
   int bn, wide, split;
 };
@@ -1053,8 +1008,7 @@ static cudaError_t fm_choose(const FmParams& p, FmChoice* choice) {
     int bn, wide, start, stage, tile, epilogue, exchange;
   } kinds[] = {{16, 0, 3300, 150, 300, 200, 400},  {32, 0, 4000, 150, 350, 300, 1000},
                {64, 0, 4700, 200, 500, 850, 1300}, {128, 0, 5200, 300, 1200, 1350, 2000},
-               {128, 1, 4000, 285, 1000, 0, 0},    {256, 1, 4300, 460, 1500, 0, 0},
-               {256, 2, 4800, 460, 1300, 0, 0}};
+               {128, 1, 4000, 285, 1000, 0, 0},    {256, 1, 4300, 460, 1500, 0, 0}};
   int capacity[9] = {};
   for (int split = 2; split <= 8; split *= 2) {
     const cudaError_t err = fm_capacity(split, &capacity[split]);
@@ -1065,14 +1019,14 @@ static cudaError_t fm_choose(const FmParams& p, FmChoice* choice) {
   long long least = -1;
   for (const auto& k : kinds) {
     if (!k.wide && k.bn < 64 && each > k.bn) continue;
-    const int bt = k.wide ? 128 * k.wide : k.bn, br = k.wide ? k.bn : 128;
+    const int bt = k.wide ? 128 : k.bn, br = k.wide ? k.bn : 128;
     const long long rows = (p.N + br - 1) / br;
     // an expert's last tile is half full on average
     const long long some = p.offsets ? p.M / bt + active / 2 : (p.M + bt - 1) / bt;
     const long long tiles = rows * (some > active ? some : active);
     for (int split = 1; split <= 8; split *= 2) {
       if (split > 1 && (!k.exchange || split > nb || rows * fm_token_tiles(p, k.bn) * split > capacity[split])) break;
-      const long long slots = split > 1 ? tiles : k.wide == 2 ? device_sm_count() / 2 : device_sm_count();
+      const long long slots = split > 1 ? tiles : device_sm_count();
       const long long rounds = (tiles + slots - 1) / slots;
       const long long one = (long long)((nb + split - 1) / split) * k.stage, more = one + k.tile;
       const long long t = k.start + one + (rounds - 1) * (more > k.epilogue ? more : k.epilogue) +
@@ -1123,8 +1077,7 @@ cudaError_t launch_fp8_matmul(const uint8_t* xc, const float* xs, const uint8_t*
   FmChoice c = {};
   const cudaError_t err = fm_choose(p, &c);
   if (err != cudaSuccess) return err;
-  if (c.wide == 2) return launch_fw<256, 2>(p, xc, wc, st);
-  if (c.wide) return c.bn == 256 ? launch_fw<256, 1>(p, xc, wc, st) : launch_fw<128, 1>(p, xc, wc, st);
+  if (c.wide) return c.bn == 256 ? launch_fw<256>(p, xc, wc, st) : launch_fw<128>(p, xc, wc, st);
   if (c.bn == 16) return launch_fm<16>(p, c.split, xc, wc, st);
   if (c.bn == 32) return launch_fm<32>(p, c.split, xc, wc, st);
   if (c.bn == 64) return launch_fm<64>(p, c.split, xc, wc, st);
