@@ -755,23 +755,27 @@ def qmoe_fp8_matmul(x_codes, x_scales, w_codes, w_scales, dtype=torch.bfloat16, 
     M, K = _mx_size(x_codes, where)
     dev, dt = x_codes.get_device(), _MX_DT.get(dtype)
     shape = w_codes.shape
-    E = 1 if offsets is None else offsets.numel() - 1
-    N = shape[-2] if len(shape) in (2, 3) else 0
-    if dt is None or N < 1 or E < 1 or (E,) + tuple(shape[-2:]) != (E, N, K) or tuple(shape[:-2]) not in ((E,), () if E == 1 else (E,)):
+    op = st = None
+    E = 1
+    if offsets is not None:
+        E = offsets.numel() - 1
+        _mx_check2(offsets, dev, _I32, (E + 1,), where, "offsets")
+        op = offsets.data_ptr()
+    if len(shape) == 3 and shape[0] == E or len(shape) == 2 and E == 1:
+        N = shape[-2]
+    else:
+        N = 0
+    if dt is None or N < 1 or E < 1 or shape[-1] != K:
         _bad(where, "x %s, W %s, %s experts, result in %s" % (tuple(x_codes.shape), tuple(shape), E, dtype))
     if E > 256:
         raise QMoEError(2, "%s: %d experts, at most 256" % (where, E))
     _fp8_size(M, K, where)
     _fp8_size(E * N, K, where)
-    nb = (K + 127) // 128
-    _mx_check2(x_codes, dev, _U8, (M, K), where, "x_codes")
+    nb, rb = (K + 127) // 128, (N + 127) // 128
+    _mx_check2(x_codes, dev, _U8, x_codes.shape, where, "x_codes")
     _mx_check2(x_scales, dev, _F32, (M, nb), where, "x_scales")
     _mx_check2(w_codes, dev, _U8, shape, where, "w_codes")
-    _mx_check2(w_scales, dev, _F32, tuple(shape[:-2]) + ((N + 127) // 128, nb), where, "w_scales")
-    op = st = None
-    if offsets is not None:
-        _mx_check2(offsets, dev, _I32, (E + 1,), where, "offsets")
-        op = offsets.data_ptr()
+    _mx_check2(w_scales, dev, _F32, (E, rb, nb) if len(shape) == 3 else (rb, nb), where, "w_scales")
     if out is None:
         out = torch.empty((M, N), dtype=dtype, device=x_codes.device)
     else:

@@ -1003,36 +1003,50 @@ static cudaError_t fm_capacity(int split, int* ctas) {
 struct FmChoice {
   int bn, wide, split;
 };
+
+// The form by an estimate of its time in ns: a start, the blocks of the CTA with
+// the most tiles (a narrower MMA is not proportionally faster), what each further
+// tile adds (rows of y off 16 bytes leave the wide forms slowly), the exchange of a
+// split tile's sums; at least what the operands' bytes take.  Where experts share
+// the rows, each is taken to have as many, and a last tile half full.
+// The constants are fits to 410 measured sizes, dense and grouped, of which 15 are
+// then more than 5 % off the best form, the worst 32 % (71 tokens x 8, 8 experts).
+// Some of them on GB300 (us; tokens x outputs a tile / CTAs along K):
+//      1 x 1408 x 2048      16x128/8 4.1  /4 4.2  /2 4.8  /1 5.7
+//     16 x 8192 x 8192      16x128/2 15.5  /1 17.2  64x128/2 15.2
+//    512 x 1408 x 2048      64x128 7.3  128x128 8.0  128x256 11.0
+//   2048 x 1408 x 2048      128x256 11.7  128x128 14.1  64x128 16.3
+//   8192 x 8192 x 8192      128x256 400 to 430 (the power limit's doing)  128x128 494  64x128 850
+//    4 rows of 4 experts    x 2816 x 2048: 16x128/1 7.1  /2 11.8
+//   8192 rows of 60 experts x 2816 x 2048: 128x256 80  128x128 88  64x128 113  32x128 179
 static cudaError_t fm_choose(const FmParams& p, FmChoice* choice) {
   static const struct {
-    int bn, wide, start, stage, tile, epilogue, exchange;
-  } kinds[] = {{16, 0, 3300, 150, 300, 200, 400},  {32, 0, 4000, 150, 350, 300, 1000},
-               {64, 0, 4700, 200, 500, 850, 1300}, {128, 0, 5200, 300, 1200, 1350, 2000},
-               {128, 1, 4000, 285, 1000, 0, 0},    {256, 1, 4300, 460, 1500, 0, 0}};
+    int bn, wide, start, block, tile, exchange;
+  } kinds[] = {{16, 0, 2570, 236, 905, 867},   {32, 0, 3520, 225, 981, 682},  {64, 0, 3740, 233, 1113, 1057},
+               {128, 0, 4090, 441, 1519, 963}, {128, 1, 3990, 276, 1569, 0}, {256, 1, 8250, 299, 4821, 0}};
   int capacity[9] = {};
   for (int split = 2; split <= 8; split *= 2) {
     const cudaError_t err = fm_capacity(split, &capacity[split]);
     if (err != cudaSuccess) return err;
   }
-  const int nb = (p.K + 127) / 128;
-  const long long active = p.offsets ? (p.E < p.M ? p.E : p.M) : 1, each = (p.M + active - 1) / active;
-  long long least = -1;
+  const long long nb = (p.K + 127) / 128, active = p.offsets ? (p.E < p.M ? p.E : p.M) : 1, each = (p.M + active - 1) / active;
+  const double bytes = (double)active * p.N * p.K + (double)p.M * p.K + 2.0 * p.M * p.N, least_time = 4180 + bytes / 6874;
+  double least = -1;
   for (const auto& k : kinds) {
     if (!k.wide && k.bn < 64 && each > k.bn) continue;
     const int bt = k.wide ? 128 : k.bn, br = k.wide ? k.bn : 128;
-    const long long rows = (p.N + br - 1) / br;
-    // an expert's last tile is half full on average
-    const long long some = p.offsets ? p.M / bt + active / 2 : (p.M + bt - 1) / bt;
-    const long long tiles = rows * (some > active ? some : active);
+    const long long rows = (p.N + br - 1) / br, some = p.offsets ? p.M / bt + active / 2 : (p.M + bt - 1) / bt;
+    const long long tiles = rows * (some > active ? some : active), of = k.wide ? p.N : each;
+    const double block = k.block * (0.53 + 0.47 * (of < k.bn ? (int)of : k.bn) / k.bn);
+    const int tile = k.tile + (k.wide && p.N % 8 ? 2222 : 0);
     for (int split = 1; split <= 8; split *= 2) {
       if (split > 1 && (!k.exchange || split > nb || rows * fm_token_tiles(p, k.bn) * split > capacity[split])) break;
-      const long long slots = split > 1 ? tiles : device_sm_count();
-      const long long rounds = (tiles + slots - 1) / slots;
-      const long long one = (long long)((nb + split - 1) / split) * k.stage, more = one + k.tile;
-      const long long t = k.start + one + (rounds - 1) * (more > k.epilogue ? more : k.epilogue) +
-                          (split > 1 ? k.exchange : 0);
-      if (least < 0 || t < least) {
-        least = t;
+      const long long slots = split > 1 ? tiles : device_sm_count(), rounds = (tiles + slots - 1) / slots;
+      const double one = (double)((nb + split - 1) / split) * block;
+      const double t = k.start + one + (double)(rounds - 1) * (one + tile) + (split > 1 ? k.exchange : 0);
+      const double total = (t > least_time ? t : least_time) + 0.05 * t;
+      if (least < 0 || total < least) {
+        least = total;
         *choice = {k.bn, k.wide, split};
       }
     }

@@ -176,3 +176,19 @@ def test_binding_refuses_sizes_that_the_abi_cannot_carry(calls):
             call()
         assert e.value.code == 2
     assert not calls
+
+
+def test_diagnosed_product_refuses_unknown_flags(L):
+    a = [v for k, v in MATMUL.items()]
+    for flags in (16, 31, 1 << 31):
+        assert L.qmoe_fp8_matmul_diagnosed(*a, 1, flags, None) == 1
+    assert call(L.qmoe_fp8_matmul, MATMUL, dict(K=40)) == 1
+
+
+def test_variant_query_refuses(L):
+    import ctypes
+    v = (ctypes.c_int * 3)()
+    for a in ((0, 2, 4, 8, 64), (1, 0, 4, 8, 64), (1, 2, 0, 8, 64), (1, 2, 4, 0, 64), (1, 2, 4, 8, 40)):
+        assert L.qmoe_fp8_matmul_variant(*a, v) == 1
+    assert L.qmoe_fp8_matmul_variant(1, 2, 4, 8, 64, None) == 1
+    assert L.qmoe_fp8_matmul_variant(1, 257, 4, 8, 64, v) == 2 and L.qmoe_fp8_matmul_variant(0, 1, BIG, 8, 64, v) == 2
