@@ -21,6 +21,8 @@ namespace qmoe {
 constexpr int kSortCluster = 8;
 constexpr int kSortAhead = 8;  // loads in flight a thread
 
+// BITS: of a bin's number.
+template <int BITS>
 __global__ void __launch_bounds__(1024) sort_experts_kernel(const int32_t* __restrict__ ids, int A, int E,
                                                             int32_t* __restrict__ offsets, int32_t* __restrict__ perm,
                                                             int32_t* __restrict__ pos) {
@@ -72,7 +74,8 @@ __global__ void __launch_bounds__(1024) sort_experts_kernel(const int32_t* __res
     if (C == 1) {
       all = s_total[tid];
     } else {
-      for (int r = 0; r < C; ++r) {
+#pragma unroll
+      for (int r = 0; r < kSortCluster; ++r) {
         const uint32_t c = __float_as_uint(ld_dsmem_f32(reinterpret_cast<const float*>(&s_total[tid]), r));
         before += r < rank ? c : 0;
         all += c;
@@ -95,11 +98,11 @@ __global__ void __launch_bounds__(1024) sort_experts_kernel(const int32_t* __res
     s_start[tid] = start + before;
   }
   __syncthreads();
-  const int bits = 32 - __clz(E);
   walk([&](int i, uint32_t e) {
     const bool in = e != ~0u;
     uint32_t peers = __ballot_sync(0xffffffffu, in);
-    for (int b = 0; b < bits; ++b) {
+#pragma unroll
+    for (int b = 0; b < BITS; ++b) {
       const uint32_t one = __ballot_sync(0xffffffffu, e >> b & 1);
       peers &= e >> b & 1 ? one : ~one;
     }
@@ -132,7 +135,7 @@ cudaError_t launch_sort_experts(const int32_t* ids, int A, int E, int32_t* offse
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, sort_experts_kernel, ids, A, E, offsets, perm, pos);
+  return cudaLaunchKernelEx(&cfg, E < 64 ? sort_experts_kernel<6> : sort_experts_kernel<9>, ids, A, E, offsets, perm, pos);
 }
 
 // ----------------------------------------------------------------- dispatch
