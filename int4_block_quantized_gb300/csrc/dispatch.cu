@@ -17,13 +17,15 @@ namespace qmoe {
 // where its expert starts, plus the expert's assignments in earlier warps and
 // rounds, plus those in lower lanes.  Lanes of one expert find each other by a
 // vote on each bit of its number (match_any goes through the experts one by one).
-// Bin E: no expert.  Bound by latency: the chain of both walks and the barriers.
-constexpr int kSortCluster = 8;
+// Bin E: no expert.  Bound by latency: the chain of both walks and the barriers, and
+// for many assignments by the integer instructions of the votes, on few SMs: 131072
+// to 256 experts take 12.1 us on 16 CTAs, 17.6 on 8 (with match_any 23).
+constexpr int kSortCluster = 8, kSortWide = 16;  // CTAs; more than 8 are not promised, so they are asked for
 constexpr int kSortAhead = 8;  // loads in flight a thread
 
 // BITS: of a bin's number.
 template <int BITS>
-__global__ void __launch_bounds__(1024) sort_experts_kernel(const int32_t* __restrict__ ids, int A, int E,
+__global__ void __launch_bounds__(1024, 1) sort_experts_kernel(const int32_t* __restrict__ ids, int A, int E,
                                                             int32_t* __restrict__ offsets, int32_t* __restrict__ perm,
                                                             int32_t* __restrict__ pos) {
   extern __shared__ uint32_t s_hist[];  // [warps][E + 1]
@@ -74,12 +76,13 @@ __global__ void __launch_bounds__(1024) sort_experts_kernel(const int32_t* __res
     if (C == 1) {
       all = s_total[tid];
     } else {
+      for (int r0 = 0; r0 < C; r0 += kSortCluster)
 #pragma unroll
-      for (int r = 0; r < kSortCluster; ++r) {
-        const uint32_t c = __float_as_uint(ld_dsmem_f32(reinterpret_cast<const float*>(&s_total[tid]), r));
-        before += r < rank ? c : 0;
-        all += c;
-      }
+        for (int r = r0; r < r0 + kSortCluster; ++r) {
+          const uint32_t c = __float_as_uint(ld_dsmem_f32(reinterpret_cast<const float*>(&s_total[tid]), r));
+          before += r < rank ? c : 0;
+          all += c;
+        }
     }
   }
   // exclusive sum over the bins (at most 257, threads of the first nine warps)
@@ -121,21 +124,46 @@ __global__ void __launch_bounds__(1024) sort_experts_kernel(const int32_t* __res
 
 cudaError_t launch_sort_experts(const int32_t* ids, int A, int E, int32_t* offsets, int32_t* perm, int32_t* pos,
                                 cudaStream_t st) {
-  const int C = A > 4096 ? kSortCluster : 1, threads = A > 1024 ? 1024 : 320;  // at least E + 1
+  const int threads = A > 1024 ? 1024 : 320;  // at least E + 1
+  auto kernel = E < 64 ? sort_experts_kernel<6> : sort_experts_kernel<9>;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(C);
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = (size_t)(threads / 32) * (E + 1) * 4;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = C;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
+  auto clusters_of = [&](int C) {
+    cfg.gridDim = dim3(C);
+    attr[0].val.clusterDim.x = C;
+  };
+  int C = A > 4096 ? kSortCluster : 1;
+  if (A > 32768) {
+    static int wide[64][2] = {};  // 1: such clusters fit the device, 2: they do not
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    int& known = wide[dev][E < 64];
+    if (!known) {
+      int n = 0;
+      clusters_of(kSortWide);
+      cfg.numAttrs = 1;
+      cfg.dynamicSmemBytes = 32 * (kMaxExperts + 1) * 4;
+      if ((err = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess ||
+          (err = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg)) != cudaSuccess)
+        return err;
+      cfg.dynamicSmemBytes = (size_t)32 * (E + 1) * 4;
+      known = n > 0 ? 1 : 2;
+    }
+    if (known == 1) C = kSortWide;
+  }
+  clusters_of(C);
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, E < 64 ? sort_experts_kernel<6> : sort_experts_kernel<9>, ids, A, E, offsets, perm, pos);
+  return cudaLaunchKernelEx(&cfg, kernel, ids, A, E, offsets, perm, pos);
 }
 
 // ----------------------------------------------------------------- dispatch
