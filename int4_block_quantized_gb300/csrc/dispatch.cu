@@ -174,7 +174,7 @@ static dim3 rows_grid(size_t threads) {
 }
 
 // A token's row is read once and written to its k places, 16 bytes a thread.
-// Bound by HBM.
+// Bound by HBM: 16384 tokens of 2048 bf16 to 8 places each in 92 us, 6.4 TB/s.
 __global__ void __launch_bounds__(256) dispatch_kernel(const uint4* __restrict__ x, int T, int units, int k,
                                                        const int32_t* __restrict__ pos, uint4* __restrict__ xs) {
   pdl_wait();
@@ -242,7 +242,8 @@ __device__ __forceinline__ void store8(void* base, size_t i, const float (&v)[8]
 
 // out[t] = residual[t] + sum_j w[t, j] ys[pos[t, j]], fp32 in this order, rounded
 // once.  A thread takes 8 columns of a token, four assignments' loads in flight.
-// Bound by HBM.
+// Bound by HBM: 16384 tokens of 2048 bf16, 8 each, in 101 us, 6.6 TB/s (108 with one
+// load in flight).
 template <typename Y, typename O>
 __global__ void __launch_bounds__(256) combine_kernel(const void* __restrict__ ys, const int32_t* __restrict__ pos,
                                                       const float* __restrict__ wt, const void* residual, int T, int H,
@@ -285,7 +286,8 @@ __global__ void __launch_bounds__(256) combine_kernel(const void* __restrict__ y
 // dys[pos[t, j]] = w[t, j] dout[t], dw[t, j] = sum_h dout[t, h] ys[pos[t, j], h] (fp32).
 // One warp per assignment, four steps of 256 columns in flight; a token's warps
 // are neighbours, so dout comes from L1 or L2 but once.  dys may be ys: a thread
-// has read what it writes.  Bound by HBM.
+// has read what it writes.  Bound by HBM: 16384 x 8 rows of 2048 bf16 in 167 us,
+// 6.7 TB/s.
 template <typename Y, typename O>
 __global__ void __launch_bounds__(256) combine_backward_kernel(const void* __restrict__ dout, const void* ys,
                                                                const int32_t* __restrict__ pos,

@@ -25,7 +25,8 @@ static dim3 fp8_grid(size_t work) {
 // -------------------------------------------------------------- activations
 // Eight lanes take a block, 16 elements each (a row's last block may have
 // fewer: its other lanes bring zeros).  With places, a token is quantised once
-// and written to each of its k rows.  Bound by HBM.
+// and written to each of its k rows.  Bound by HBM and, nearly as much, by its
+// eleven instructions an element: 8192 x 4096 bf16 in 17.7 us, 5.7 TB/s.
 template <typename T, bool PLACES>
 __global__ void __launch_bounds__(256) fp8_rows_kernel(const void* __restrict__ x, int M, int K,
                                                        const int32_t* __restrict__ pos, int k,
@@ -60,7 +61,9 @@ __global__ void __launch_bounds__(256) fp8_rows_kernel(const void* __restrict__ 
   }
 }
 
-// silu(g) * u of h [M, 2 I] (gate, then up), in fp32, quantised as above.
+// silu(g) * u of h [M, 2 I] (gate, then up), in fp32, quantised as above.  Bound by
+// instructions, the exponential's and the quantiser's: 8192 x 1408 bf16 in 13.0 us,
+// 4.5 TB/s (12.0 with an exponential that loses accuracy far from 0).
 template <typename T>
 __global__ void __launch_bounds__(256) fp8_swiglu_kernel(const void* __restrict__ h, int M, int I,
                                                          uint8_t* __restrict__ codes, float* __restrict__ scales) {
@@ -89,9 +92,11 @@ __global__ void __launch_bounds__(256) fp8_swiglu_kernel(const void* __restrict_
 
 // ------------------------------------------------------------------ weights
 // One CTA per 128 x 128 block: a thread takes 16 columns of four rows, which it
-// keeps as they came until the block's maximum is known.  Bound by HBM.
+// keeps as they came until the block's maximum is known.  Five CTAs an SM, so that
+// others load while one reduces or writes (three: 91 us, four: 84).  Bound by HBM:
+// 60 x 1408 x 2048 fp16 in 81 us, 6.4 TB/s.
 template <typename T>
-__global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 4) fp8_weights_kernel(const void* __restrict__ w, int N, int K,
+__global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 5) fp8_weights_kernel(const void* __restrict__ w, int N, int K,
                                                           uint8_t* __restrict__ codes, float* __restrict__ scales) {
   pdl_wait();
   const uint32_t nb = (uint32_t)(K + 127) / 128, rb = (uint32_t)(N + 127) / 128;
@@ -125,7 +130,8 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 4) fp8_weights_kerne
 }
 
 // ------------------------------------------------------------------- reader
-// code * scale in fp32, rounded once to T.  BR: rows that share a scale.
+// code * scale in fp32, rounded once to T.  BR: rows that share a scale.  Bound by
+// HBM: 60 x 1408 x 2048 to fp16 in 78 us, 6.7 TB/s.
 template <typename T, int BR>
 __global__ void __launch_bounds__(256) fp8_dequant_kernel(const uint8_t* __restrict__ codes,
                                                           const float* __restrict__ scales, int E, int N, int K,

@@ -8,12 +8,19 @@
 // block of 128 k at a time into a buffer of tensor memory of its own; eight warps
 // read it from there, multiply with the block's scales and add to sums that they
 // keep in registers, while the next block is multiplied into the next buffer.
-// Weight rows are the MMA's M = 128 operand and tokens its N, so that a few
-// tokens cost a narrow MMA; a tile of weight rows lies within one scale block,
-// so a block's scales are a vector over the tokens, which two warps put together
-// in shared memory.  Tensor memory is read in the layout of 8 x 8 fragments, in
-// which a thread's neighbouring values are neighbouring tokens: one pair of
-// scales serves eight values, and packed fp32 arithmetic does two at a time.
+// Two forms, by which operand the MMA has as its M = 128:
+//   few tokens   128 weight rows (one scale block) by 16 to 128 tokens, so that a
+//                few tokens cost a narrow MMA; K is split over the CTAs of a
+//                cluster where there are few tiles.  Bound by the weights' bytes:
+//                256 rows of 60 experts x 2816 x 2048 run at 6.8 TB/s; one token's
+//                four experts take 7.1 us for 3.4 us of bytes, the rest is a start
+//                of 3 us (launch, first copies, last block).
+//   many tokens  128 tokens by 128 or 256 weight rows.  A block of 128 x 256 takes
+//                860 cycles: its 48 KB come at 62 bytes a cycle to an SM (780
+//                cycles), reading, scaling and adding takes 450 a warp, which
+//                two buffers leave in a chain with the MMA's 515 and 500 of
+//                hand-overs.  8192^3 in 400 to 430 us, 2.6 to 2.75 PFLOP/s at the
+//                power limit (clocks down to about 1.6 GHz).
 #include <cuda.h>
 
 #include "fp8.cuh"
@@ -22,8 +29,12 @@
 
 namespace qmoe {
 
-// Warp 0 copies codes, 1 issues MMAs, 2 and 3 prepare scales, 4 to 11 scale and
-// add the blocks' sums and write y.
+// Few tokens.  A block's scales are a vector over the tokens, which two warps put
+// together in shared memory.  Tensor memory is read in the layout of 8 x 8
+// fragments, in which a thread's neighbouring values are neighbouring tokens: one
+// pair of scales serves eight values, and packed fp32 arithmetic does two at a
+// time.  Warp 0 copies codes, 1 issues MMAs, 2 and 3 prepare scales, 4 to 11 scale
+// and add the blocks' sums and write y.
 constexpr int kFmThreads = 384;
 constexpr uint32_t kFmSmem = 232448;  // 227 KB
 constexpr uint32_t kFmBars = 1024;
@@ -548,14 +559,15 @@ __global__ void __launch_bounds__(kFmThreads, 1)
   }
 }
 
-
 // ------------------------------------------------------------- many tokens
 // Here 128 tokens are the MMA's M operand and BN weight rows its N: a thread of
 // the warps that add has a token to itself, so that a block's scale is one number
 // to it, and reads tensor memory in whole rows (32x32b, measured at 18 cycles for
-// 32 columns of a warp; fragments take 32).  Two warps to each lane quadrant, a
-// half of the columns each.  Warp 0 copies codes, 1 issues MMAs, 2 prepares
-// scales, 3 to 10 add and write y.
+// 32 columns of a warp; fragments take 32), 16 columns ahead of its sums.  Warp 0
+// copies codes, 1 issues MMAs, 2 prepares scales, 4 to 11 add and write y, two to
+// each lane quadrant with a half of the columns each.  Measured at 8192^3 and not
+// kept (400 to 415 us): pairs of CTAs (cta_group::2) 415, a buffer handed back by
+// halves 423 to 450, sixteen adding warps 497, three stages 432.
 constexpr int kFwThreads = 384;
 // 256 outputs: the adding warps hold 128 sums a thread and take registers of the
 // others: 256 x 208 + 128 x 88 = 384 x 168, which the launch has (checked there).
@@ -592,6 +604,10 @@ __device__ __forceinline__ void fw_wait(uint32_t (&r)[16]) {
                :
                : "memory");
 }
+
+struct FwTile : FmTile {
+  int n0, n1;  // outputs
+};
 
 template <int BN>
 __global__ void __launch_bounds__(kFwThreads, 1)
@@ -650,7 +666,17 @@ __global__ void __launch_bounds__(kFwThreads, 1)
   pdl_trigger();
   fm_table<BT>(p, tab, s_sum);
 
-  const int tiles = tab.first[p.E] * p.row_tiles, nb = (p.K + 127) / 128;
+  // The tiles of a last round that fewer than half of the CTAs would have are
+  // dealt in halves of their outputs (8192^3: 14 rounds of which the last is half as long).
+  const int tiles = tab.first[p.E] * p.row_tiles, nb = (p.K + 127) / 128, rest = tiles % (int)gridDim.x;
+  const int whole = BN == 256 && 2 * rest <= (int)gridDim.x ? tiles - rest : tiles, parts = 2 * tiles - whole;
+  auto part = [&](int v) {
+    const int h = v - whole;
+    FwTile f = {fm_tile<BT>(p, tab, h < 0 ? v : whole + h / 2)};
+    f.n0 = f.rt * BN + (h > 0 && h % 2 ? BN / 2 : 0);
+    f.n1 = min(p.N, f.n0 + (h < 0 ? BN : BN / 2));
+    return f;  // (an empty half where the outputs end before it)
+  };
   auto stalled = [&](uint32_t role) { return (p.stall & role) && !fm_wait(never, 0, p, s_abort); };
   if (warp >= 4) {
     if (BN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFwManyRegs));
@@ -659,9 +685,10 @@ __global__ void __launch_bounds__(kFwThreads, 1)
     float* buf = reinterpret_cast<float*>(outbuf) + (warp - 4) * 32 * 17;
     int n = 0, it = 0;
     bool ok = !stalled(QMOE_DIAG_STALL_FP8_OUTPUT);
-    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-      const FmTile f = fm_tile<BT>(p, tab, t);
-      const int n0 = f.rt * BN + set * (BN / 2), cols = p.N - n0;  // this warp's columns
+    for (int t = blockIdx.x; t < parts && ok; t += gridDim.x) {
+      const FwTile f = part(t);
+      if (f.n1 <= f.n0) continue;
+      const int n0 = f.n0 + set * (BN / 2), cols = f.n1 - n0;      // this warp's columns
       const int m0 = f.m0 + qd * 32;                               // and tokens
       const bool live = cols > 0 && m0 < f.m1;
       float acc[P::kC][16];
@@ -777,9 +804,10 @@ __global__ void __launch_bounds__(kFwThreads, 1)
       uint32_t ph = 0;
       bool ok = !stalled(QMOE_DIAG_STALL_FP8_CODES);
       const uint32_t el = elect_lane();
-      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-        const FmTile f = fm_tile<BT>(p, tab, t);
-        const int xb = (f.m1 - f.m0 + 63) / 64, wb = (min(BN, p.N - f.rt * BN) + 63) / 64;  // copies of 64 rows
+      for (int t = blockIdx.x; t < parts && ok; t += gridDim.x) {
+        const FwTile f = part(t);
+        if (f.n1 <= f.n0) continue;
+        const int xb = (f.m1 - f.m0 + 63) / 64, wb = (f.n1 - f.n0 + 63) / 64;  // copies of 64 rows
         for (int c = 0; c < nb; ++c, ++it) {
           if (it >= S) ok = fm_wait(&empty[s], ph ^ 1u, p, s_abort);
           if (!ok) break;
@@ -788,7 +816,7 @@ __global__ void __launch_bounds__(kFwThreads, 1)
             mbar_arrive_expect_tx(&full[s], (xb + wb) * 64 * 128);
             for (int i = 0; i < xb; ++i) tma_load_2d(st + i * 8192, &tm_x, c * 128, f.m0 + 64 * i, &full[s]);
             for (int i = 0; i < wb; ++i)
-              tma_load_2d(st + P::kA + i * 8192, &tm_w, c * 128, f.e * p.N + f.rt * BN + 64 * i, &full[s]);
+              tma_load_2d(st + P::kA + i * 8192, &tm_w, c * 128, f.e * p.N + f.n0 + 64 * i, &full[s]);
           }
           __syncwarp();
           if (++s == S) {
@@ -804,9 +832,10 @@ __global__ void __launch_bounds__(kFwThreads, 1)
       uint32_t ph = 0;
       bool ok = !stalled(QMOE_DIAG_STALL_FP8_MMA), issued = false;
       const uint32_t el = elect_lane();
-      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-        const FmTile f = fm_tile<BT>(p, tab, t);
-        const int cols = (min(BN, p.N - f.rt * BN) + 15) & ~15;
+      for (int t = blockIdx.x; t < parts && ok; t += gridDim.x) {
+        const FwTile f = part(t);
+        if (f.n1 <= f.n0) continue;
+        const int cols = (f.n1 - f.n0 + 15) & ~15;
         const uint32_t idesc = 1u << 4 | (uint32_t)(cols >> 3) << 17 | (uint32_t)(BT >> 4) << 24;
         for (int c = 0; c < nb; ++c, ++n) {
           const int b = n % NB;
@@ -817,7 +846,7 @@ __global__ void __launch_bounds__(kFwThreads, 1)
           const uint32_t st = (smem_u32(ring + s * P::kStage) >> 4) & 0x3FFFu;  // a descriptor's address field
           const uint32_t da = st | 1u << 16, db = (st + (P::kA >> 4)) | 1u << 16;
           const int left = p.K - c * 128;
-  #pragma unroll
+#pragma unroll
           for (int j = 0; j < 4; ++j) {
             if (32 * j >= left) break;
             mma_f8(el, tmem + b * BN, da + 2 * j, db + 2 * j, idesc, j > 0);
@@ -840,17 +869,18 @@ __global__ void __launch_bounds__(kFwThreads, 1)
       int it = 0;
       const int rb = (p.N + 127) / 128;
       bool ok = !stalled(QMOE_DIAG_STALL_FP8_SCALES);
-      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-        const FmTile f = fm_tile<BT>(p, tab, t);
-        const float* ws = p.ws + ((size_t)f.e * rb + f.rt * P::kHalves) * nb;
+      for (int t = blockIdx.x; t < parts && ok; t += gridDim.x) {
+        const FwTile f = part(t);
+        if (f.n1 <= f.n0) continue;
+        const float* ws = p.ws + ((size_t)f.e * rb + f.n0 / 128) * nb;
         for (int c = 0; c < nb; c += 4, ++it) {
           const int q = it % SQ;
           float v[4][4] = {}, w[P::kHalves][4];
-  #pragma unroll
+#pragma unroll
           for (int h = 0; h < P::kHalves; ++h)
-  #pragma unroll
-            for (int j = 0; j < 4; ++j) w[h][j] = f.rt * P::kHalves + h < rb && c + j < nb ? ws[h * nb + c + j] : 0.f;
-  #pragma unroll
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[h][j] = f.n0 / 128 + h < rb && c + j < nb ? ws[h * nb + c + j] : 0.f;
+#pragma unroll
           for (int i = 0; i < 4; ++i)
             if (f.m0 + 32 * i + lane < f.m1) {
               const float* xs = p.xs + (size_t)(f.m0 + 32 * i + lane) * nb + c;
@@ -858,18 +888,18 @@ __global__ void __launch_bounds__(kFwThreads, 1)
                 const float4 u = *reinterpret_cast<const float4*>(xs);
                 v[i][0] = u.x, v[i][1] = u.y, v[i][2] = u.z, v[i][3] = u.w;
               } else {
-  #pragma unroll
+#pragma unroll
                 for (int j = 0; j < 4; ++j) v[i][j] = c + j < nb ? xs[j] : 0.f;
               }
             }
           if (it >= SQ) ok = fm_wait(&sc_free[q], (it / SQ - 1) & 1, p, s_abort);
           if (!ok) break;
           float* out = scales + q * 4 * P::kHalves * 128;
-  #pragma unroll
+#pragma unroll
           for (int j = 0; j < 4; ++j)
-  #pragma unroll
+#pragma unroll
             for (int h = 0; h < P::kHalves; ++h)
-  #pragma unroll
+#pragma unroll
               for (int i = 0; i < 4; ++i) out[(j * P::kHalves + h) * 128 + 32 * i + lane] = v[i][j] * w[h][j];
           __syncwarp();
           if (lane == 0) mbar_arrive(&sc_full[q]);
