@@ -627,6 +627,10 @@ def qmoe_mx_untile_scales(scales, R, K):
 # call that makes its own output leaves them undefined.  Checked and run like the
 # microscaled calls above.
 
+# Each tensor's check is written out where it passes and made again, by
+# _mx_check2, where it does not, to say what is wrong (a call of _mx_check2 takes
+# 0.3 us, and a product has six tensors).
+
 _F32 = torch.float32
 _I32 = torch.int32
 _ROWS_MAX = 1 << 30
@@ -652,11 +656,11 @@ def _fp8_out(codes, scales, shape, sshape, x, dev, where):
     """(codes, scales) to write to: the caller's, or new ones."""
     if codes is None:
         codes = torch.empty(shape, dtype=_U8, device=x.device)
-    else:
+    elif codes.get_device() != dev or codes.dtype is not _U8 or codes.shape != shape or not codes.is_contiguous():
         _mx_check2(codes, dev, _U8, shape, where, "codes")
     if scales is None:
         scales = torch.empty(sshape, dtype=_F32, device=x.device)
-    else:
+    elif scales.get_device() != dev or scales.dtype is not _F32 or scales.shape != sshape or not scales.is_contiguous():
         _mx_check2(scales, dev, _F32, sshape, where, "scales")
     return codes, scales
 
@@ -669,7 +673,8 @@ def _places(pos, T, dev, where):
     k = shape[1]
     if T * k > _ROWS_MAX:
         raise QMoEError(2, "%s: %d x %d assignments, at most 2^30" % (where, T, k))
-    _mx_check2(pos, dev, _I32, shape, where, "pos")
+    if pos.get_device() != dev or dev < 0 or pos.dtype is not _I32 or not pos.is_contiguous():
+        _mx_check2(pos, dev, _I32, shape, where, "pos")
     return k
 
 
@@ -679,7 +684,9 @@ def qmoe_fp8_quantize(x, pos=None, codes=None, scales=None):
     where = "qmoe_fp8_quantize"
     T, K = _mx_size(x, where)
     dev = x.get_device()
-    dt = _fp8_in(x, dev, where, "x")
+    dt = _MX_DT.get(x.dtype)
+    if dt is None or dev < 0 or not x.is_contiguous():
+        _fp8_in(x, dev, where, "x")
     rows, k, pp = T, 0, None
     if pos is not None:
         k = _places(pos, T, dev, where)
@@ -724,17 +731,22 @@ def qmoe_fp8_dequant(codes, scales, dtype=torch.bfloat16, out=None):
     """Values (fp16, bf16 or fp32) of an FP8 tensor; whether a scale covers one row
     or 128 is read from the scales' shape."""
     where = "qmoe_fp8_dequant"
-    shape = tuple(codes.shape)
-    if len(shape) not in (2, 3) or len(scales.shape) != len(shape):
-        _bad(where, "codes %s with scales %s" % (shape, tuple(scales.shape)))
-    E, N, K = (1,) * (3 - len(shape)) + shape
+    shape = codes.shape
+    dims = len(shape)
+    if dims not in (2, 3) or len(scales.shape) != dims:
+        _bad(where, "codes %s with scales %s" % (tuple(shape), tuple(scales.shape)))
+    N, K = shape[-2], shape[-1]
+    E = shape[0] if dims == 3 else 1
     dev, dt = codes.get_device(), _MX_DT.get(dtype)
     if dt is None:
         _bad(where, "unsupported output type %s" % dtype)
     _fp8_size(E * N, K, where)
-    _mx_check2(codes, dev, _U8, shape, where, "codes")
+    if dev < 0 or codes.dtype is not _U8 or not codes.is_contiguous():
+        _mx_check2(codes, dev, _U8, shape, where, "codes")
     rows = 1 if scales.shape[-2] == N else 128
-    _mx_check2(scales, dev, _F32, shape[:-2] + ((N + rows - 1) // rows, (K + 127) // 128), where, "scales")
+    sshape = ((N + rows - 1) // rows, (K + 127) // 128) if dims == 2 else (E, (N + rows - 1) // rows, (K + 127) // 128)
+    if scales.get_device() != dev or scales.dtype is not _F32 or scales.shape != sshape or not scales.is_contiguous():
+        _mx_check2(scales, dev, _F32, sshape, where, "scales")
     if out is None:
         out = torch.empty(shape, dtype=dtype, device=codes.device)
     else:
@@ -759,26 +771,31 @@ def qmoe_fp8_matmul(x_codes, x_scales, w_codes, w_scales, dtype=torch.bfloat16, 
     E = 1
     if offsets is not None:
         E = offsets.numel() - 1
-        _mx_check2(offsets, dev, _I32, (E + 1,), where, "offsets")
+        if offsets.get_device() != dev or offsets.dtype is not _I32 or len(offsets.shape) != 1 or not offsets.is_contiguous():
+            _mx_check2(offsets, dev, _I32, (E + 1,), where, "offsets")
         op = offsets.data_ptr()
-    if len(shape) == 3 and shape[0] == E or len(shape) == 2 and E == 1:
-        N = shape[-2]
-    else:
-        N = 0
+    dims = len(shape)
+    N = shape[-2] if dims == 3 and shape[0] == E or dims == 2 and E == 1 else 0
     if dt is None or N < 1 or E < 1 or shape[-1] != K:
         _bad(where, "x %s, W %s, %s experts, result in %s" % (tuple(x_codes.shape), tuple(shape), E, dtype))
     if E > 256:
         raise QMoEError(2, "%s: %d experts, at most 256" % (where, E))
     _fp8_size(M, K, where)
-    _fp8_size(E * N, K, where)
+    if E * N > _ROWS_MAX:
+        _fp8_size(E * N, K, where)
     nb, rb = (K + 127) // 128, (N + 127) // 128
-    _mx_check2(x_codes, dev, _U8, x_codes.shape, where, "x_codes")
-    _mx_check2(x_scales, dev, _F32, (M, nb), where, "x_scales")
-    _mx_check2(w_codes, dev, _U8, shape, where, "w_codes")
-    _mx_check2(w_scales, dev, _F32, (E, rb, nb) if len(shape) == 3 else (rb, nb), where, "w_scales")
+    sshape = (E, rb, nb) if dims == 3 else (rb, nb)
+    if not (dev >= 0 and x_codes.dtype is _U8 and x_codes.is_contiguous() and
+            x_scales.get_device() == dev and x_scales.dtype is _F32 and x_scales.shape == (M, nb) and x_scales.is_contiguous() and
+            w_codes.get_device() == dev and w_codes.dtype is _U8 and w_codes.is_contiguous() and
+            w_scales.get_device() == dev and w_scales.dtype is _F32 and w_scales.shape == sshape and w_scales.is_contiguous()):
+        _mx_check2(x_codes, dev, _U8, (M, K), where, "x_codes")
+        _mx_check2(x_scales, dev, _F32, (M, nb), where, "x_scales")
+        _mx_check2(w_codes, dev, _U8, shape, where, "w_codes")
+        _mx_check2(w_scales, dev, _F32, sshape, where, "w_scales")
     if out is None:
         out = torch.empty((M, N), dtype=dtype, device=x_codes.device)
-    else:
+    elif out.get_device() != dev or out.dtype is not dtype or out.shape != (M, N) or not out.is_contiguous():
         _mx_check2(out, dev, dtype, (M, N), where, "out")
     if status is not None:
         _mx_check(status, dev, _I32, 1, where, "status")
@@ -822,10 +839,12 @@ def qmoe_sort_experts(ids, E):
         raise QMoEError(2, "%s: %d experts, %d assignments: at most 256 and 2^30" % (where, E, T * k))
     if E < 1 or T < 1 or k < 1:
         _bad(where, "ids %s, %d experts" % ((T, k), E))
-    _mx_check2(ids, dev, _I32, (T, k), where, "ids")
-    offsets = torch.empty(E + 1, dtype=_I32, device=ids.device)
-    perm = torch.empty(T * k, dtype=_I32, device=ids.device)
-    pos = torch.empty((T, k), dtype=_I32, device=ids.device)
+    if dev < 0 or ids.dtype is not _I32 or not ids.is_contiguous():
+        _mx_check2(ids, dev, _I32, (T, k), where, "ids")
+    at = ids.device
+    offsets = torch.empty(E + 1, dtype=_I32, device=at)
+    perm = torch.empty(T * k, dtype=_I32, device=at)
+    pos = torch.empty((T, k), dtype=_I32, device=at)
     _mx_call(dev, lib().qmoe_sort_experts, where, ids.data_ptr(), T, k, E, offsets.data_ptr(), perm.data_ptr(),
              pos.data_ptr())
     return offsets, perm, pos
@@ -848,7 +867,7 @@ def qmoe_dispatch(x, pos, out=None):
     k = _places(pos, T, dev, where)
     if out is None:
         out = torch.empty((T * k, H), dtype=x.dtype, device=x.device)
-    else:
+    elif out.get_device() != dev or out.dtype is not x.dtype or out.shape != (T * k, H) or not out.is_contiguous():
         _mx_check2(out, dev, x.dtype, (T * k, H), where, "out")
     _mx_call(dev, lib().qmoe_dispatch, where, x.data_ptr(), dt, T, H, k, pos.data_ptr(), out.data_ptr())
     return out
@@ -856,8 +875,10 @@ def qmoe_dispatch(x, pos, out=None):
 
 def _combine(where, ys, pos, w, residual, out):
     rows, H = _mx_size(ys, where)
-    dev = ys.get_device()
-    dt = _fp8_in(ys, dev, where, "ys")
+    dev, yt = ys.get_device(), ys.dtype
+    dt = _MX_DT.get(yt)
+    if dt is None or dev < 0 or not ys.is_contiguous():
+        _fp8_in(ys, dev, where, "ys")
     if len(pos.shape) != 2:
         _bad(where, "pos: wants [T, k], got %s" % (tuple(pos.shape),))
     T = pos.shape[0]
@@ -867,18 +888,24 @@ def _combine(where, ys, pos, w, residual, out):
         _bad(where, "ys: wants %d rows, got %d" % (T * k, rows))
     wp = rp = None
     if w is not None:
-        _mx_check2(w, dev, _F32, (T, k), where, "w")
+        if w.get_device() != dev or w.dtype is not _F32 or w.shape != (T, k) or not w.is_contiguous():
+            _mx_check2(w, dev, _F32, (T, k), where, "w")
         wp = w.data_ptr()
     if residual is not None:
-        ot = _fp8_in(residual, dev, where, "residual")
-        _mx_check2(residual, dev, residual.dtype, (T, H), where, "residual")
+        yt = residual.dtype
+        ot = _MX_DT.get(yt)
+        if ot is None or residual.get_device() != dev or residual.shape != (T, H) or not residual.is_contiguous():
+            _fp8_in(residual, dev, where, "residual")
+            _mx_check2(residual, dev, yt, (T, H), where, "residual")
         rp = residual.data_ptr()
+    elif out is not None:
+        ot, yt = _fp8_in(out, dev, where, "out"), out.dtype
     else:
-        ot = dt if out is None else _fp8_in(out, dev, where, "out")
+        ot = dt
     if out is None:
-        out = torch.empty((T, H), dtype=ys.dtype if residual is None else residual.dtype, device=ys.device)
-    else:
-        _mx_check2(out, dev, out.dtype if residual is None else residual.dtype, (T, H), where, "out")
+        out = torch.empty((T, H), dtype=yt, device=ys.device)
+    elif out.get_device() != dev or out.dtype is not yt or out.shape != (T, H) or not out.is_contiguous():
+        _mx_check2(out, dev, yt, (T, H), where, "out")
     _mx_call(dev, lib().qmoe_combine, where, ys.data_ptr(), dt, pos.data_ptr(), wp, rp, T, H, k, out.data_ptr(), ot)
     return out
 
@@ -905,14 +932,16 @@ def qmoe_combine_backward(dout, ys, pos, w=None, dys=None, dw=None):
     dt, yt = _fp8_in(dout, dev, where, "dout"), _fp8_in(ys, dev, where, "ys")
     _fp8_rows(T, H, where)
     k = _places(pos, T, dev, where)
-    _mx_check2(ys, dev, ys.dtype, (T * k, H), where, "ys")
+    if ys.shape != (T * k, H):
+        _mx_check2(ys, dev, ys.dtype, (T * k, H), where, "ys")
     wp = None
     if w is not None:
-        _mx_check2(w, dev, _F32, (T, k), where, "w")
+        if w.get_device() != dev or w.dtype is not _F32 or w.shape != (T, k) or not w.is_contiguous():
+            _mx_check2(w, dev, _F32, (T, k), where, "w")
         wp = w.data_ptr()
     if dys is None:
         dys = torch.empty_like(ys)
-    else:
+    elif dys.get_device() != dev or dys.dtype is not ys.dtype or dys.shape != (T * k, H) or not dys.is_contiguous():
         _mx_check2(dys, dev, ys.dtype, (T * k, H), where, "dys")
     if dw is None:
         dw = torch.empty((T, k), dtype=_F32, device=dout.device)
