@@ -16,11 +16,12 @@
 //                four experts take 7.1 us for 3.4 us of bytes, the rest is a start
 //                of 3 us (launch, first copies, last block).
 //   many tokens  128 tokens by 128 or 256 weight rows.  A block of 128 x 256 takes
-//                860 cycles: its 48 KB come at 62 bytes a cycle to an SM (780
-//                cycles), reading, scaling and adding takes 450 a warp, which
-//                two buffers leave in a chain with the MMA's 515 and 500 of
-//                hand-overs.  8192^3 in 400 to 430 us, 2.6 to 2.75 PFLOP/s at the
-//                power limit (clocks down to about 1.6 GHz).
+//                860 cycles: a copy takes about 1700 to arrive and four stages of
+//                48 KB fit, so that one is there every 780; reading, scaling and
+//                adding takes 450 a warp, which two buffers leave in a chain with
+//                the MMA's 515 and the hand-overs.  8192^3 in 400 to 415 us, 2.7
+//                PFLOP/s, and 455 where it runs for seconds (the power limit,
+//                1360 W, takes the clocks down to 1.67 GHz).
 #include <cuda.h>
 
 #include "fp8.cuh"
@@ -566,8 +567,9 @@ __global__ void __launch_bounds__(kFmThreads, 1)
 // 32 columns of a warp; fragments take 32), 16 columns ahead of its sums.  Warp 0
 // copies codes, 1 issues MMAs, 2 prepares scales, 4 to 11 add and write y, two to
 // each lane quadrant with a half of the columns each.  Measured at 8192^3 and not
-// kept (400 to 415 us): pairs of CTAs (cta_group::2) 415, a buffer handed back by
-// halves 423 to 450, sixteen adding warps 497, three stages 432.
+// kept (400 to 415 us, for seconds 455): pairs of CTAs (cta_group::2) 415, for
+// seconds 437; a buffer handed back by halves 423 to 450; sixteen adding warps 497;
+// three stages 432; blocks issued by two warps in turn 403.
 constexpr int kFwThreads = 384;
 // 256 outputs: the adding warps hold 128 sums a thread and take registers of the
 // others: 256 x 208 + 128 x 88 = 384 x 168, which the launch has (checked there).
@@ -1046,7 +1048,7 @@ struct FmChoice {
 //     16 x 8192 x 8192      16x128/2 15.5  /1 17.2  64x128/2 15.2
 //    512 x 1408 x 2048      64x128 7.3  128x128 8.0  128x256 11.0
 //   2048 x 1408 x 2048      128x256 11.7  128x128 14.1  64x128 16.3
-//   8192 x 8192 x 8192      128x256 400 to 430 (the power limit's doing)  128x128 494  64x128 850
+//   8192 x 8192 x 8192      128x256 400 to 415  128x128 494  64x128 850
 //    4 rows of 4 experts    x 2816 x 2048: 16x128/1 7.1  /2 11.8
 //   8192 rows of 60 experts x 2816 x 2048: 128x256 80  128x128 88  64x128 113  32x128 179
 static cudaError_t fm_choose(const FmParams& p, FmChoice* choice) {
