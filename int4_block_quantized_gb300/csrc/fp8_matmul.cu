@@ -13,8 +13,8 @@
 //                few tokens cost a narrow MMA; K is split over the CTAs of a
 //                cluster where there are few tiles.  Bound by the weights' bytes:
 //                256 rows of 60 experts x 2816 x 2048 run at 6.8 TB/s; one token's
-//                four experts take 7.1 us for 3.4 us of bytes, the rest is a start
-//                of 3 us (launch, first copies, last block).
+//                four experts take 6.5 us for 3.4 us of bytes, the rest is launch,
+//                first copies and last block.
 //   many tokens  128 tokens by 128 or 256 weight rows.  A block of 128 x 256 takes
 //                860 cycles: a copy takes about 1700 to arrive and four stages of
 //                48 KB fit, so that one is there every 780; reading, scaling and
@@ -50,7 +50,7 @@ struct FmParams {
   int row_tiles;        // tiles of an expert's weight rows
   int wide_out;         // y: 16 bits, rows on 16-byte boundaries
   int wide_scales;      // four of a row's scales on 16 bytes
-  int split;            // CTAs of a cluster that share a tile's K
+  int split, lsplit;    // CTAs of a cluster that share a tile's K, and the logarithm of that
   uint32_t stall;       // QMOE_DIAG_STALL_FP8_*: this role waits for what cannot arrive
   long long wait_limit; // SM cycles
 };
@@ -69,7 +69,8 @@ struct FmPlan {
   // a split tile's partial sums [split][tokens of a CTA / 2][128][2]: a place of
   // their own where they are small, else the ring once the cluster is done with it
   static constexpr uint32_t kPart = BN <= 64 ? BN * 512 : 0;
-  static constexpr uint32_t kFixed = kFmBars + kFmTable + kOut + kScales + kPart;
+  static constexpr int kList = 64;                               // a CTA's first tiles, worked out at the start
+  static constexpr uint32_t kFixed = kFmBars + kFmTable + kList * 16 + kOut + kScales + kPart;
   static constexpr uint32_t kAt = (kFixed + 1023) & ~1023u;      // the ring's place
   static constexpr uint32_t kStage = (kA + kB + 1023) & ~1023u;
   static constexpr int kStages0 = (int)((kFmSmem - 1024 - kAt) / kStage);
@@ -187,7 +188,7 @@ __device__ __forceinline__ void fm_prefetch_map(const void* tmap) {
 }
 
 // A tile: the expert, which of its tiles of weight rows, tokens m0 .. m1 - 1.
-struct FmTile {
+struct alignas(16) FmTile {
   int e, rt, m0, m1;
 };
 struct FmTable {
@@ -245,10 +246,14 @@ __device__ __forceinline__ FmTile fm_tile(const FmParams& p, const FmTable& tab,
   }
   const int tok = tab.first[lo + 1] - tab.first[lo];
   t -= tab.first[lo] * p.row_tiles;
-  const int per = 8 * tok, g = t / per, r = t - g * per, rows = min(8, p.row_tiles - g * 8);
   f.e = lo;
-  f.rt = g * 8 + r % rows;
-  f.m0 = tab.start[lo] + r / rows * BN;
+  f.rt = t;
+  f.m0 = tab.start[lo];
+  if (tok > 1) {
+    const int per = 8 * tok, g = t / per, r = t - g * per, rows = min(8, p.row_tiles - g * 8);
+    f.rt = g * 8 + r % rows;
+    f.m0 += r / rows * BN;
+  }
   f.m1 = min(f.m0 + BN, tab.end[lo]);
   return f;
 }
@@ -273,29 +278,21 @@ __global__ void __launch_bounds__(kFmThreads, 1)
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   int* s_sum = reinterpret_cast<int*>(s_tmem + 2);  // [8]
   FmTable& tab = *reinterpret_cast<FmTable*>(smem + kFmBars);
-  uint8_t* outbuf = smem + kFmBars + kFmTable;
+  FmTile* list = reinterpret_cast<FmTile*>(smem + kFmBars + kFmTable);
+  uint8_t* outbuf = smem + kFmBars + kFmTable + P::kList * sizeof(FmTile);
   float* scales = reinterpret_cast<float*>(outbuf + P::kOut);
   float* part_own = scales + P::kScales / 4;
   uint8_t* ring = smem + P::kAt;
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be the same in all lanes
 
-  if (tid == 0) {
-    for (int s = 0; s < S; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+  // (by 32 threads: one takes 300 cycles for fifty barriers)
+  if (warp == 2) {
+    for (int i = lane; i < 2 * S + 2 * NB + 2 * SQ + 2; i += 32) {
+      const int a = i - 2 * S, q = a - 2 * NB;
+      mbar_init(&full[i], a >= NB && q < 0 ? 8 : q < 0 || q >= 2 * SQ ? 1 : q < SQ ? 2 : 8);
     }
-    for (int b = 0; b < NB; ++b) {
-      mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_free[b], 8);
-    }
-    for (int b = 0; b < SQ; ++b) {
-      mbar_init(&sc_full[b], 2);
-      mbar_init(&sc_free[b], 8);
-    }
-    mbar_init(fin, 1);
-    mbar_init(never, 1);
-    *s_abort = 0;
+    if (lane == 0) *s_abort = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -317,10 +314,18 @@ __global__ void __launch_bounds__(kFmThreads, 1)
   // this CTA's tiles and its share [c0, c1) of their blocks along K
   const int rank = p.split > 1 ? (int)cluster_ctarank() : 0;
   const int tiles = tab.first[p.E] * p.row_tiles;
-  const int first = blockIdx.x / p.split, step = p.split > 1 ? max(tiles, (int)gridDim.x) : gridDim.x;
+  const int first = blockIdx.x >> p.lsplit, step = p.split > 1 ? max(tiles, (int)gridDim.x) : gridDim.x;
   const int nb = (p.K + 127) / 128;
   auto stalled = [&](uint32_t role) { return (p.stall & role) && !fm_wait(never, 0, p, s_abort); };
-  const int c0 = (int)((long long)nb * rank / p.split), c1 = (int)((long long)nb * (rank + 1) / p.split);
+  const int c0 = nb * rank >> p.lsplit, c1 = nb * (rank + 1) >> p.lsplit;  // (nb is at most 2^24)
+  // (a search and divisions of some 400 cycles, which every role would wait for
+  // at each tile: 60 experts' 8192 rows 81 -> 77.5 us in the wide form, one token's
+  // four experts 7.1 -> 6.5 with the barriers' setup by 32 threads)
+  static_assert(sizeof(FmTile) == 16, "list");
+  for (int i = tid; i < P::kList && first + (long long)i * step < tiles; i += kFmThreads)
+    list[i] = fm_tile<BN>(p, tab, first + i * step);
+  __syncthreads();
+  auto nth = [&](int i, int t) { return i < P::kList ? list[i] : fm_tile<BN>(p, tab, t); };
   f2 acc[P::kQ][P::kG][4];
 
   if (warp == 0) {
@@ -329,8 +334,8 @@ __global__ void __launch_bounds__(kFmThreads, 1)
     uint32_t ph = 0;
     bool ok = !stalled(QMOE_DIAG_STALL_FP8_CODES);
     const uint32_t el = elect_lane();
-    for (int t = first; t < tiles && ok; t += step) {
-      const FmTile f = fm_tile<BN>(p, tab, t);
+    for (int t = first, i = 0; t < tiles && ok; t += step, ++i) {
+      const FmTile f = nth(i, t);
       const int row = f.e * p.N + f.rt * 128;
       const int boxes = (f.m1 - f.m0 + P::kBox - 1) / P::kBox;  // copies, as many as the tile has tokens
       for (int c = c0; c < c1; ++c, ++it) {
@@ -357,8 +362,8 @@ __global__ void __launch_bounds__(kFmThreads, 1)
     uint32_t ph = 0;
     bool ok = !stalled(QMOE_DIAG_STALL_FP8_MMA), issued = false;
     const uint32_t el = elect_lane();
-    for (int t = first; t < tiles && ok; t += step) {
-      const FmTile f = fm_tile<BN>(p, tab, t);
+    for (int t = first, i = 0; t < tiles && ok; t += step, ++i) {
+      const FmTile f = nth(i, t);
       const int cols = (f.m1 - f.m0 + 15) & ~15;
       // D fp32, A and B e4m3, both K-major
       const uint32_t idesc = 1u << 4 | (uint32_t)(cols >> 3) << 17 | (uint32_t)(128 >> 4) << 24;
@@ -394,8 +399,8 @@ __global__ void __launch_bounds__(kFmThreads, 1)
     int it = 0;
     const int rb = (p.N + 127) / 128;
     bool ok = !stalled(QMOE_DIAG_STALL_FP8_SCALES);
-    for (int t = first; t < tiles && ok; t += step) {
-      const FmTile f = fm_tile<BN>(p, tab, t);
+    for (int t = first, i = 0; t < tiles && ok; t += step, ++i) {
+      const FmTile f = nth(i, t);
       const int rt = f.rt;
       const float* ws = p.ws + ((size_t)f.e * rb + rt) * nb;
       for (int c = c0; c < c1; c += 4, ++it) {
@@ -432,8 +437,8 @@ __global__ void __launch_bounds__(kFmThreads, 1)
     uint8_t* buf = outbuf + (warp - 4) * (P::kW * 64);
     int n = 0, it = 0;
     bool ok = !stalled(QMOE_DIAG_STALL_FP8_OUTPUT);
-    for (int t = first; t < tiles && ok; t += step) {
-      const FmTile f = fm_tile<BN>(p, tab, t);
+    for (int t = first, i = 0; t < tiles && ok; t += step, ++i) {
+      const FmTile f = nth(i, t);
       const int cols = f.m1 - f.m0;
 #pragma unroll
       for (int q = 0; q < P::kQ; ++q)
@@ -517,7 +522,7 @@ __global__ void __launch_bounds__(kFmThreads, 1)
     float* part = P::kPart ? part_own : reinterpret_cast<float*>(ring);
     const bool some = first < tiles;
     FmTile f = {0, 0, 0, 0};
-    if (some) f = fm_tile<BN>(p, tab, first);
+    if (some) f = list[0];
     const int rows = f.m1 - f.m0, per = max(2, BN / p.split), lper = 31 - __clz(per);
     if (!P::kPart) cluster_arrive();
     cluster_wait();
@@ -585,7 +590,8 @@ struct FwPlan {
   static constexpr int kQuads = 2;                                // scales: slots of four blocks
   static constexpr uint32_t kScales = kQuads * 4 * kHalves * 512;
   static constexpr uint32_t kOut = 8 * 32 * 17 * 4;               // rows of y that are not written in wide words
-  static constexpr uint32_t kAt = (kFmBars + kFmTable + kScales + kOut + 1023) & ~1023u;
+  static constexpr int kList = 64;                                // a CTA's first tiles, worked out at the start
+  static constexpr uint32_t kAt = (kFmBars + kFmTable + kList * 32 + kScales + kOut + 1023) & ~1023u;
   static constexpr int kStages = (int)((kFmSmem - 1024 - kAt) / kStage);
 };
 
@@ -607,7 +613,7 @@ __device__ __forceinline__ void fw_wait(uint32_t (&r)[16]) {
                : "memory");
 }
 
-struct FwTile : FmTile {
+struct alignas(16) FwTile : FmTile {
   int n0, n1;  // outputs
 };
 
@@ -631,28 +637,19 @@ __global__ void __launch_bounds__(kFwThreads, 1)
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   int* s_sum = reinterpret_cast<int*>(s_tmem + 2);  // [8]
   FmTable& tab = *reinterpret_cast<FmTable*>(smem + kFmBars);
-  float* scales = reinterpret_cast<float*>(smem + kFmBars + kFmTable);
-  uint8_t* outbuf = smem + kFmBars + kFmTable + P::kScales;
+  FwTile* list = reinterpret_cast<FwTile*>(smem + kFmBars + kFmTable);
+  float* scales = reinterpret_cast<float*>(smem + kFmBars + kFmTable + P::kList * sizeof(FwTile));
+  uint8_t* outbuf = reinterpret_cast<uint8_t*>(scales) + P::kScales;
   uint8_t* ring = smem + P::kAt;
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be the same in all lanes
 
-  if (tid == 0) {
-    for (int s = 0; s < S; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+  if (warp == 2) {
+    for (int i = lane; i < 2 * S + 2 * NB + 2 * SQ + 2; i += 32) {
+      const int a = i - 2 * S, q = a - 2 * NB;
+      mbar_init(&full[i], (a >= NB && q < 0) || (q >= SQ && q < 2 * SQ) ? 8 : 1);
     }
-    for (int b = 0; b < NB; ++b) {
-      mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_free[b], 8);
-    }
-    for (int b = 0; b < SQ; ++b) {
-      mbar_init(&sc_full[b], 1);
-      mbar_init(&sc_free[b], 8);
-    }
-    mbar_init(fin, 1);
-    mbar_init(never, 1);
-    *s_abort = 0;
+    if (lane == 0) *s_abort = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -679,6 +676,12 @@ __global__ void __launch_bounds__(kFwThreads, 1)
     f.n1 = min(p.N, f.n0 + (h < 0 ? BN : BN / 2));
     return f;  // (an empty half where the outputs end before it)
   };
+  // (as in the form for few tokens)
+  static_assert(sizeof(FwTile) == 32, "list");
+  for (int i = tid; i < P::kList && blockIdx.x + (long long)i * gridDim.x < parts; i += kFwThreads)
+    list[i] = part(blockIdx.x + i * gridDim.x);
+  __syncthreads();
+  auto nth = [&](int i, int t) { return i < P::kList ? list[i] : part(t); };
   auto stalled = [&](uint32_t role) { return (p.stall & role) && !fm_wait(never, 0, p, s_abort); };
   if (warp >= 4) {
     if (BN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFwManyRegs));
@@ -687,8 +690,8 @@ __global__ void __launch_bounds__(kFwThreads, 1)
     float* buf = reinterpret_cast<float*>(outbuf) + (warp - 4) * 32 * 17;
     int n = 0, it = 0;
     bool ok = !stalled(QMOE_DIAG_STALL_FP8_OUTPUT);
-    for (int t = blockIdx.x; t < parts && ok; t += gridDim.x) {
-      const FwTile f = part(t);
+    for (int t = blockIdx.x, i = 0; t < parts && ok; t += gridDim.x, ++i) {
+      const FwTile f = nth(i, t);
       if (f.n1 <= f.n0) continue;
       const int n0 = f.n0 + set * (BN / 2), cols = f.n1 - n0;      // this warp's columns
       const int m0 = f.m0 + qd * 32;                               // and tokens
@@ -806,8 +809,8 @@ __global__ void __launch_bounds__(kFwThreads, 1)
       uint32_t ph = 0;
       bool ok = !stalled(QMOE_DIAG_STALL_FP8_CODES);
       const uint32_t el = elect_lane();
-      for (int t = blockIdx.x; t < parts && ok; t += gridDim.x) {
-        const FwTile f = part(t);
+      for (int t = blockIdx.x, i = 0; t < parts && ok; t += gridDim.x, ++i) {
+        const FwTile f = nth(i, t);
         if (f.n1 <= f.n0) continue;
         const int xb = (f.m1 - f.m0 + 63) / 64, wb = (f.n1 - f.n0 + 63) / 64;  // copies of 64 rows
         for (int c = 0; c < nb; ++c, ++it) {
@@ -834,8 +837,8 @@ __global__ void __launch_bounds__(kFwThreads, 1)
       uint32_t ph = 0;
       bool ok = !stalled(QMOE_DIAG_STALL_FP8_MMA), issued = false;
       const uint32_t el = elect_lane();
-      for (int t = blockIdx.x; t < parts && ok; t += gridDim.x) {
-        const FwTile f = part(t);
+      for (int t = blockIdx.x, i = 0; t < parts && ok; t += gridDim.x, ++i) {
+        const FwTile f = nth(i, t);
         if (f.n1 <= f.n0) continue;
         const int cols = (f.n1 - f.n0 + 15) & ~15;
         const uint32_t idesc = 1u << 4 | (uint32_t)(cols >> 3) << 17 | (uint32_t)(BT >> 4) << 24;
@@ -871,8 +874,8 @@ __global__ void __launch_bounds__(kFwThreads, 1)
       int it = 0;
       const int rb = (p.N + 127) / 128;
       bool ok = !stalled(QMOE_DIAG_STALL_FP8_SCALES);
-      for (int t = blockIdx.x; t < parts && ok; t += gridDim.x) {
-        const FwTile f = part(t);
+      for (int t = blockIdx.x, i = 0; t < parts && ok; t += gridDim.x, ++i) {
+        const FwTile f = nth(i, t);
         if (f.n1 <= f.n0) continue;
         const float* ws = p.ws + ((size_t)f.e * rb + f.n0 / 128) * nb;
         for (int c = 0; c < nb; c += 4, ++it) {
@@ -931,6 +934,7 @@ static cudaError_t launch_fm(FmParams p, int split, const uint8_t* xc, const uin
   static_assert(P::kStages >= 3 && P::kBufs * BN <= 512, "plan");
   static_assert((2 * P::kStages + 2 * P::kBufs + 2 * P::kQuads + 2) * 8 + 40 <= kFmBars, "barriers");
   p.split = split;
+  p.lsplit = split == 8 ? 3 : split / 2;
   p.row_tiles = (p.N + 127) / 128;
   const long long tiles = fm_token_tiles(p, BN) * p.row_tiles;
   if (tiles > (1LL << 27)) return cudaErrorInvalidValue;
@@ -1042,27 +1046,27 @@ struct FmChoice {
 // split tile's sums; at least what the operands' bytes take.  Where experts share
 // the rows, each is taken to have as many, and a last tile half full.
 // The constants are fits to 410 measured sizes, dense and grouped, of which 15 are
-// then more than 5 % off the best form, the worst 32 % (71 tokens x 8, 8 experts).
+// then more than 5 % off the best form, the worst 27 % (71 tokens x 8, 8 experts).
 // Some of them on GB300 (us; tokens x outputs a tile / CTAs along K):
-//      1 x 1408 x 2048      16x128/8 4.1  /4 4.2  /2 4.8  /1 5.7
-//     16 x 8192 x 8192      16x128/2 15.5  /1 17.2  64x128/2 15.2
-//    512 x 1408 x 2048      64x128 7.3  128x128 8.0  128x256 11.0
-//   2048 x 1408 x 2048      128x256 11.7  128x128 14.1  64x128 16.3
-//   8192 x 8192 x 8192      128x256 400 to 415  128x128 494  64x128 850
-//    4 rows of 4 experts    x 2816 x 2048: 16x128/1 7.1  /2 11.8
-//   8192 rows of 60 experts x 2816 x 2048: 128x256 80  128x128 88  64x128 113  32x128 179
+//      1 x 1408 x 2048      16x128/8 3.4  /4 3.6  /2 4.2  /1 5.2
+//     16 x 8192 x 8192      64x128/2 14.2  16x128/2 14.6  /1 16.6
+//    512 x 1408 x 2048      64x128 7.0  128x128 7.6  128x256 10.7
+//   2048 x 1408 x 2048      128x256 11.2  128x128 13.4  64x128 15.3
+//   8192 x 8192 x 8192      128x256 400 to 415  128x128 490  64x128 810
+//    4 rows of 4 experts    x 2816 x 2048: 16x128/1 6.5  /2 11
+//   8192 rows of 60 experts x 2816 x 2048: 128x256 77  128x128 82  64x128 106
 static cudaError_t fm_choose(const FmParams& p, FmChoice* choice) {
   static const struct {
     int bn, wide, start, block, tile, exchange;
-  } kinds[] = {{16, 0, 2570, 236, 905, 867},   {32, 0, 3520, 225, 981, 682},  {64, 0, 3740, 233, 1113, 1057},
-               {128, 0, 4090, 441, 1519, 963}, {128, 1, 3990, 276, 1569, 0}, {256, 1, 8250, 299, 4821, 0}};
+  } kinds[] = {{16, 0, 2400, 247, 796, 411},   {32, 0, 3486, 223, 979, 227},  {64, 0, 3725, 233, 1113, 1027},
+               {128, 0, 4090, 511, 1827, 813}, {128, 1, 3990, 301, 2290, 0}, {256, 1, 8320, 367, 5385, 0}};
   int capacity[9] = {};
   for (int split = 2; split <= 8; split *= 2) {
     const cudaError_t err = fm_capacity(split, &capacity[split]);
     if (err != cudaSuccess) return err;
   }
   const long long nb = (p.K + 127) / 128, active = p.offsets ? (p.E < p.M ? p.E : p.M) : 1, each = (p.M + active - 1) / active;
-  const double bytes = (double)active * p.N * p.K + (double)p.M * p.K + 2.0 * p.M * p.N, least_time = 4180 + bytes / 6874;
+  const double bytes = (double)active * p.N * p.K + (double)p.M * p.K + 2.0 * p.M * p.N, least_time = 3610 + bytes / 7171;
   double least = -1;
   for (const auto& k : kinds) {
     if (!k.wide && k.bn < 64 && each > k.bn) continue;
@@ -1070,7 +1074,7 @@ static cudaError_t fm_choose(const FmParams& p, FmChoice* choice) {
     const long long rows = (p.N + br - 1) / br, some = p.offsets ? p.M / bt + active / 2 : (p.M + bt - 1) / bt;
     const long long tiles = rows * (some > active ? some : active), of = k.wide ? p.N : each;
     const double block = k.block * (0.53 + 0.47 * (of < k.bn ? (int)of : k.bn) / k.bn);
-    const int tile = k.tile + (k.wide && p.N % 8 ? 2222 : 0);
+    const int tile = k.tile + (k.wide && p.N % 8 ? 1486 : 0);
     for (int split = 1; split <= 8; split *= 2) {
       if (split > 1 && (!k.exchange || split > nb || rows * fm_token_tiles(p, k.bn) * split > capacity[split])) break;
       const long long slots = split > 1 ? tiles : device_sm_count(), rounds = (tiles + slots - 1) / slots;

@@ -25,11 +25,11 @@ FORMS = [
     (35, 5, 784, 2, (32, 0, 4)), (18, 1, 1104, None, (32, 0, 8)), (37, 8, 976, 2, (32, 0, 8)),
     (37, 1, 16, None, (64, 0, 1)), (69, 8, 16, 2, (64, 0, 1)), (588, 397, 1424, None, (64, 0, 2)), (719, 8, 2064, 60, (64, 0, 2)),
     (76, 40, 816, None, (64, 0, 4)), (109, 62, 832, 2, (64, 0, 4)), (33, 8, 960, None, (64, 0, 8)), (85, 1, 928, 2, (64, 0, 8)),
-    (4221, 518, 16, None, (128, 0, 1)), (4933, 261, 32, 60, (128, 0, 1)), (197, 2057, 2992, 3, (128, 0, 2)),
-    (75, 2992, 1376, None, (128, 0, 4)), (485, 273, 1664, 8, (128, 0, 4)), (67, 1425, 2816, None, (128, 0, 8)),
+    (3623, 1320, 32, None, (128, 0, 1)), (5578, 463, 48, 60, (128, 0, 1)), (93, 2854, 4016, None, (128, 0, 4)),
+    (75, 2992, 1376, None, (128, 0, 4)), (490, 353, 1392, 8, (128, 0, 4)), (67, 1425, 2816, None, (128, 0, 8)),
     (519, 8, 3024, 8, (128, 0, 8)),
-    (48, 8, 544, None, (128, 1, 1)), (141, 1, 336, 2, (128, 1, 1)), (3604, 400, 384, 60, (128, 1, 1)),
-    (1601, 1415, 672, None, (256, 1, 1)), (1854, 1368, 1392, None, (256, 1, 1)), (1955, 1351, 656, 2, (256, 1, 1)),
+    (57, 3, 528, None, (128, 1, 1)), (106, 8, 672, 2, (128, 1, 1)), (3604, 400, 384, 60, (64, 0, 1)),
+    (1854, 1303, 976, None, (256, 1, 1)), (1854, 1368, 1392, None, (256, 1, 1)), (3656, 994, 432, 2, (256, 1, 1)),
     (4303, 528, 1456, 3, (256, 1, 1))]
 
 
