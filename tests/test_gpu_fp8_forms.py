@@ -92,6 +92,31 @@ def test_each_form(M, N, K, E, form, dtype):
         assert (outs[0][int(off[-1]):] == 7).all()
 
 
+@pytest.mark.parametrize("M,N,K,E,form", [(8192, 4900, 16, 256, (64, 0, 1)), (20000, 8199, 144, None, (128, 0, 1)),
+                                          (20000, 8200, 272, None, (128, 1, 1)), (20000, 16000, 400, None, (256, 1, 1))])
+def test_more_tiles_than_a_cta_lists(M, N, K, E, form):
+    """Above 64 tiles to each of 152 CTAs: the first ones come from the list, the
+    others are worked out by each role."""
+    assert B.qmoe_fp8_matmul_variant(M, N, K, E) == form
+    tiles = (E if E else -(-M // (128 if form[1] else form[0]))) * -(-N // (form[0] if form[1] else 128))
+    assert tiles > 64 * 152
+    ops, off, X, W = make(M, N, K, E)
+    y = torch.full((M, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    B.qmoe_fp8_matmul(*ops, offsets=off, out=y)
+    check(y, off, X, W)
+    if off is not None:
+        assert (y[int(off[-1]):] == 7).all()
+
+
+@pytest.mark.parametrize("K", [16, 400])
+def test_more_than_2_to_the_32_outputs(K):
+    M, N = 70000, 62000
+    ops, _, X, W = make(M, N, K, None)
+    y = B.qmoe_fp8_matmul(*ops)
+    for m in (0, M // 2, M - 200):
+        check(y[m:m + 200], None, X[m:m + 200], W)
+
+
 def run_out(ops, off, flags):
     """(status bits, seconds on the device) of a call that stalls."""
     status = torch.zeros(1, dtype=torch.int32, device=DEV)
