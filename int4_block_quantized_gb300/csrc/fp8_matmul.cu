@@ -785,17 +785,29 @@ __global__ void __launch_bounds__(kFwThreads, 1)
         }
       } else {
         // 32 tokens x 16 columns at a time through shared memory, so that
-        // neighbouring lanes write neighbouring columns
+        // neighbouring lanes write neighbouring columns; the type and the address are
+        // settled outside the loop (4096 x 8195 x 2048 bf16: 96 -> 80 us; a loop
+        // unrolled in full, 81, takes registers that rows on 16 bytes miss: 6 %)
 #pragma unroll
         for (int q = 0; q < P::kC; ++q) {
           if (16 * q < cols) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) buf[lane * 17 + j] = acc[q][j];
             __syncwarp();
-            const int col = lane & 15;
-            for (int r = lane >> 4; r < 32; r += 2)
-              if (m0 + r < f.m1 && 16 * q + col < cols)
-                fm_store(p, (size_t)(m0 + r) * p.N + n0 + 16 * q + col, buf[r * 17 + col]);
+            const int col = lane & 15, rows = 16 * q + col < cols ? f.m1 - m0 : 0;
+            const float* from = buf + (lane >> 4) * 17 + col;
+            const size_t to = (size_t)(m0 + (lane >> 4)) * p.N + n0 + 16 * q + col, step = 2 * (size_t)p.N;
+            if (p.y_dtype == QMOE_F32) {
+              float* y = static_cast<float*>(p.y) + to;
+#pragma unroll 4
+              for (int r = 0; r < 32; r += 2, y += step)
+                if (r + (lane >> 4) < rows) *y = from[r * 17];
+            } else {
+              uint16_t* y = static_cast<uint16_t*>(p.y) + to;
+#pragma unroll 4
+              for (int r = 0; r < 32; r += 2, y += step)
+                if (r + (lane >> 4) < rows) *y = (uint16_t)fm_pack(p, make_float2(from[r * 17], 0.f));
+            }
             __syncwarp();
           }
         }
