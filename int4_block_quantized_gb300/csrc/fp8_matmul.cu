@@ -1058,35 +1058,36 @@ struct FmChoice {
 // split tile's sums; at least what the operands' bytes take.  Where experts share
 // the rows, each is taken to have as many, and a last tile half full.
 // The constants are fits to 410 measured sizes, dense and grouped, of which 15 are
-// then more than 5 % off the best form, the worst 27 % (71 tokens x 8, 8 experts).
+// then more than 5 % off the best form, the worst 29 % (71 tokens x 8, 8 experts).
 // Some of them on GB300 (us; tokens x outputs a tile / CTAs along K):
 //      1 x 1408 x 2048      16x128/8 3.4  /4 3.6  /2 4.2  /1 5.2
 //     16 x 8192 x 8192      64x128/2 14.2  16x128/2 14.6  /1 16.6
-//    512 x 1408 x 2048      64x128 7.0  128x128 7.6  128x256 10.7
-//   2048 x 1408 x 2048      128x256 11.2  128x128 13.4  64x128 15.3
+//     64 x 2048 x 5632      32x128/4 6.9  64x128/4 7.5  /1 12.7
+//    512 x 1408 x 2048      64x128 7.0  128x128 8.1  128x256 11.2
+//   2048 x 1408 x 2048      128x256 11.6  128x128 13.9  64x128 15.5
 //   8192 x 8192 x 8192      128x256 400 to 415  128x128 490  64x128 810
 //    4 rows of 4 experts    x 2816 x 2048: 16x128/1 6.5  /2 11
-//   8192 rows of 60 experts x 2816 x 2048: 128x256 77  128x128 82  64x128 106
+//   8192 rows of 60 experts x 2816 x 2048: 128x256 77  128x128 83  64x128 100
 static cudaError_t fm_choose(const FmParams& p, FmChoice* choice) {
   static const struct {
-    int bn, wide, start, block, tile, exchange;
-  } kinds[] = {{16, 0, 2400, 247, 796, 411},   {32, 0, 3486, 223, 979, 227},  {64, 0, 3725, 233, 1113, 1027},
-               {128, 0, 4090, 511, 1827, 813}, {128, 1, 3990, 301, 2290, 0}, {256, 1, 8320, 367, 5385, 0}};
+    int bn, wide, start, block, tile, exchange, odd;  // odd: a tile more where rows of y are off 16 bytes
+  } kinds[] = {{16, 0, 2422, 246, 709, 361, 0},   {32, 0, 3172, 223, 977, 223, 0}, {64, 0, 3725, 230, 1097, 1045, 0},
+               {128, 0, 4089, 462, 1631, 679, 0}, {128, 1, 3990, 269, 1413, 0, 664}, {256, 1, 6800, 348, 3068, 0, 1940}};
   int capacity[9] = {};
   for (int split = 2; split <= 8; split *= 2) {
     const cudaError_t err = fm_capacity(split, &capacity[split]);
     if (err != cudaSuccess) return err;
   }
   const long long nb = (p.K + 127) / 128, active = p.offsets ? (p.E < p.M ? p.E : p.M) : 1, each = (p.M + active - 1) / active;
-  const double bytes = (double)active * p.N * p.K + (double)p.M * p.K + 2.0 * p.M * p.N, least_time = 3610 + bytes / 7171;
+  const double bytes = (double)active * p.N * p.K + (double)p.M * p.K + 2.0 * p.M * p.N, least_time = 3523 + bytes / 7000;
   double least = -1;
   for (const auto& k : kinds) {
-    if (!k.wide && k.bn < 64 && each > k.bn) continue;
+    if (!k.wide && k.bn < 64 && each > 4 * k.bn) continue;
     const int bt = k.wide ? 128 : k.bn, br = k.wide ? k.bn : 128;
     const long long rows = (p.N + br - 1) / br, some = p.offsets ? p.M / bt + active / 2 : (p.M + bt - 1) / bt;
     const long long tiles = rows * (some > active ? some : active), of = k.wide ? p.N : each;
-    const double block = k.block * (0.53 + 0.47 * (of < k.bn ? (int)of : k.bn) / k.bn);
-    const int tile = k.tile + (k.wide && p.N % 8 ? 1486 : 0);
+    const double block = k.block * (0.52 + 0.48 * (of < k.bn ? (int)of : k.bn) / k.bn);
+    const int tile = k.tile + (p.N % 8 ? k.odd : 0);
     for (int split = 1; split <= 8; split *= 2) {
       if (split > 1 && (!k.exchange || split > nb || rows * fm_token_tiles(p, k.bn) * split > capacity[split])) break;
       const long long slots = split > 1 ? tiles : device_sm_count(), rounds = (tiles + slots - 1) / slots;

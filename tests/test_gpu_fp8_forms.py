@@ -19,18 +19,19 @@ LIMIT = 1024  # x 1024 SM cycles
 # (M, N, K, experts or None, (tile, form, CTAs along K)): odd numbers of tokens,
 # outputs and blocks, several tiles to a CTA where K is not shared
 FORMS = [
-    (3, 8, 16, 2, (16, 0, 1)), (40, 8, 1696, 60, (16, 0, 2)), (8, 2, 800, None, (16, 0, 4)), (14, 8, 832, 2, (16, 0, 4)),
-    (3, 8, 912, None, (16, 0, 8)), (3, 1, 1056, 3, (16, 0, 8)),
-    (18, 1, 16, None, (32, 0, 1)), (34, 8, 16, 2, (32, 0, 1)), (368, 8, 1984, 60, (32, 0, 2)), (17, 8, 768, None, (32, 0, 4)),
-    (35, 5, 784, 2, (32, 0, 4)), (18, 1, 1104, None, (32, 0, 8)), (37, 8, 976, 2, (32, 0, 8)),
-    (37, 1, 16, None, (64, 0, 1)), (69, 8, 16, 2, (64, 0, 1)), (588, 397, 1424, None, (64, 0, 2)), (719, 8, 2064, 60, (64, 0, 2)),
-    (76, 40, 816, None, (64, 0, 4)), (109, 62, 832, 2, (64, 0, 4)), (33, 8, 960, None, (64, 0, 8)), (85, 1, 928, 2, (64, 0, 8)),
-    (3623, 1320, 32, None, (128, 0, 1)), (5578, 463, 48, 60, (128, 0, 1)), (93, 2854, 4016, None, (128, 0, 4)),
-    (75, 2992, 1376, None, (128, 0, 4)), (490, 353, 1392, 8, (128, 0, 4)), (67, 1425, 2816, None, (128, 0, 8)),
-    (519, 8, 3024, 8, (128, 0, 8)),
-    (57, 3, 528, None, (128, 1, 1)), (106, 8, 672, 2, (128, 1, 1)), (3604, 400, 384, 60, (64, 0, 1)),
-    (1854, 1303, 976, None, (256, 1, 1)), (1854, 1368, 1392, None, (256, 1, 1)), (3656, 994, 432, 2, (256, 1, 1)),
-    (4303, 528, 1456, 3, (256, 1, 1))]
+    (3, 8, 16, 2, (16, 0, 1)), (50, 1562, 448, None, (16, 0, 2)), (42, 2, 720, 60, (16, 0, 2)), (3, 1, 528, None, (16, 0, 4)),
+    (106, 8, 672, 2, (16, 0, 4)), (3, 8, 912, None, (16, 0, 8)), (3, 1, 1056, 3, (16, 0, 8)), (67, 1, 16, None, (32, 0, 1)),
+    (143, 1, 16, 2, (32, 0, 1)), (99, 1491, 512, None, (32, 0, 2)), (490, 353, 1392, 8, (32, 0, 2)),
+    (76, 2, 416, None, (32, 0, 4)), (67, 1425, 2816, None, (32, 0, 4)), (136, 1, 432, 2, (32, 0, 4)),
+    (69, 1, 1120, None, (32, 0, 8)), (150, 4, 976, 2, (32, 0, 8)), (132, 2, 16, None, (64, 0, 1)), (288, 8, 16, 2, (64, 0, 1)),
+    (588, 397, 1424, None, (64, 0, 2)), (555, 2, 3152, 60, (64, 0, 2)), (188, 46, 832, None, (64, 0, 4)),
+    (428, 70, 816, 3, (64, 0, 4)), (143, 1, 976, None, (64, 0, 8)), (268, 28, 960, 2, (64, 0, 8)),
+    (5714, 797, 80, None, (128, 0, 1)), (4933, 261, 32, 60, (128, 0, 1)), (2165, 64, 4544, 60, (128, 0, 2)),
+    (108, 2482, 3344, None, (128, 0, 4)), (160, 1328, 1696, 2, (128, 0, 4)), (88, 1848, 2928, None, (128, 0, 8)),
+    (963, 3, 3856, 8, (128, 0, 8)), (137, 2, 416, None, (128, 1, 1)), (290, 8, 400, 2, (128, 1, 1)),
+    (3604, 400, 384, 60, (128, 1, 1)), (900, 2561, 512, None, (256, 1, 1)), (1385, 1896, 1024, None, (256, 1, 1)),
+    (4086, 607, 416, 2, (256, 1, 1)), (3262, 776, 992, 3, (256, 1, 1)), (3, 8, 400, 2, (16, 0, 4)), (65, 8, 960, None, (32, 0, 8)),
+    (132, 8, 992, None, (64, 0, 8))]
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -93,7 +94,7 @@ def test_each_form(M, N, K, E, form, dtype):
 
 
 @pytest.mark.parametrize("M,N,K,E,form", [(8192, 4900, 16, 256, (64, 0, 1)), (20000, 8199, 144, None, (128, 0, 1)),
-                                          (20000, 8200, 272, None, (128, 1, 1)), (20000, 16000, 400, None, (256, 1, 1))])
+                                          (20000, 8199, 272, None, (128, 1, 1)), (20000, 16000, 400, None, (256, 1, 1))])
 def test_more_tiles_than_a_cta_lists(M, N, K, E, form):
     """Above 64 tiles to each of 152 CTAs: the first ones come from the list, the
     others are worked out by each role."""
