@@ -62,8 +62,36 @@ __global__ void __launch_bounds__(256) fp8_rows_kernel(const void* __restrict__ 
 }
 
 // silu(g) * u of h [M, 2 I] (gate, then up), in fp32, quantised as above.  Bound by
-// instructions, the exponential's and the quantiser's: 8192 x 1408 bf16 in 13.0 us,
-// 4.5 TB/s (12.0 with an exponential that loses accuracy far from 0).
+// instructions, the exponential's and the quantiser's: 8192 x 1408 bf16 in 13.9 us,
+// 4.2 TB/s (a tenth less with an exponential that loses accuracy far from 0).
+//
+// Below kDeepGate exp(-g) comes near the end of fp32, and its reciprocal is no
+// normal number any more.  1 + exp(g) is 1 there, and g exp(g) u is computed as
+// g exp(g + 96) (u 2^-64) (2^64 exp(-96)), whose factors and products are normal
+// numbers for every u that leaves a code (g + 96 is exact down to -192; what is
+// further below is no code for any u).  Such gates are rare, and a thread asks once
+// whether it has one among its 16.  What it does then is a function of its own:
+// unrolled in place it takes registers of everybody (bf16 7 to 16 % slower than without
+// it; so, 3, and fp16 8).
+constexpr float kDeepGate = -87.f;
+__device__ __forceinline__ float fp8_swiglu(float g, float u) {
+  float r;  // (a rounded quotient takes eight instructions more)
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + expf(-g)));
+  return u * (g * r);
+}
+__device__ __forceinline__ float fp8_swiglu_deep(float g, float u) {
+  return g * expf(g + 96.f) * (u * 0x1p-64f) * 3.7467047e-23f;
+}
+// v's elements with such gates; h from the first of the 16 gates on
+template <typename T>
+__device__ __noinline__ void fp8_swiglu_deep16(const void* h, size_t at, int I, float* v) {
+  float g[16], u[16];
+  load16<T>(h, at, g);
+  load16<T>(h, at + I, u);
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    if (g[j] < kDeepGate) v[j] = fp8_swiglu_deep(g[j], u[j]);
+}
 template <typename T>
 __global__ void __launch_bounds__(256) fp8_swiglu_kernel(const void* __restrict__ h, int M, int I,
                                                          uint8_t* __restrict__ codes, float* __restrict__ scales) {
@@ -73,14 +101,22 @@ __global__ void __launch_bounds__(256) fp8_swiglu_kernel(const void* __restrict_
     const bool in = 16 * w.u < (uint32_t)I;
     float v[16] = {};
     if (in) {
+      const size_t at = (size_t)w.r * 2 * I + 16 * w.u;
       float g[16];
-      load16<T>(h, (size_t)w.r * 2 * I + 16 * w.u, g);
-      load16<T>(h, (size_t)w.r * 2 * I + I + 16 * w.u, v);
+      Sixteen<T> gate;
+      gate.load(h, at);
+      load16<T>(h, at + I, v);
+      gate.values(g);
+      const bool deep = !(gate.lowest() >= kDeepGate);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        float r;  // (a rounded quotient takes eight instructions more)
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + expf(-g[j])));
-        v[j] *= g[j] * r;
+      for (int j = 0; j < 16; ++j) v[j] = fp8_swiglu(g[j], v[j]);
+      if (deep) {
+        float t[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) t[j] = v[j];
+        fp8_swiglu_deep16<T>(h, at, I, t);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = t[j];
       }
     }
     const Fp8Block b(fp8_group_max(fp8_max16(v)));

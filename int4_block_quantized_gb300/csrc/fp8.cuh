@@ -38,6 +38,20 @@ struct Sixteen {
     if constexpr (sizeof(T) == 4) return raw;
     else return __float_as_uint(Half<T>::to_float((uint16_t)max(raw & 0xffffu, raw >> 16)));
   }
+  // the lowest of them where one is below zero (its bits are then the largest, but
+  // for a NaN's), else some other, as fp32
+  __device__ __forceinline__ float lowest() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (uint32_t q = 0; q < sizeof(T) / 2; ++q)
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) {
+        if constexpr (sizeof(T) == 4) m = __vimax3_u32(m, w[q][j], w[q][j + 1]);
+        else m = __vimax3_u16x2(m, w[q][j], w[q][j + 1]);
+      }
+    if constexpr (sizeof(T) == 4) return __uint_as_float(m);
+    else return Half<T>::to_float((uint16_t)max(m & 0xffffu, m >> 16));
+  }
   __device__ __forceinline__ void values(float (&v)[16]) const {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
