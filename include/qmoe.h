@@ -569,7 +569,9 @@ int qmoe_fp8_dequant(const uint8_t* codes, const float* scales, int E, int N, in
  *                 were.  Offsets that decrease or leave 0 .. M set QMOE_ST_INDEX,
  *                 and all of y is left as it was.  At most QMOE_MAX_EXPERTS
  *                 experts.
- * A NaN scale or code makes the outputs that it enters NaN, and no others.
+ * A NaN scale or code makes the outputs that it enters NaN, and no others.  Scales
+ * may be any fp32 numbers: a token with a pair of scales whose product fp32 does not
+ * hold as a normal number is computed by a slow path (some 300 times the time).
  * One kernel.  Its tile and the split of K are chosen by E, M, N, K, whether
  * there are offsets, and the device: calls that agree in these give the same
  * bits, others sum in another order.

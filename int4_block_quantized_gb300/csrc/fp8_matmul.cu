@@ -4,7 +4,8 @@
 // with fp32 sums, rounded once to the output's type.  Grouped: row m meets the
 // weights of the expert e with offsets[e] <= m < offsets[e + 1].
 //
-// The scales are any fp32 numbers, so the tensor cores (kind::f8f6f4) sum one
+// The scales are any fp32 numbers (for products of theirs that fp32 does not hold see
+// fm_power), so the tensor cores (kind::f8f6f4) sum one
 // block of 128 k at a time into a buffer of tensor memory of its own; eight warps
 // read it from there, multiply with the block's scales and add to sums that they
 // keep in registers, while the next block is multiplied into the next buffer.
@@ -42,6 +43,7 @@ constexpr uint32_t kFmBars = 1024;
 constexpr uint32_t kFmTable = 3328;  // experts' first token tile, first and last row
 
 struct FmParams {
+  const uint8_t *xc, *wc;
   const float *xs, *ws;
   const int32_t* offsets;
   void* y;
@@ -76,6 +78,8 @@ struct FmPlan {
   static constexpr int kStages0 = (int)((kFmSmem - 1024 - kAt) / kStage);
   static constexpr int kStages = kStages0 > 12 ? 12 : kStages0;
 };
+
+constexpr float kFmLargest = 3.40282347e38f;
 
 // The status word of the calls that bring none.
 __device__ uint32_t g_fp8_status;
@@ -135,6 +139,77 @@ __device__ __forceinline__ uint32_t fm_pack(const FmParams& p, f2 v) {
   }
   const __half2 h = __floats2half2_rn(v.x, v.y);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// A block's sum is multiplied with the product of its two scales.  Where that product
+// is no normal number of fp32 although neither scale is 0, infinite or NaN, it has
+// lost bits that the outcome has (2^-70 times 2^-70 with a sum of 2^20), or is
+// infinite where the sum is 0 or small.  A token's outputs with such a product are
+// worked out again at the end (fm_again).  What brings such a product back, or 1:
+__device__ __forceinline__ float fm_power(float x, float w) {
+  const float f = fabsf(x * w);
+  if ((f >= 0x1p-126f && f <= kFmLargest) || x == 0.f || w == 0.f || !isfinite(x) || !isfinite(w)) return 1.f;
+  return f < 1.f ? 0x1p64f : 0x1p-64f;
+}
+// The warps that prepare scales only keep the least and the largest of each kind, from
+// which they tell whether some product could be out of range.  So the usual call takes
+// 0 to 2 % longer than unasked, the smallest 5 (1 x 1408 x 2048: 3.36 -> 3.5 us); asked
+// product by product, with the sums brought back in tensor memory, 8192^3 took 6 to 11.
+struct FmRange {
+  uint32_t least_x = ~0u, most_x = 0, least_w = ~0u, most_w = 0;  // bits
+  __device__ __forceinline__ void token(float v) {
+    least_x = min(least_x, __float_as_uint(v));
+    most_x = max(most_x, __float_as_uint(v));
+  }
+  __device__ __forceinline__ void weight(float v) {
+    least_w = min(least_w, __float_as_uint(v));
+    most_w = max(most_w, __float_as_uint(v));
+  }
+  // exponents (biased by 127) of normal numbers below 2^-126 or above 2^127 together, or
+  // numbers that are subnormal, 0 or negative
+  __device__ __forceinline__ bool left() const {
+    return (least_x >> 23) + (least_w >> 23) < 2 * 127 - 126 || (most_x >> 23) + (most_w >> 23) > 2 * 127 + 126 ||
+           min(least_x, least_w) < 0x00800000u || max(most_x, most_w) >= 0x80000000u;
+  }
+};
+
+// Outputs n .. n1 - 1 (in one block of 128) of token m again, if it has a product out of
+// range.  The product is taken times a power of two that brings it back, rounded once;
+// the block's sum, which is 0 or 2^-18 to 2^25 in magnitude, takes the inverse exactly.
+// A warp calls it, a lane to an output, in plain fp32: 2048^3 with every token so 4.8 ms
+// instead of 13 us, one token of 2048 0.15.
+__device__ __forceinline__ void fm_again(const FmParams& p, int e, int n, int n1, int m) {
+  const int lane = threadIdx.x & 31, nb = (p.K + 127) / 128;
+  const float *xs = p.xs + (size_t)m * nb, *ws = p.ws + ((size_t)e * ((p.N + 127) / 128) + n / 128) * nb;
+  bool out = false;
+  for (int c = lane; c < nb; c += 32) out |= fm_power(xs[c], ws[c]) != 1.f;
+  if (!__any_sync(0xffffffffu, out)) return;
+  for (int i = n + lane; i < n1; i += 32) {
+    const uint8_t *x = p.xc + (size_t)m * p.K, *w = p.wc + ((size_t)e * p.N + i) * p.K;
+    float y = 0.f;
+    for (int c = 0; c < nb; ++c) {
+      float sum = 0.f;
+#pragma unroll 1
+      for (int k = c * 128; k < min(p.K, c * 128 + 128); k += 16) {
+        const uint4 q = *reinterpret_cast<const uint4*>(x + k), r = *reinterpret_cast<const uint4*>(w + k);
+        auto four = [&](uint32_t s, uint32_t t) {
+          float a[4], b[4];
+          mx_from_e4m3x4(s, a);
+          mx_from_e4m3x4(t, b);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sum = fmaf(a[j], b[j], sum);
+        };
+        four(q.x, r.x), four(q.y, r.y), four(q.z, r.z), four(q.w, r.w);
+      }
+      const float u = xs[c], v = ws[c], power = fm_power(u, v);
+      // (u times the power is exact: u is below 2^23 where the product is small, since v is
+      // at least 2^-149, and above 1 where it is large)
+      float s = u * power * v;
+      if (power < 1.f) s = fminf(fmaxf(s, -kFmLargest), kFmLargest);  // a sum of 0 stays 0
+      y = fmaf(sum * (1.f / power), s, y);
+    }
+    fm_store(p, (size_t)m * p.N + i, y);
+  }
 }
 
 // 32 lanes x 8 G columns of tensor memory as fragments: r[i][j] holds columns
@@ -261,7 +336,7 @@ __device__ __forceinline__ FmTile fm_tile(const FmParams& p, const FmTable& tab,
 template <int BN>
 __global__ void __launch_bounds__(kFmThreads, 1)
     fp8_matmul_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
-                      const FmParams p) {
+                      const __grid_constant__ FmParams p) {
   using P = FmPlan<BN>;
   constexpr int S = P::kStages, NB = P::kBufs, SQ = P::kQuads;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -277,6 +352,7 @@ __global__ void __launch_bounds__(kFmThreads, 1)
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(never + 1);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   int* s_sum = reinterpret_cast<int*>(s_tmem + 2);  // [8]
+  volatile int* s_left = s_sum + 8;  // a scale has left FmRange
   FmTable& tab = *reinterpret_cast<FmTable*>(smem + kFmBars);
   FmTile* list = reinterpret_cast<FmTile*>(smem + kFmBars + kFmTable);
   uint8_t* outbuf = smem + kFmBars + kFmTable + P::kList * sizeof(FmTile);
@@ -292,7 +368,7 @@ __global__ void __launch_bounds__(kFmThreads, 1)
       const int a = i - 2 * S, q = a - 2 * NB;
       mbar_init(&full[i], a >= NB && q < 0 ? 8 : q < 0 || q >= 2 * SQ ? 1 : q < SQ ? 2 : 8);
     }
-    if (lane == 0) *s_abort = 0;
+    if (lane == 0) *s_abort = 0, *s_left = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -327,6 +403,7 @@ __global__ void __launch_bounds__(kFmThreads, 1)
   __syncthreads();
   auto nth = [&](int i, int t) { return i < P::kList ? list[i] : fm_tile<BN>(p, tab, t); };
   f2 acc[P::kQ][P::kG][4];
+  bool left = false;  // the warps of the scales: FmRange
 
   if (warp == 0) {
     // ------------------------------------------------------------ codes
@@ -398,6 +475,7 @@ __global__ void __launch_bounds__(kFmThreads, 1)
     // ----------------------------------------- scales, four blocks at a time
     int it = 0;
     const int rb = (p.N + 127) / 128;
+    FmRange range;
     bool ok = !stalled(QMOE_DIAG_STALL_FP8_SCALES);
     for (int t = first, i = 0; t < tiles && ok; t += step, ++i) {
       const FmTile f = nth(i, t);
@@ -407,13 +485,13 @@ __global__ void __launch_bounds__(kFmThreads, 1)
         const int q = it % SQ;
         float w[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = rt < rb && c + j < c1 ? ws[c + j] : 0.f;
+        for (int j = 0; j < 4; ++j) w[j] = rt < rb && c + j < c1 ? ws[c + j] : 1.f;  // (1: nobody reads it)
         if (it >= SQ) ok = fm_wait(&sc_free[q], (it / SQ - 1) & 1, p, s_abort);
         if (!ok) break;
         float* out = scales + q * 4 * BN;
 #pragma unroll
         for (int i = (warp - 2) * 32 + lane; i < BN; i += 64) {
-          float v[4] = {};
+          float v[4] = {1.f, 1.f, 1.f, 1.f};
           if (f.m0 + i < f.m1) {
             const float* xs = p.xs + (size_t)(f.m0 + i) * nb + c;
             if (p.wide_scales) {
@@ -421,16 +499,22 @@ __global__ void __launch_bounds__(kFmThreads, 1)
               v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
             } else {
 #pragma unroll
-              for (int j = 0; j < 4; ++j) v[j] = c + j < c1 ? xs[j] : 0.f;
+              for (int j = 0; j < 4; ++j) v[j] = c + j < c1 ? xs[j] : 1.f;
             }
           }
 #pragma unroll
-          for (int j = 0; j < 4; ++j) out[j * BN + i] = v[j] * w[j];
+          for (int j = 0; j < 4; ++j) {
+            out[j * BN + i] = v[j] * w[j];
+            range.token(v[j]);
+          }
         }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) range.weight(w[j]);  // (not before the loads that follow w's)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sc_full[q]);
       }
     }
+    left = range.left();
   } else if (warp >= 4) {
     // ------------------------------------- the blocks' sums, scaled and added
     const int qd = warp & 3, set = (warp - 4) >> 2;
@@ -542,6 +626,9 @@ __global__ void __launch_bounds__(kFmThreads, 1)
           }
         }
     }
+    if (left)
+      for (int r = 0; r < p.split; ++r)
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer_u32(const_cast<int*>(s_left), r)), "r"(1) : "memory");
     __syncwarp();
     cluster_sync_all();
     const int mine = min(per, rows - rank * per);
@@ -556,12 +643,23 @@ __global__ void __launch_bounds__(kFmThreads, 1)
         if (j + 1 < rows) fm_store(p, o + p.N, v.y);
       }
     }
+  } else if (left) {
+    *s_left = 1;
   }
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
+  }
+  if (*s_left) {
+    const int per = max(2, BN / p.split);  // a CTA's tokens of a split tile
+    for (int t = first, i = 0; t < tiles; t += step, ++i) {
+      const FmTile f = nth(i, t);
+      const int a = f.m0 + rank * per, n0 = f.rt * 128, many = (p.split > 1 ? min(a + per, f.m1) : f.m1) - a;
+      for (int j = warp; j < 4 * many; j += kFmThreads / 32)
+        fm_again(p, f.e, n0 + (j & 3) * 32, min(p.N, n0 + (j & 3) * 32 + 32), a + j / 4);
+    }
   }
 }
 
@@ -619,7 +717,8 @@ struct alignas(16) FwTile : FmTile {
 
 template <int BN>
 __global__ void __launch_bounds__(kFwThreads, 1)
-    fp8_wide_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x, const FmParams p) {
+    fp8_wide_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
+                    const __grid_constant__ FmParams p) {
   using P = FwPlan<BN>;
   constexpr int BT = 128;  // tokens of a tile
   constexpr int S = P::kStages, NB = P::kBufs, SQ = P::kQuads;
@@ -636,6 +735,7 @@ __global__ void __launch_bounds__(kFwThreads, 1)
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(never + 1);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   int* s_sum = reinterpret_cast<int*>(s_tmem + 2);  // [8]
+  volatile int* s_left = s_sum + 8;  // a scale has left FmRange
   FmTable& tab = *reinterpret_cast<FmTable*>(smem + kFmBars);
   FwTile* list = reinterpret_cast<FwTile*>(smem + kFmBars + kFmTable);
   float* scales = reinterpret_cast<float*>(smem + kFmBars + kFmTable + P::kList * sizeof(FwTile));
@@ -649,7 +749,7 @@ __global__ void __launch_bounds__(kFwThreads, 1)
       const int a = i - 2 * S, q = a - 2 * NB;
       mbar_init(&full[i], (a >= NB && q < 0) || (q >= SQ && q < 2 * SQ) ? 8 : 1);
     }
-    if (lane == 0) *s_abort = 0;
+    if (lane == 0) *s_abort = 0, *s_left = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -813,6 +913,14 @@ __global__ void __launch_bounds__(kFwThreads, 1)
         }
       }
     }
+    __syncwarp();
+    if (ok && *s_left)
+      for (int t = blockIdx.x, i = 0; t < parts; t += gridDim.x, ++i) {
+        const FwTile f = nth(i, t);
+        const int n0 = f.n0 + set * (BN / 2), n1 = min(f.n1, n0 + BN / 2);
+        for (int m = f.m0 + qd * 32; m < min(f.m1, f.m0 + qd * 32 + 32); ++m)
+          if (n0 < n1) fm_again(p, f.e, n0, n1, m);
+      }
   } else {
     if (BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFwFewRegs));
     if (warp == 0) {
@@ -885,6 +993,7 @@ __global__ void __launch_bounds__(kFwThreads, 1)
       // ------------ scales of 128 tokens by kHalves weight blocks, four k blocks at a time
       int it = 0;
       const int rb = (p.N + 127) / 128;
+      FmRange range;
       bool ok = !stalled(QMOE_DIAG_STALL_FP8_SCALES);
       for (int t = blockIdx.x, i = 0; t < parts && ok; t += gridDim.x, ++i) {
         const FwTile f = nth(i, t);
@@ -892,13 +1001,15 @@ __global__ void __launch_bounds__(kFwThreads, 1)
         const float* ws = p.ws + ((size_t)f.e * rb + f.n0 / 128) * nb;
         for (int c = 0; c < nb; c += 4, ++it) {
           const int q = it % SQ;
-          float v[4][4] = {}, w[P::kHalves][4];
+          float v[4][4], w[P::kHalves][4];
 #pragma unroll
           for (int h = 0; h < P::kHalves; ++h)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) w[h][j] = f.n0 / 128 + h < rb && c + j < nb ? ws[h * nb + c + j] : 0.f;
+            for (int j = 0; j < 4; ++j) w[h][j] = f.n0 / 128 + h < rb && c + j < nb ? ws[h * nb + c + j] : 1.f;  // (1: nobody reads it)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[i][j] = 1.f;
             if (f.m0 + 32 * i + lane < f.m1) {
               const float* xs = p.xs + (size_t)(f.m0 + 32 * i + lane) * nb + c;
               if (p.wide_scales) {
@@ -906,9 +1017,10 @@ __global__ void __launch_bounds__(kFwThreads, 1)
                 v[i][0] = u.x, v[i][1] = u.y, v[i][2] = u.z, v[i][3] = u.w;
               } else {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v[i][j] = c + j < nb ? xs[j] : 0.f;
+                for (int j = 0; j < 4; ++j) v[i][j] = c + j < nb ? xs[j] : 1.f;
               }
             }
+          }
           if (it >= SQ) ok = fm_wait(&sc_free[q], (it / SQ - 1) & 1, p, s_abort);
           if (!ok) break;
           float* out = scales + q * 4 * P::kHalves * 128;
@@ -918,6 +1030,14 @@ __global__ void __launch_bounds__(kFwThreads, 1)
             for (int h = 0; h < P::kHalves; ++h)
 #pragma unroll
               for (int i = 0; i < 4; ++i) out[(j * P::kHalves + h) * 128 + 32 * i + lane] = v[i][j] * w[h][j];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+#pragma unroll
+            for (int h = 0; h < P::kHalves; ++h) range.weight(w[h][j]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) range.token(v[i][j]);
+          }
+          if (range.left()) *s_left = 1;
           __syncwarp();
           if (lane == 0) mbar_arrive(&sc_full[q]);
         }
@@ -944,7 +1064,7 @@ template <int BN>
 static cudaError_t launch_fm(FmParams p, int split, const uint8_t* xc, const uint8_t* wc, cudaStream_t st) {
   using P = FmPlan<BN>;
   static_assert(P::kStages >= 3 && P::kBufs * BN <= 512, "plan");
-  static_assert((2 * P::kStages + 2 * P::kBufs + 2 * P::kQuads + 2) * 8 + 40 <= kFmBars, "barriers");
+  static_assert((2 * P::kStages + 2 * P::kBufs + 2 * P::kQuads + 2) * 8 + 44 <= kFmBars, "barriers");
   p.split = split;
   p.lsplit = split == 8 ? 3 : split / 2;
   p.row_tiles = (p.N + 127) / 128;
@@ -985,7 +1105,7 @@ template <int BN>
 static cudaError_t launch_fw(FmParams p, const uint8_t* xc, const uint8_t* wc, cudaStream_t st) {
   using P = FwPlan<BN>;
   static_assert(P::kStages >= 3, "plan");
-  static_assert((2 * P::kStages + 2 * P::kBufs + 2 * P::kQuads + 2) * 8 + 40 <= kFmBars, "barriers");
+  static_assert((2 * P::kStages + 2 * P::kBufs + 2 * P::kQuads + 2) * 8 + 44 <= kFmBars, "barriers");
   p.split = 1;
   p.row_tiles = (p.N + BN - 1) / BN;
   const long long tiles = fm_token_tiles(p, 128) * p.row_tiles;
@@ -1132,6 +1252,8 @@ cudaError_t launch_fp8_matmul(const uint8_t* xc, const float* xs, const uint8_t*
                               const int32_t* offsets, int E, int M, int N, int K, void* y, int y_dtype, uint32_t* status,
                               uint32_t wait_limit_kilocycles, uint32_t stall, cudaStream_t st) {
   FmParams p = fm_params(xs, ws, offsets, E, M, N, K);
+  p.xc = xc;
+  p.wc = wc;
   p.y = y;
   p.y_dtype = y_dtype;
   p.status = status;
