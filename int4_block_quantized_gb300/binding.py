@@ -828,10 +828,22 @@ def qmoe_fp8_status():
     return rc, bits.value
 
 
-def qmoe_sort_experts(ids, E):
+def _fp8_wanted(t, shape, dtype, like, dev, where, name):
+    """(output, its address): the caller's tensor, a new one for None, nothing for False."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+    elif t is False:
+        return None, None
+    elif t.get_device() != dev or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _mx_check2(t, dev, dtype, shape, where, name)
+    return t, t.data_ptr()
+
+
+def qmoe_sort_experts(ids, E, offsets=None, perm=None, pos=None):
     """(offsets [E + 1], perm [T * k], pos [T, k]), int32, of ids int32 [T, k]: the
     assignments by expert, stably; an id outside 0 .. E - 1 goes nowhere (pos -1,
-    and perm -1 behind the last)."""
+    and perm -1 behind the last).  An output that is given is written to; False: it
+    is not wanted, and None stands in its place."""
     where = "qmoe_sort_experts"
     T, k = _mx_size(ids, where)
     dev = ids.get_device()
@@ -841,12 +853,10 @@ def qmoe_sort_experts(ids, E):
         _bad(where, "ids %s, %d experts" % ((T, k), E))
     if dev < 0 or ids.dtype is not _I32 or not ids.is_contiguous():
         _mx_check2(ids, dev, _I32, (T, k), where, "ids")
-    at = ids.device
-    offsets = torch.empty(E + 1, dtype=_I32, device=at)
-    perm = torch.empty(T * k, dtype=_I32, device=at)
-    pos = torch.empty((T, k), dtype=_I32, device=at)
-    _mx_call(dev, lib().qmoe_sort_experts, where, ids.data_ptr(), T, k, E, offsets.data_ptr(), perm.data_ptr(),
-             pos.data_ptr())
+    offsets, po = _fp8_wanted(offsets, (E + 1,), _I32, ids, dev, where, "offsets")
+    perm, pm = _fp8_wanted(perm, (T * k,), _I32, ids, dev, where, "perm")
+    pos, pp = _fp8_wanted(pos, (T, k), _I32, ids, dev, where, "pos")
+    _mx_call(dev, lib().qmoe_sort_experts, where, ids.data_ptr(), T, k, E, po, pm, pp)
     return offsets, perm, pos
 
 
@@ -925,28 +935,34 @@ def qmoe_dispatch_backward(dxs, pos, out=None):
 
 
 def qmoe_combine_backward(dout, ys, pos, w=None, dys=None, dw=None):
-    """(dys [T * k, H], dw [T, k] fp32) of qmoe_combine for dout [T, H]."""
+    """(dys [T * k, H], dw [T, k] fp32) of qmoe_combine for dout [T, H].  A gradient
+    that is given is written to; False: it is not wanted, and None stands in its
+    place.  ys may be None where dw is not wanted (dys is then of dout's type, or as
+    given).  Rows of a new dys that no place names are not initialised."""
     where = "qmoe_combine_backward"
     T, H = _mx_size(dout, where)
     dev = dout.get_device()
-    dt, yt = _fp8_in(dout, dev, where, "dout"), _fp8_in(ys, dev, where, "ys")
+    dt = _fp8_in(dout, dev, where, "dout")
     _fp8_rows(T, H, where)
     k = _places(pos, T, dev, where)
-    if ys.shape != (T * k, H):
-        _mx_check2(ys, dev, ys.dtype, (T * k, H), where, "ys")
+    if dw is False and dys is False:
+        _bad(where, "neither gradient is wanted")
+    if ys is not None:
+        yt = _fp8_in(ys, dev, where, "ys")
+        if ys.shape != (T * k, H):
+            _mx_check2(ys, dev, ys.dtype, (T * k, H), where, "ys")
+        dtype, yp = ys.dtype, ys.data_ptr()
+    elif dw is not False:
+        _bad(where, "ys: wanted for dw")
+    else:
+        dtype, yp = (dout if dys is None else dys).dtype, None
+        yt = dt if dys is None else _fp8_in(dys, dev, where, "dys")
     wp = None
     if w is not None:
         if w.get_device() != dev or w.dtype is not _F32 or w.shape != (T, k) or not w.is_contiguous():
             _mx_check2(w, dev, _F32, (T, k), where, "w")
         wp = w.data_ptr()
-    if dys is None:
-        dys = torch.empty_like(ys)
-    elif dys.get_device() != dev or dys.dtype is not ys.dtype or dys.shape != (T * k, H) or not dys.is_contiguous():
-        _mx_check2(dys, dev, ys.dtype, (T * k, H), where, "dys")
-    if dw is None:
-        dw = torch.empty((T, k), dtype=_F32, device=dout.device)
-    else:
-        _mx_check2(dw, dev, _F32, (T, k), where, "dw")
-    _mx_call(dev, lib().qmoe_combine_backward, where, dout.data_ptr(), dt, ys.data_ptr(), yt, pos.data_ptr(), wp, T, H, k,
-             dys.data_ptr(), dw.data_ptr())
+    dys, dp = _fp8_wanted(dys, (T * k, H), dtype, dout, dev, where, "dys")
+    dw, dwp = _fp8_wanted(dw, (T, k), _F32, dout, dev, where, "dw")
+    _mx_call(dev, lib().qmoe_combine_backward, where, dout.data_ptr(), dt, yp, yt, pos.data_ptr(), wp, T, H, k, dp, dwp)
     return dys, dw
