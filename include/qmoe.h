@@ -542,7 +542,7 @@ int qmoe_fp8_quantize(const void* x, int x_dtype, int T, int K, const int32_t* p
  * first I columns; fp16, bf16 or fp32; 16-byte aligned), computed in fp32 (within
  * 9 2^-24 of itself, whatever the gate) and quantised to codes [M, I] without a
  * rounding in between.  I a multiple of 16.
- * Bound by HBM. */
+ * Bound by its instructions at many rows. */
 int qmoe_fp8_quantize_swiglu(const void* h, int h_dtype, int M, int I, uint8_t* codes, float* scales, void* stream);
 
 /* Weights w [E, N, K] (fp16, bf16 or fp32; 16-byte aligned) to FP8, a scale for
