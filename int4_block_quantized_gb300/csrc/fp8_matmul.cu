@@ -14,11 +14,11 @@
 //                few tokens cost a narrow MMA; K is split over the CTAs of a
 //                cluster where there are few tiles.  Bound by the weights' bytes:
 //                256 rows of 60 experts x 2816 x 2048 run at 6.8 TB/s; one token's
-//                four experts take 6.6 us for 3.4 us of bytes: their 88 tiles leave 64
-//                of 152 SMs without one (K is not split there: its CTAs would
-//                outnumber the SMs), and launch, first copies and last block add
-//                to it.  16 x 8192 x 8192 runs on 128 SMs, 333 x 4099 x 1424,
-//                in the other form, on 99.
+//                four experts take 8.8 us for 3.4 us of bytes (6.6 where these lie
+//                in L2): their 88 tiles leave 64 of 152 SMs without one (K over two
+//                CTAs each would be more than the SMs), and launch, first copies
+//                and last block add to it.  16 x 8192 x 8192 runs on 128 SMs, 333 x
+//                4099 x 1424, in the other form, on 99.
 //   many tokens  128 tokens by 128 or 256 weight rows.  A block of 128 x 256 takes
 //                860 cycles: a copy takes about 1700 to arrive and four stages of
 //                48 KB fit, so that one is there every 780; reading, scaling and
@@ -1182,14 +1182,15 @@ struct FmChoice {
 // the rows, each is taken to have as many, and a last tile half full.
 // The constants are fits to 410 measured sizes, dense and grouped, of which 15 are
 // then more than 5 % off the best form, the worst 29 % (71 tokens x 8, 8 experts).
-// Some of them on GB300 (us; tokens x outputs a tile / CTAs along K):
-//      1 x 1408 x 2048      16x128/8 3.5  /4 3.6  /2 4.2  /1 5.2
+// Some of them on GB300 (us, the forms of a row side by side, before FmRange's 0 to 0.2;
+// tokens x outputs a tile / CTAs along K):
+//      1 x 1408 x 2048      16x128/8 3.4  /4 3.6  /2 4.2  /1 5.2
 //     16 x 8192 x 8192      64x128/2 14.2  16x128/2 14.6  /1 16.6
 //     64 x 2048 x 5632      32x128/4 6.9  64x128/4 7.5  /1 12.7
-//    512 x 1408 x 2048      64x128 7.1  128x128 8.1  128x256 11.2
-//   2048 x 1408 x 2048      128x256 11.8  128x128 13.9  64x128 15.5
+//    512 x 1408 x 2048      64x128 7.0  128x128 8.1  128x256 11.2
+//   2048 x 1408 x 2048      128x256 11.6  128x128 13.9  64x128 15.5
 //   8192 x 8192 x 8192      128x256 400 to 415  128x128 490  64x128 810
-//    4 rows of 4 experts    x 2816 x 2048: 16x128/1 6.6  /2 11
+//    4 rows of 4 experts    x 2816 x 2048: 16x128/1 6.5  /2 11
 //   8192 rows of 60 experts x 2816 x 2048: 128x256 77  128x128 83  64x128 100
 static cudaError_t fm_choose(const FmParams& p, FmChoice* choice) {
   static const struct {
