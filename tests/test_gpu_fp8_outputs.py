@@ -59,3 +59,16 @@ def test_combine_backward_without_one_gradient(T, k, E, H, ydt, odt):
         there = torch.zeros(T * k, dtype=torch.bool, device=DEV)
         there[pos[pos >= 0].long()] = True
         assert torch.equal(only[there], dys[there]) and torch.equal(only[~there], ys[~there])
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("T,k,E,H", [(1, 4, 60, 2048), (3, 1, 2, 8), (70, 8, 60, 1000)])
+def test_dispatch_backward_of_the_library(T, k, E, H, dtype):
+    """The C entry, which the binding reaches through the combine, gives the same."""
+    g = torch.Generator(device=DEV).manual_seed(T)
+    pos = B.qmoe_sort_experts(ids_of(T, k, E), E)[2]
+    dxs = torch.randn((T * k, H), generator=g, device=DEV).to(dtype)
+    buf = torch.full((3, T, H), 7.0, dtype=dtype, device=DEV)
+    rc = B.lib().qmoe_dispatch_backward(dxs.data_ptr(), B._MX_DT[dtype], pos.data_ptr(), T, H, k, buf[1].data_ptr(),
+                                        torch.cuda.current_stream().cuda_stream)
+    assert rc == 0 and torch.equal(buf[1], B.qmoe_dispatch_backward(dxs, pos)) and (buf[::2] == 7).all()
